@@ -1,4 +1,4 @@
-"""Compile the CUDA library (csrc/*.cu) for sm_103a into libbsmoe.so, in tree.
+"""Compile the CUDA library (csrc/*.cu, csrc/block/*.cu) for sm_103a into libbsmoe.so, in tree.
 
 Each translation unit is compiled in parallel with nvcc; the objects are
 linked into one shared library next to this file. Rebuilds only what changed
@@ -29,7 +29,13 @@ def _nvcc():
 
 
 def _headers():
-    return glob.glob(os.path.join(SRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return [h for d in (SRC, os.path.join(SRC, "block"), INCLUDE) for e in ("*.cuh", "*.h")
+            for h in glob.glob(os.path.join(d, e))]
+
+
+def _sources():
+    """Every translation unit; file names are unique over the folders."""
+    return sorted(glob.glob(os.path.join(SRC, "*.cu")) + glob.glob(os.path.join(SRC, "block", "*.cu")))
 
 
 def _stale(obj, src, newest_header):
@@ -40,7 +46,7 @@ def build(verbose=False, ptxas_verbose=False):
     """Build libbsmoe.so; returns its path. Raises RuntimeError on failure."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
-    sources = sorted(glob.glob(os.path.join(SRC, "*.cu")))
+    sources = _sources()
     newest_header = max([os.path.getmtime(h) for h in _headers()] + [0])
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     jobs = []

@@ -14,6 +14,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "device_check.h"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
 #include "route_quant.cuh"
@@ -66,9 +67,32 @@ bool make_tmap(CUtensorMap* m, bool fp4, const void* base, uint64_t k_elems, uin
   return r == CUDA_SUCCESS;
 }
 
-struct DevInfo {
-  int id = -1, sms = 0, major = 0, minor = 0;
-};
+// Self-test of the bounded-wait paths: thread 0 waits, through the helper
+// the GEMM pipeline uses, on an mbarrier phase that nothing completes; thread
+// 32 waits, through the helper the single-launch forward's GEMM2 units use,
+// for a counter (the status word's neighbour, zeroed here) that nothing
+// increments. Each wait gives up after its bound, raises the abort flag, and
+// the kernel reports MOE_DEV_TIMEOUT the way the GEMMs do, then returns.
+__global__ void wait_timeout_selftest_kernel(uint32_t* status) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int abort_bar, abort_cnt;
+  if (threadIdx.x == 0) {
+    abort_bar = 0;
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+    const bool done = mbar_wait(&bar, 0, &abort_bar);
+    if (!done && abort_bar) atomicOr(status, MOE_DEV_TIMEOUT);
+  } else if (threadIdx.x == 32) {
+    abort_cnt = 0;
+    int32_t* counter = reinterpret_cast<int32_t*>(status + 1);
+    *counter = 0;
+    __threadfence();
+    const bool done = wait_counter(counter, 1, &abort_cnt);
+    if (!done && abort_cnt) atomicOr(status, MOE_DEV_TIMEOUT);
+  }
+}
+
+}  // namespace
 
 moe_status current_device(DevInfo* d) {
   if (cudaGetDevice(&d->id) != cudaSuccess) return MOE_ERR_CUDA;
@@ -99,33 +123,6 @@ moe_status check_ptr(const void* p, int dev) {
   if (a.device != dev) return MOE_ERR_DEVICE_MISMATCH;
   return MOE_OK;
 }
-
-// Self-test of the bounded-wait paths: thread 0 waits, through the helper
-// the GEMM pipeline uses, on an mbarrier phase that nothing completes; thread
-// 32 waits, through the helper the single-launch forward's GEMM2 units use,
-// for a counter (the status word's neighbour, zeroed here) that nothing
-// increments. Each wait gives up after its bound, raises the abort flag, and
-// the kernel reports MOE_DEV_TIMEOUT the way the GEMMs do, then returns.
-__global__ void wait_timeout_selftest_kernel(uint32_t* status) {
-  __shared__ __align__(8) uint64_t bar;
-  __shared__ int abort_bar, abort_cnt;
-  if (threadIdx.x == 0) {
-    abort_bar = 0;
-    mbar_init(&bar, 1);
-    fence_mbar_init();
-    const bool done = mbar_wait(&bar, 0, &abort_bar);
-    if (!done && abort_bar) atomicOr(status, MOE_DEV_TIMEOUT);
-  } else if (threadIdx.x == 32) {
-    abort_cnt = 0;
-    int32_t* counter = reinterpret_cast<int32_t*>(status + 1);
-    *counter = 0;
-    __threadfence();
-    const bool done = wait_counter(counter, 1, &abort_cnt);
-    if (!done && abort_cnt) atomicOr(status, MOE_DEV_TIMEOUT);
-  }
-}
-
-}  // namespace
 
 bool ws_layout(int fmt, int T, int H, int I, int E, int K, WsLayout* out) {
   if (!shape_ok(fmt, H, I, E) || T < 0 || K < 1 || K > kMaxTopK) return false;
