@@ -13,6 +13,7 @@ their gradients as plain calls. Rows may be strided (the elements of a row
 contiguous); anything else is made contiguous first.
 """
 import ctypes
+import functools
 import math
 
 import torch
@@ -73,13 +74,23 @@ def lib():
     return L
 
 
-def _stream():
-    return torch.cuda.current_stream().cuda_stream
+# The calls below are short at decode, so the checks are written to cost little
+# where they pass: one comparison for each property, the message built only on
+# a refusal.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check(status, what):
     if status != 0:
         raise _b.MoeError(status, what)
+
+
+def _device(t):
+    """The current device's index, which t must live on."""
+    dev = torch.cuda.current_device() if t.is_cuda else -1
+    if t.get_device() != dev:
+        _b._same_device(t)
+    return dev
 
 
 def _dtype(t, what):
@@ -89,29 +100,50 @@ def _dtype(t, what):
     return code
 
 
-def _rows(t, like, shape, what):
-    """A [n, H] operand of `like`'s type with contiguous rows."""
-    if t.dtype != like.dtype:
-        raise ValueError(f"{what} must be {like.dtype} like the rows it goes with, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _row_strided(t)
-
-
-def _row_strided(t):
-    return t if (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= 0 else t.contiguous()
-
-
 def _2d(t, what):
     if t.dim() != 2:
         raise ValueError(f"{what} must be [tokens, width], got {tuple(t.shape)}")
 
 
+def _rows(t, dtype, shape, dev, what):
+    """(tensor, row stride) of an operand [n, H] of the given type with
+    contiguous rows."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype} like the rows it goes with, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        _b._same_device(t)
+    ld, step = t.stride()
+    if step != 1 and shape[1] != 1:
+        t = t.contiguous()
+        ld = t.stride(0)
+    return t, ld
+
+
+def _first(t, what):
+    """(tensor, row stride, dtype code, device, shape): the operand that the
+    others have to match."""
+    if t.dim() != 2:
+        _2d(t, what)
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        _dtype(t, what)
+    dev = _device(t)
+    shape = t.shape
+    ld, step = t.stride()
+    if step != 1 and shape[1] != 1:
+        t = t.contiguous()
+        ld = t.stride(0)
+    return t, ld, code, dev, shape
+
+
 def _out(out, shape, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if out.dtype != dtype or tuple(out.shape) != tuple(shape) or not out.is_contiguous():
+    if out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    _b._same_device(out)
     return out
 
 
@@ -127,20 +159,43 @@ class SortPlan:
     row (-1 if skipped), row_slot [row_capacity] each row's slot (-1 if none).
     `buffer` starts with the status word that `device_status` reads."""
 
+    __slots__ = ("buffer", "T", "num_experts", "K", "row_align", "row_capacity", "_layout", "_args", "_parts")
+
     def __init__(self, buffer, layout, T, E, K, row_align):
-        self.buffer, self.nbytes = buffer, layout.total_bytes
+        self.buffer, self._layout, self._parts = buffer, layout, None
         self.T, self.num_experts, self.K, self.row_align = T, E, K, row_align
         self.row_capacity = layout.row_capacity
-        i, M = buffer, layout.row_capacity
-        self.counts = i.as_strided((E,), (1,), layout.counts // 4)
-        self.offsets = i.as_strided((E + 1,), (1,), layout.offsets // 4)
-        self.inv = i.as_strided((T, K), (K, 1), layout.inv // 4)
-        self.row_slot = i.as_strided((M,), (1,), layout.row_slot // 4)
+        self._args = buffer.data_ptr(), layout.total_bytes, T
+
+    def _views(self):
+        if self._parts is None:
+            self._parts = self.buffer.split_with_sizes(self._layout.split)
+        return self._parts
+
+    @property
+    def counts(self):
+        return self._views()[1][:self.num_experts]
+
+    @property
+    def offsets(self):
+        return self._views()[2][:self.num_experts + 1]
+
+    @property
+    def inv(self):
+        return self.buffer.as_strided((self.T, self.K), (self.K, 1), self._layout.inv // 4)
+
+    @property
+    def row_slot(self):
+        return self._views()[4][:self.row_capacity]
 
 
+@functools.lru_cache(maxsize=256)
 def sort_layout(T, num_experts, K, row_align=1):
+    """The plan's layout for these sizes (moe_query_sort_layout)."""
     out = MoeSortLayout()
     _check(lib().moe_query_sort_layout(T, num_experts, K, row_align, _c.byref(out)), "moe_query_sort_layout")
+    ends = [out.counts, out.offsets, out.inv, out.row_slot, out.total_bytes]
+    out.split = [(e - b) // 4 for b, e in zip([0] + ends, ends)]
     return out
 
 
@@ -149,108 +204,90 @@ def sort_tokens(topk_idx, num_experts, row_align=1):
     group starting at a multiple of row_align. Returns a SortPlan. An id outside
     [-1, num_experts) counts as skipped and sets MOE_DEV_BAD_EXPERT_ID, which
     device_status(plan.buffer) reads."""
-    if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2:
+    if topk_idx.dtype is not torch.int32 or topk_idx.dim() != 2:
         raise ValueError("topk_idx must be an int32 tensor [T, K]")
-    topk_idx = topk_idx.contiguous()
-    _b._same_device(topk_idx)
+    dev = _device(topk_idx)
+    if not topk_idx.is_contiguous():
+        topk_idx = topk_idx.contiguous()
     T, K = topk_idx.shape
     layout = sort_layout(T, num_experts, K, row_align)
-    buffer = torch.empty(layout.total_bytes // 4, dtype=torch.int32, device=topk_idx.device)
-    _check(lib().moe_sort_tokens(topk_idx.data_ptr(), T, num_experts, K, row_align, buffer.data_ptr(),
-                                 layout.total_bytes, _stream()), "moe_sort_tokens")
-    return SortPlan(buffer, layout, T, num_experts, K, row_align)
+    nbytes = layout.total_bytes
+    buffer = torch.empty(nbytes // 4, dtype=torch.int32, device=topk_idx.device)
+    plan = SortPlan(buffer, layout, T, num_experts, K, row_align)
+    _check(lib().moe_sort_tokens(topk_idx.data_ptr(), T, num_experts, K, row_align, plan._args[0], nbytes,
+                                 _raw_stream(dev)), "moe_sort_tokens")
+    return plan
 
 
-def _plan_args(plan, H):
-    return plan.buffer.data_ptr(), plan.nbytes, plan.T, H, plan.num_experts, plan.K, plan.row_align
-
-
-def _weights_arg(topk_w, plan):
+def _weights_arg(topk_w, plan, dev):
     if topk_w is None:
         return None
-    if topk_w.dtype != torch.float32 or tuple(topk_w.shape) != (plan.T, plan.K):
+    if topk_w.dtype is not torch.float32 or topk_w.shape != (plan.T, plan.K):
         raise ValueError(f"topk_w must be a float32 tensor [{plan.T}, {plan.K}]")
-    return topk_w.contiguous()
+    if topk_w.get_device() != dev:
+        _b._same_device(topk_w)
+    return topk_w if topk_w.is_contiguous() else topk_w.contiguous()
 
 
-def _tokens(t, plan, what):
-    _2d(t, what)
-    if t.shape[0] != plan.T:
-        raise ValueError(f"{what} has {t.shape[0]} tokens, the plan {plan.T}")
-    return _row_strided(t)
-
-
-def _plan_rows(t, plan, what):
-    _2d(t, what)
-    if t.shape[0] != plan.row_capacity:
-        raise ValueError(f"{what} has {t.shape[0]} rows, the plan {plan.row_capacity}")
-    return _row_strided(t)
+def _plan_operand(t, plan, n, what):
+    """_first of [n, H] rows that go with the plan."""
+    first = _first(t, what)
+    if first[4][0] != n:
+        raise ValueError(f"{what} has {first[4][0]} rows, the plan {n}")
+    if plan.buffer.get_device() != first[3]:
+        _b._same_device(plan.buffer)
+    return first
 
 
 def _permute(hidden, plan, topk_w, out=None):
-    hidden, topk_w = _tokens(hidden, plan, "hidden"), _weights_arg(topk_w, plan)
-    code, H = _dtype(hidden, "hidden"), hidden.shape[1]
+    hidden, ld, code, dev, (_, H) = _plan_operand(hidden, plan, plan.T, "hidden")
+    topk_w = _weights_arg(topk_w, plan, dev)
     out = _out(out, (plan.row_capacity, H), hidden.dtype, hidden.device)
-    _b._same_device(hidden, plan.buffer, out, *([] if topk_w is None else [topk_w]))
-    _check(lib().moe_permute_tokens(code, hidden.data_ptr(), hidden.stride(0), _p(topk_w), *_plan_args(plan, H),
-                                    out.data_ptr(), _stream()), "moe_permute_tokens")
+    _check(lib().moe_permute_tokens(code, hidden.data_ptr(), ld, _p(topk_w), *plan._args, H, plan.num_experts, plan.K,
+                                    plan.row_align, out.data_ptr(), _raw_stream(dev)), "moe_permute_tokens")
     return out
 
 
 def _unpermute(rows, plan, topk_w, out=None):
-    rows, topk_w = _plan_rows(rows, plan, "rows"), _weights_arg(topk_w, plan)
-    code, H = _dtype(rows, "rows"), rows.shape[1]
+    rows, ld, code, dev, (_, H) = _plan_operand(rows, plan, plan.row_capacity, "rows")
+    topk_w = _weights_arg(topk_w, plan, dev)
     out = _out(out, (plan.T, H), rows.dtype, rows.device)
-    _b._same_device(rows, plan.buffer, out, *([] if topk_w is None else [topk_w]))
-    _check(lib().moe_unpermute_tokens(code, rows.data_ptr(), rows.stride(0), _p(topk_w), *_plan_args(plan, H),
-                                      out.data_ptr(), _stream()), "moe_unpermute_tokens")
+    _check(lib().moe_unpermute_tokens(code, rows.data_ptr(), ld, _p(topk_w), *plan._args, H, plan.num_experts, plan.K,
+                                      plan.row_align, out.data_ptr(), _raw_stream(dev)), "moe_unpermute_tokens")
     return out
+
+
+def _rows_backward(fn, grad, n_grad, other, n_other, plan, topk_w, out_rows, names):
+    """The two gradients differ in which side is rows and which tokens."""
+    grad, ld, code, dev, (_, H) = _plan_operand(grad, plan, n_grad, names[0])
+    topk_w = _weights_arg(topk_w, plan, dev)
+    d_in = torch.empty((out_rows, H), dtype=grad.dtype, device=grad.device)
+    d_w, ld_other = None, 0
+    if topk_w is None:
+        other = None
+    elif other is None:
+        raise ValueError(f"the gradient of topk_w needs {names[1]}")
+    else:
+        other, ld_other = _rows(other, grad.dtype, (n_other, H), dev, names[1])
+        d_w = torch.empty_like(topk_w)
+    _check(getattr(lib(), fn)(code, grad.data_ptr(), ld, _p(other), ld_other, _p(topk_w), *plan._args, H,
+                              plan.num_experts, plan.K, plan.row_align, d_in.data_ptr(), _p(d_w), _raw_stream(dev)),
+           fn)
+    return d_in, d_w
 
 
 def permute_tokens_backward(d_rows, plan, hidden=None, topk_w=None):
     """Gradient of permute_tokens: (d_hidden, d_topk_w). hidden is needed with
     topk_w only; without it d_topk_w is None."""
-    d_rows, topk_w = _plan_rows(d_rows, plan, "d_rows"), _weights_arg(topk_w, plan)
-    code, H = _dtype(d_rows, "d_rows"), d_rows.shape[1]
-    d_hidden = torch.empty(plan.T, H, dtype=d_rows.dtype, device=d_rows.device)
-    d_w, ld = None, 0
-    tensors = [d_rows, plan.buffer]
-    if topk_w is not None:
-        if hidden is None:
-            raise ValueError("the gradient of topk_w needs hidden")
-        hidden = _rows(hidden, d_rows, (plan.T, H), "hidden")
-        d_w, ld = torch.empty_like(topk_w), hidden.stride(0)
-        tensors += [hidden, topk_w]
-    else:
-        hidden = None
-    _b._same_device(*tensors)
-    _check(lib().moe_permute_tokens_backward(code, d_rows.data_ptr(), d_rows.stride(0), _p(hidden), ld, _p(topk_w),
-                                             *_plan_args(plan, H), d_hidden.data_ptr(), _p(d_w), _stream()),
-           "moe_permute_tokens_backward")
-    return d_hidden, d_w
+    return _rows_backward("moe_permute_tokens_backward", d_rows, plan.row_capacity, hidden, plan.T, plan, topk_w,
+                          plan.T, ("d_rows", "hidden"))
 
 
 def unpermute_tokens_backward(d_out, plan, rows=None, topk_w=None):
     """Gradient of unpermute_tokens: (d_rows, d_topk_w). rows is needed with
     topk_w only; without it d_topk_w is None. Rows of no slot get zeros."""
-    d_out, topk_w = _tokens(d_out, plan, "d_out"), _weights_arg(topk_w, plan)
-    code, H = _dtype(d_out, "d_out"), d_out.shape[1]
-    d_rows = torch.empty(plan.row_capacity, H, dtype=d_out.dtype, device=d_out.device)
-    d_w, ld = None, 0
-    tensors = [d_out, plan.buffer]
-    if topk_w is not None:
-        if rows is None:
-            raise ValueError("the gradient of topk_w needs rows")
-        rows = _rows(rows, d_out, (plan.row_capacity, H), "rows")
-        d_w, ld = torch.empty_like(topk_w), rows.stride(0)
-        tensors += [rows, topk_w]
-    else:
-        rows = None
-    _b._same_device(*tensors)
-    _check(lib().moe_unpermute_tokens_backward(code, d_out.data_ptr(), d_out.stride(0), _p(rows), ld, _p(topk_w),
-                                               *_plan_args(plan, H), d_rows.data_ptr(), _p(d_w), _stream()),
-           "moe_unpermute_tokens_backward")
-    return d_rows, d_w
+    return _rows_backward("moe_unpermute_tokens_backward", d_out, plan.T, rows, plan.row_capacity, plan, topk_w,
+                          plan.row_capacity, ("d_out", "rows"))
 
 
 class _Permute(torch.autograd.Function):
@@ -280,7 +317,10 @@ class _Unpermute(torch.autograd.Function):
 
 
 def _tracked(*ts):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+    for t in ts:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
 
 
 def _no_out(out):
@@ -309,60 +349,59 @@ def unpermute_tokens(rows, plan, topk_w=None, out=None):
 
 # --------------------------------------------------------- norms around a block
 
-def _norm_weight(w, x, what):
-    if w is None:
-        return None
-    if w.dim() != 1 or w.shape[0] != x.shape[1]:
-        raise ValueError(f"{what} must have the shape ({x.shape[1]},), got {tuple(w.shape)}")
-    if w.dtype != x.dtype and w.dtype != torch.float32:
-        raise ValueError(f"{what} must be {x.dtype} or float32, got {w.dtype}")
-    return w.contiguous()
+def _norm_weight(w, H, dtype, dev, what):
+    if w.dim() != 1 or w.shape[0] != H:
+        raise ValueError(f"{what} must have the shape ({H},), got {tuple(w.shape)}")
+    if w.dtype is not dtype and w.dtype is not torch.float32:
+        raise ValueError(f"{what} must be {dtype} or float32, got {w.dtype}")
+    if w.get_device() != dev:
+        _b._same_device(w)
+    return w if w.is_contiguous() else w.contiguous()
 
 
-def _norm_weights(x, weight, next_weight):
+def _norm_weights(weight, next_weight, H, dtype, dev):
     """(weight, next_weight, are they fp32)."""
-    weight, next_weight = _norm_weight(weight, x, "weight"), _norm_weight(next_weight, x, "next_weight")
-    if weight is not None and next_weight is not None and weight.dtype != next_weight.dtype:
-        raise ValueError("weight and next_weight must have one type")
-    w = weight if weight is not None else next_weight
-    return weight, next_weight, int(w is not None and w.dtype == torch.float32)
+    f32 = 0
+    if weight is not None:
+        weight = _norm_weight(weight, H, dtype, dev, "weight")
+        f32 = int(weight.dtype is torch.float32)
+    if next_weight is not None:
+        next_weight = _norm_weight(next_weight, H, dtype, dev, "next_weight")
+        if weight is not None and next_weight.dtype is not weight.dtype:
+            raise ValueError("weight and next_weight must have one type")
+        f32 = int(next_weight.dtype is torch.float32)
+    return weight, next_weight, f32
 
 
-def _gate(gate, gate_act, x):
+def _gate(gate, gate_act, shape, dtype, dev):
     """(gate, kind, act, row stride)."""
     act = GATE_ACT.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACT)}, got {gate_act!r}")
     if gate is None:
         return None, 0, act, 0
-    T, H = x.shape
-    if gate.dtype != x.dtype:
-        raise ValueError(f"gate must be {x.dtype} like x, got {gate.dtype}")
+    T, H = shape
+    if gate.dtype is not dtype:
+        raise ValueError(f"gate must be {dtype} like x, got {gate.dtype}")
+    if gate.get_device() != dev:
+        _b._same_device(gate)
     if gate.dim() == 1 and gate.shape[0] == H:
         return gate.contiguous(), 1, act, 0
-    if gate.dim() == 2 and tuple(gate.shape) == (T, H) and H > 1:
-        gate = _row_strided(gate)
-        return gate, 3, act, gate.stride(0)
-    if gate.dim() == 2 and tuple(gate.shape) == (T, 1):
-        gate = gate if gate.stride(0) >= 0 else gate.contiguous()
+    if gate.dim() == 2 and gate.shape == shape and H > 1:
+        gate, ld = _rows(gate, dtype, shape, dev, "gate")
+        return gate, 3, act, ld
+    if gate.dim() == 2 and gate.shape == (T, 1):
         return gate, 2, act, gate.stride(0)
-    raise ValueError(f"gate must be [H], [T, 1] or [T, H] for x of {tuple(x.shape)}, got {tuple(gate.shape)}")
-
-
-def _present(*ts):
-    return [t for t in ts if t is not None]
+    raise ValueError(f"gate must be [H], [T, 1] or [T, H] for x of {tuple(shape)}, got {tuple(gate.shape)}")
 
 
 def _norm_before(x, weight, eps, w_offset, out=None):
-    _2d(x, "x")
-    code = _dtype(x, "x")
-    x = _row_strided(x)
-    weight, _, f32 = _norm_weights(x, weight, None)
-    out = _out(out, x.shape, x.dtype, x.device)
-    _b._same_device(*_present(x, weight, out))
-    T, H = x.shape
-    _check(lib().moe_norm_before(code, x.data_ptr(), x.stride(0), _p(weight), f32, w_offset, eps, T, H,
-                                 out.data_ptr(), _stream()), "moe_norm_before")
+    x, ld, code, dev, shape = _first(x, "x")
+    T, H = shape
+    weight, _, f32 = _norm_weights(weight, None, H, x.dtype, dev)
+    out = _out(out, shape, x.dtype, x.device)
+    _check(lib().moe_norm_before(code, x.data_ptr(), ld, _p(weight), f32, w_offset, eps, T, H, out.data_ptr(),
+                                 _raw_stream(dev)), "moe_norm_before")
     return out
 
 
@@ -376,46 +415,38 @@ def _norm_workspace(H, device):
 def norm_before_backward(dy, x, weight=None, eps=1e-6, weight_offset=0.0, dr=None):
     """Gradient of norm_before: (dx, d_weight); d_weight is None without weight.
     dr, if given, is added to dx: the gradient that reaches x by the residual."""
-    _2d(x, "x")
-    code = _dtype(x, "x")
-    x = _row_strided(x)
-    T, H = x.shape
-    dy = _rows(dy, x, x.shape, "dy")
-    dr = None if dr is None else _rows(dr, x, x.shape, "dr")
-    weight, _, f32 = _norm_weights(x, weight, None)
-    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    x, ld, code, dev, shape = _first(x, "x")
+    T, H = shape
+    dy, ld_dy = _rows(dy, x.dtype, shape, dev, "dy")
+    ld_dr = 0
+    if dr is not None:
+        dr, ld_dr = _rows(dr, x.dtype, shape, dev, "dr")
+    weight, _, f32 = _norm_weights(weight, None, H, x.dtype, dev)
+    dx = torch.empty(shape, dtype=x.dtype, device=x.device)
     d_weight = None if weight is None else torch.empty_like(weight)
-    _b._same_device(*_present(x, dy, dr, weight))
     ws, n = _norm_workspace(H, x.device)
-    _check(lib().moe_norm_before_backward(code, dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), _p(dr),
-                                          0 if dr is None else dr.stride(0), _p(weight), f32, weight_offset, eps, T,
-                                          H, dx.data_ptr(), _p(d_weight), ws.data_ptr(), n, _stream()),
-           "moe_norm_before_backward")
+    _check(lib().moe_norm_before_backward(code, dy.data_ptr(), ld_dy, x.data_ptr(), ld, _p(dr), ld_dr, _p(weight), f32,
+                                          weight_offset, eps, T, H, dx.data_ptr(), _p(d_weight), ws.data_ptr(), n,
+                                          _raw_stream(dev)), "moe_norm_before_backward")
     return dx, d_weight
 
 
-def _after_args(x, weight, gate, gate_act, norm, next_weight, next_norm):
+def _norm_after(x, h, weight, gate, gate_act, alpha, beta, eps, w_offset, norm, next_weight, next_norm, next_eps):
+    x, ld, code, dev, shape = _first(x, "x")
+    T, H = shape
+    dtype = x.dtype
+    h, ld_h = _rows(h, dtype, shape, dev, "h")
     if weight is not None and not norm:
         raise ValueError("weight belongs to the norm of h: norm must be true")
-    if next_weight is not None and next_norm is False:
+    if next_weight is not None and not next_norm:
         raise ValueError("next_weight belongs to the next block's norm: next_norm must not be False")
-    return (*_norm_weights(x, weight, next_weight), *_gate(gate, gate_act, x))
-
-
-def _norm_after(x, h, weight, gate, gate_act, alpha, beta, eps, w_offset, norm, next_weight, next_norm, next_eps):
-    _2d(x, "x")
-    code = _dtype(x, "x")
-    x = _row_strided(x)
-    h = _rows(h, x, x.shape, "h")
-    weight, next_weight, f32, gate, kind, act, ld_gate = _after_args(x, weight, gate, gate_act, norm, next_weight,
-                                                                     next_norm)
-    T, H = x.shape
-    r = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    weight, next_weight, f32 = _norm_weights(weight, next_weight, H, dtype, dev)
+    gate, kind, act, ld_gate = _gate(gate, gate_act, shape, dtype, dev)
+    r = torch.empty(shape, dtype=dtype, device=x.device)
     y = torch.empty_like(r) if next_norm else None
-    _b._same_device(*_present(x, h, weight, next_weight, gate))
-    _check(lib().moe_norm_after(code, x.data_ptr(), x.stride(0), h.data_ptr(), h.stride(0), int(norm), _p(weight),
-                                _p(next_weight), f32, w_offset, kind, act, _p(gate), ld_gate, alpha, beta, eps,
-                                next_eps, T, H, r.data_ptr(), _p(y), _stream()), "moe_norm_after")
+    _check(lib().moe_norm_after(code, x.data_ptr(), ld, h.data_ptr(), ld_h, int(norm), _p(weight), _p(next_weight),
+                                f32, w_offset, kind, act, _p(gate), ld_gate, alpha, beta, eps, next_eps, T, H,
+                                r.data_ptr(), _p(y), _raw_stream(dev)), "moe_norm_after")
     return (r, y) if next_norm else r
 
 
@@ -425,31 +456,33 @@ def norm_after_backward(dr, h, weight=None, *, gate=None, gate_act="none", alpha
     for what the forward did not have. dr is the gradient of r; with the next
     norm, dy that of y, and r the forward's result. Without the next norm and
     with beta = 1, dx is dr itself."""
-    _2d(h, "h")
-    code = _dtype(h, "h")
-    h = _row_strided(h)
-    T, H = h.shape
-    dr = _rows(dr, h, h.shape, "dr")
+    h, ld_h, code, dev, shape = _first(h, "h")
+    T, H = shape
+    dtype, device = h.dtype, h.device
+    dr, ld_dr = _rows(dr, dtype, shape, dev, "dr")
     if (dy is None) != (r is None):
         raise ValueError("dy and r come together")
-    if dy is None and next_weight is not None:
-        raise ValueError("next_weight belongs to the next block's norm: dy is missing")
+    if weight is not None and not norm:
+        raise ValueError("weight belongs to the norm of h: norm must be true")
+    ld_dy = ld_r = 0
     if dy is not None:
-        dy, r = _rows(dy, h, h.shape, "dy"), _rows(r, h, h.shape, "r")
-    weight, next_weight, f32, gate, kind, act, ld_gate = _after_args(h, weight, gate, gate_act, norm, next_weight,
-                                                                     dy is not None)
-    dx = None if dy is None and beta == 1.0 else torch.empty(T, H, dtype=h.dtype, device=h.device)
-    dh = torch.empty(T, H, dtype=h.dtype, device=h.device)
+        dy, ld_dy = _rows(dy, dtype, shape, dev, "dy")
+        r, ld_r = _rows(r, dtype, shape, dev, "r")
+    elif next_weight is not None:
+        raise ValueError("next_weight belongs to the next block's norm: dy is missing")
+    weight, next_weight, f32 = _norm_weights(weight, next_weight, H, dtype, dev)
+    gate, kind, act, ld_gate = _gate(gate, gate_act, shape, dtype, dev)
+    dx = None if dy is None and beta == 1.0 else torch.empty(shape, dtype=dtype, device=device)
+    dh = torch.empty(shape, dtype=dtype, device=device)
     d_weight = None if weight is None else torch.empty_like(weight)
     d_next = None if next_weight is None else torch.empty_like(next_weight)
-    d_gate = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
-    _b._same_device(*_present(dr, dy, h, r, weight, next_weight, gate))
-    ws, n = _norm_workspace(H, h.device)
+    d_gate = None if gate is None else torch.empty(gate.shape, dtype=dtype, device=device)
+    ws, n = _norm_workspace(H, device)
     _check(lib().moe_norm_after_backward(
-        code, dr.data_ptr(), dr.stride(0), _p(dy), 0 if dy is None else dy.stride(0), h.data_ptr(), h.stride(0),
-        _p(r), 0 if r is None else r.stride(0), int(norm), _p(weight), _p(next_weight), f32, weight_offset, kind,
-        act, _p(gate), ld_gate, alpha, beta, eps, eps if next_eps is None else next_eps, T, H, _p(dx), dh.data_ptr(),
-        _p(d_weight), _p(d_gate), _p(d_next), ws.data_ptr(), n, _stream()), "moe_norm_after_backward")
+        code, dr.data_ptr(), ld_dr, _p(dy), ld_dy, h.data_ptr(), ld_h, _p(r), ld_r, int(norm), _p(weight),
+        _p(next_weight), f32, weight_offset, kind, act, _p(gate), ld_gate, alpha, beta, eps,
+        eps if next_eps is None else next_eps, T, H, _p(dx), dh.data_ptr(), _p(d_weight), _p(d_gate), _p(d_next),
+        ws.data_ptr(), n, _raw_stream(dev)), "moe_norm_after_backward")
     return dr if dx is None else dx, dh, d_weight, d_gate, d_next
 
 
@@ -519,10 +552,8 @@ class PreparedMatvec:
     def __init__(self, fmt, N, K, group, swiglu, scale_dtype, prepared):
         self.fmt, self.N, self.K, self.group, self.swiglu = fmt, N, K, group, swiglu
         self.scale_dtype, self.prepared = scale_dtype, prepared
-
-    @property
-    def out_features(self):
-        return self.N // 2 if self.swiglu else self.N
+        self.out_features = N // 2 if swiglu else N
+        self._args = QFMT[fmt], N, K, group, int(swiglu)
 
 
 def prepare_matvec(weights, swiglu=False):
@@ -550,32 +581,32 @@ def prepare_matvec(weights, swiglu=False):
     if zero is not None and (fmt == "fp4" or zero.dtype != torch.uint8 or tuple(zero.shape) != (N, groups)):
         raise ValueError(f"w_zero must be uint8 [{N}, {groups}], for int4 weights")
     w, scale, zero = w.contiguous(), scale.contiguous(), None if zero is None else zero.contiguous()
-    _b._same_device(*_present(w, scale, zero))
+    dev = _device(w)
+    _b._same_device(scale, *([] if zero is None else [zero]))
     prepared = torch.empty(n, dtype=torch.uint8, device=w.device)
     scale_dtype = 0 if fmt == "fp4" else DTYPES[scale.dtype]
     _check(lib().moe_matvec_prepare(QFMT[fmt], N, K, group, int(swiglu), w.data_ptr(), scale.data_ptr(), scale_dtype,
-                                    _p(zero), prepared.data_ptr(), n, _stream()), "moe_matvec_prepare")
+                                    _p(zero), prepared.data_ptr(), n, _raw_stream(dev)), "moe_matvec_prepare")
     return PreparedMatvec(fmt, N, K, group, bool(swiglu), scale_dtype, prepared)
 
 
 def matvec(x, prepared, swiglu_limit=None, out=None):
     """x [T, K] bf16 or fp16 times the prepared weights, [T, N] ([T, N/2] with
     SwiGLU) of x's type, for few tokens. Not differentiable."""
-    _2d(x, "x")
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"matvec takes bfloat16 or float16 x, got {x.dtype}")
+    x, ld, code, dev, (T, K) = _first(x, "x")
+    if code == 2:
+        raise ValueError("matvec takes bfloat16 or float16 x, got torch.float32")
     p = prepared
-    if x.shape[1] != p.K:
-        raise ValueError(f"x has {x.shape[1]} columns, the prepared weights {p.K}")
+    if K != p.K:
+        raise ValueError(f"x has {K} columns, the prepared weights {p.K}")
     if swiglu_limit is not None and not p.swiglu:
         raise ValueError("swiglu_limit is for weights prepared with swiglu=True")
-    x = _row_strided(x)
-    out = _out(out, (x.shape[0], p.out_features), x.dtype, x.device)
-    _b._same_device(x, p.prepared, out)
-    _check(lib().moe_matvec(QFMT[p.fmt], p.N, p.K, p.group, int(p.swiglu),
-                            _NO_LIMIT if swiglu_limit is None else swiglu_limit, p.scale_dtype,
-                            p.prepared.data_ptr(), DTYPES[x.dtype], x.data_ptr(), x.stride(0), x.shape[0],
-                            out.data_ptr(), _stream()), "moe_matvec")
+    if p.prepared.get_device() != dev:
+        _b._same_device(p.prepared)
+    out = _out(out, (T, p.out_features), x.dtype, x.device)
+    _check(lib().moe_matvec(*p._args, _NO_LIMIT if swiglu_limit is None else swiglu_limit, p.scale_dtype,
+                            p.prepared.data_ptr(), code, x.data_ptr(), ld, T, out.data_ptr(), _raw_stream(dev)),
+           "moe_matvec")
     return out
 
 

@@ -161,7 +161,7 @@ moe_status moe_norm_before(int dtype, const void* x, int64_t ld_x, const void* w
 }
 
 size_t moe_norm_backward_workspace_bytes(int H) {
-  return norm_shape_ok(0, H) ? sizeof(float) * 3 * kNormParts * H : 0;
+  return norm_shape_ok(0, H) ? sizeof(float) * 2 * kNormParts * H : 0;
 }
 
 moe_status moe_norm_before_backward(int dtype, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,

@@ -67,7 +67,7 @@ struct NormBackwardArgs {
   const void *dr, *dy;
   int64_t ld_dr, ld_dy, ld_r;
   void *dx, *dh, *d_weight, *d_gate, *d_next_weight;
-  float* partials;  // [3][kNormParts][H]
+  float* partials;  // [2][kNormParts][H]
 };
 constexpr int kNormParts = 304;  // column sums are taken over at most this many row sets
 cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& a, int num_sms, cudaStream_t st);

@@ -13,16 +13,12 @@
 // become fp16 in registers, exactly; the group scale multiplies the group's
 // fp32 sums.
 //
-// x is staged in shared memory as fp16. bf16 rows are first scaled by a power
-// of two that brings their largest finite value to [2^14, 2^15): fp16 then
-// holds every element exactly down to 2^-29 of the largest, and below that
-// with an error under 2^-40 of the largest, far below the fp32 sums' own. The
-// 2^14 is taken back with the group scales, so that the fp32 sums stay in the
-// range of the result's for every UE8M0 scale; the rest of the power at the end.
+// x is staged in shared memory as fp16. The 128 elements of a bf16 row that
+// meet one block are scaled by a power of two that brings their largest finite
+// value to [2^14, 2^15): fp16 then holds every element exactly down to 2^-29
+// of the largest, and below that with an error under 2^-40 of the largest, far
+// below the fp32 sums' own. The power is taken back on each group's sums.
 #include <cooperative_groups.h>
-#include <cuda_fp4.h>
-#include <cuda_fp8.h>
-
 #include <cmath>
 #include <type_traits>
 
@@ -43,7 +39,6 @@ constexpr int kMvDepth = 4;    // blocks in flight per warp
 constexpr int kMvTokens = 16;  // tokens of a pass, two N = 8 tiles
 constexpr int kMvMaxSmem = 184 * 1024;  // for x
 constexpr int kMvMaxCluster = 8;
-constexpr int kXTop = 14;      // bf16 rows are brought to a largest value in [2^14, 2^15)
 template <typename X>
 constexpr bool kScaledX = std::is_same<X, __nv_bfloat16>::value;
 constexpr int kCodeBytes = kMvRows * kMvStep / 2;
@@ -72,6 +67,7 @@ struct MvArgs {
   int cluster;   // CTAs that share a tile's K range
   float limit;
   bool swiglu;
+  bool x_vec;  // rows of x allow 16-byte loads
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -82,15 +78,46 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t fp4_pair(uint32_t word, int p) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(word >> (8 * p)), __NV_E2M1);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// The eight e2m1 codes of a word as fp16 pairs, in order.
+__device__ __forceinline__ void fp4_pairs(uint32_t word, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(word));
 }
-// 1024 + code as fp16, minus 1024 + zero: exact.
-__device__ __forceinline__ uint32_t int4_pair(uint32_t word, int p, __half2 zero) {
-  const uint32_t biased = ((word >> (4 * p)) & 0x000F000Fu) | 0x64006400u;
-  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&biased), zero);
-  return *reinterpret_cast<const uint32_t*>(&v);
+// Four UE8M0 bytes as floats (bf16 holds them all; 255 is NaN).
+__device__ __forceinline__ void ue8m0_scales(uint32_t word, float (&s)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(word));
+  s[0] = __uint_as_float(lo << 16);
+  s[1] = __uint_as_float(lo & 0xFFFF0000u);
+  s[2] = __uint_as_float(hi << 16);
+  s[3] = __uint_as_float(hi & 0xFFFF0000u);
+}
+// The eight codes of a word minus zero as fp16 pairs: with the bits of 1024
+// above a code the half is 1024 + code, or 1024 + 16 code where the code sits
+// four bits up; both differences are exact. zero: 1024 + z.
+__device__ __forceinline__ void int4_pairs(uint32_t word, __half2 zero, uint32_t (&h)[4]) {
+  const __half2 up = __float2half2_rn(0.0625f);
+  const __half2 zero16 = __hsub2(__float2half2_rn(960.f), zero);  // -(64 + z)
+#pragma unroll
+  for (int p = 0; p < 4; p += 2) {
+    const uint32_t w = word >> (4 * p);
+    const uint32_t a = (w & 0x000F000Fu) | 0x64006400u, b = (w & 0x00F000F0u) | 0x64006400u;
+    const __half2 va = __hsub2(*reinterpret_cast<const __half2*>(&a), zero);
+    const __half2 vb = __hfma2(*reinterpret_cast<const __half2*>(&b), up, zero16);
+    h[p] = *reinterpret_cast<const uint32_t*>(&va);
+    h[p + 1] = *reinterpret_cast<const uint32_t*>(&vb);
+  }
 }
 
 // What a warp holds of one block.
@@ -113,12 +140,22 @@ __device__ __forceinline__ void load_block(Block<SW>& b, const uint8_t* p, int l
   }
 }
 
-// acc += block x tokens. GROUPS: scale groups per block (4, 2 or 1).
+// acc += block x tokens. GROUPS: scale groups per block (4, 2 or 1). xs: the
+// tokens' rows at the block's k, x_scale: their powers for this block.
 template <int FMT, int GROUPS, int NT, typename S, typename X, int SW>
 __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<SW>& b, const uint8_t* xs,
-                                               int x_stride, int T, int lane) {
-  constexpr float kBack = kScaledX<X> ? 1.f / (1 << kXTop) : 1.f;
+                                               int x_stride, const float* x_scale, int T, int lane) {
   const int g = lane >> 2, q = lane & 3;
+  float scale[2][4];
+  if constexpr (FMT == MOE_Q_FP4) {
+    ue8m0_scales(b.scale[0], scale[0]);
+    ue8m0_scales(b.scale[1], scale[1]);
+  }
+  float2 back[NT];
+  if constexpr (kScaledX<X>) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) back[n] = *reinterpret_cast<const float2*>(x_scale + n * 8 + 2 * q);
+  }
   float c[NT][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // 32 k each
@@ -131,36 +168,33 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
     const uint32_t w1 = (i & 1) ? b.codes[i >> 1].w : b.codes[i >> 1].y;
     const bool first = (i * GROUPS) % 4 == 0, last = ((i + 1) * GROUPS) % 4 == 0;
     const int grp = i * GROUPS / 4;
-    uint32_t a[2][4];
+    uint32_t a0[4], a1[4];
     float s0, s1;
-    if (FMT == MOE_Q_FP4) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        a[0][p] = fp4_pair(w0, p);
-        a[1][p] = fp4_pair(w1, p);
-      }
-      const __nv_bfloat16_raw e0 = __nv_cvt_e8m0_to_bf16raw((b.scale[0] >> (8 * i)) & 0xFF);
-      const __nv_bfloat16_raw e1 = __nv_cvt_e8m0_to_bf16raw((b.scale[1] >> (8 * i)) & 0xFF);
-      s0 = __uint_as_float(static_cast<uint32_t>(e0.x) << 16) * kBack;
-      s1 = __uint_as_float(static_cast<uint32_t>(e1.x) << 16) * kBack;
+    if constexpr (FMT == MOE_Q_FP4) {
+      fp4_pairs(w0, a0);
+      fp4_pairs(w1, a1);
+      s0 = scale[0][i];
+      s1 = scale[1][i];
     } else {
       const uint32_t sz0 = b.scale[2 * grp], sz1 = b.scale[2 * grp + 1];
-      const __half2 z0 = __half2half2(__ushort_as_half(sz0 >> 16)), z1 = __half2half2(__ushort_as_half(sz1 >> 16));
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        a[0][p] = int4_pair(w0, p, z0);
-        a[1][p] = int4_pair(w1, p, z1);
-      }
+      int4_pairs(w0, __half2half2(__ushort_as_half(sz0 >> 16)), a0);
+      int4_pairs(w1, __half2half2(__ushort_as_half(sz1 >> 16)), a1);
       const uint16_t h0 = sz0 & 0xFFFF, h1 = sz1 & 0xFFFF;
-      s0 = to_f32(*reinterpret_cast<const S*>(&h0)) * kBack;
-      s1 = to_f32(*reinterpret_cast<const S*>(&h1)) * kBack;
+      s0 = to_f32(*reinterpret_cast<const S*>(&h0));
+      s1 = to_f32(*reinterpret_cast<const S*>(&h1));
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (first) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-      mma_16816(c[n], a[0][0], a[1][0], a[0][1], a[1][1], xv[n].x, xv[n].y);
-      mma_16816(c[n], a[0][2], a[1][2], a[0][3], a[1][3], xv[n].z, xv[n].w);
+      mma_16816(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y);
+      mma_16816(c[n], a0[2], a1[2], a0[3], a1[3], xv[n].z, xv[n].w);
       if (last) {
+        if constexpr (kScaledX<X>) {
+          c[n][0] *= back[n].x;
+          c[n][1] *= back[n].y;
+          c[n][2] *= back[n].x;
+          c[n][3] *= back[n].y;
+        }
         acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
         acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
         acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
@@ -172,8 +206,7 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
 
 // A lane's sums: rows g and g + 8 of the tile for tokens 2q, 2q + 1.
 template <typename X, int NT>
-__device__ __forceinline__ void store_tile(const MvArgs& a, int tile, const float (&acc)[NT][4], const float* s_unscale,
-                                           int lane) {
+__device__ __forceinline__ void store_tile(const MvArgs& a, int tile, const float (&acc)[NT][4], int lane) {
   const int g = lane >> 2, q = lane & 3;
   X* y = static_cast<X*>(a.y);
 #pragma unroll
@@ -182,8 +215,7 @@ __device__ __forceinline__ void store_tile(const MvArgs& a, int tile, const floa
     for (int i = 0; i < 2; ++i) {
       const int t = n * 8 + 2 * q + i;
       if (t >= a.T) continue;
-      const float u = s_unscale[t];
-      float lo = acc[n][i] * u, hi = acc[n][2 + i] * u;
+      float lo = acc[n][i], hi = acc[n][2 + i];
       if (a.swiglu) {
         const int col = tile * 8 + g;
         if (a.limit > 0.f) {
@@ -209,8 +241,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   constexpr int SW = FMT == MOE_Q_FP4 ? 2 : 2 * GROUPS;
   extern __shared__ __align__(16) uint8_t s_x[];
   __shared__ float s_red[2][kMvWarps][NT][4][32];
-  __shared__ float s_amax[kMvTokens][kMvWarps];
-  __shared__ float s_scale[kMvTokens], s_unscale[kMvTokens];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int first_step = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.cluster);
@@ -239,43 +269,49 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
 #pragma unroll
   for (int d = 0; d < kMvDepth; ++d) advance(ring[d]);
 
-  // x: this CTA's K range as fp16, rows 64 bytes apart modulo 128
-  const int k0 = first_step * kMvStep, kn = cta_steps * kMvStep;
-  const int x_stride = kn * 2 + 64;
+  // x: this CTA's K range as fp16, rows 64 bytes apart modulo 128 (the four
+  // 16-byte reads of two tokens fill the banks), then the powers [step][token]
+  const int x_stride = cta_steps * kMvStep * 2 + 64;
+  float* s_power = reinterpret_cast<float*>(s_x + static_cast<size_t>(a.T) * x_stride);
   const X* x = static_cast<const X*>(a.x);
-  if (kScaledX<X>) {
-    for (int t = 0; t < a.T; ++t) {
-      float m = 0.f;
-      for (int k = tid; k < a.K; k += kMvThreads) {
-        const float v = fabsf(to_f32(x[t * a.ld_x + k]));
-        if (v < INFINITY) m = fmaxf(m, v);
-      }
+  for (int unit = tid >> 4; unit < a.T * cta_steps; unit += kMvThreads / 16) {
+    const int t = unit / cta_steps, step = unit - t * cta_steps;
+    const int at = step * kMvStep + (lane & 15) * 8, k = first_step * kMvStep + at;
+    Pack<X, 8> p;
+    if (a.x_vec && k < a.K) {
+      p = load_pack<8>(x + t * a.ld_x + k);
+    } else {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane == 0) s_amax[t][warp] = m;
+      for (int i = 0; i < 8; ++i) p.e[i] = k < a.K ? x[t * a.ld_x + k + i] : from_f32<X>(0.f);
     }
-    __syncthreads();
-    if (tid < a.T) {
-      float m = 0.f;
-      for (int w = 0; w < kMvWarps; ++w) m = fmaxf(m, s_amax[tid][w]);
-      const int e = m > 0.f ? max(kXTop - 126, ilogbf(m)) : 0;
-      s_scale[tid] = ldexpf(1.f, kXTop - e);
-      s_unscale[tid] = ldexpf(1.f, e);
+    uint4 out;
+    if constexpr (kScaledX<X>) {
+      float f[8], m = 0.f;
+      unpack(p, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fabsf(f[i]) < INFINITY ? fmaxf(m, fabsf(f[i])) : m;
+      const unsigned half = 0xFFFFu << (lane & 16);  // the units of a warp end apart
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
+      // 2^(14 - e) and back, e the exponent of m (at least -112: both are normal)
+      const int e = max(15, static_cast<int>(__float_as_uint(m) >> 23));
+      const float scale = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+      uint32_t* w = &out.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(f[2 * i] * scale, f[2 * i + 1] * scale);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if ((lane & 15) == 0) s_power[step * kMvTokens + t] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+    } else {
+      out = *reinterpret_cast<const uint4*>(&p);
     }
-  } else if (tid < kMvTokens) {
-    s_scale[tid] = s_unscale[tid] = 1.f;
-  }
-  __syncthreads();
-  for (int t = 0; t < a.T; ++t) {
-    __half* row = reinterpret_cast<__half*>(s_x + static_cast<size_t>(t) * x_stride);
-    for (int k = tid; k < kn; k += kMvThreads) {
-      const int gk = k0 + k;
-      row[k] = gk < a.K ? __float2half_rn(to_f32(x[t * a.ld_x + gk]) * s_scale[t]) : __half(__ushort_as_half(0));
-    }
+    *reinterpret_cast<uint4*>(s_x + static_cast<size_t>(t) * x_stride + at * 2) = out;
   }
   __syncthreads();
 
   const uint8_t* xs = s_x + s0 * (kMvStep * 2);
+  const float* xp = s_power + s0 * kMvTokens;
   float acc[NT][4] = {};
   int tile = tile0, s = 0;
   int parity = 0;
@@ -295,7 +331,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
       }
       parity ^= 1;
     }
-    if (wk == 0 && a.cluster == 1 && tile < a.tiles) store_tile<X, NT>(a, tile, acc, s_unscale, lane);
+    if (wk == 0 && a.cluster == 1 && tile < a.tiles) store_tile<X, NT>(a, tile, acc, lane);
   };
   if (a.cluster > 1) {
     // one tile: the whole CTA shares it
@@ -303,7 +339,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
 #pragma unroll
       for (int d = 0; d < kMvDepth; ++d) {
         if (i + d >= ns) break;
-        multiply_block<FMT, GROUPS, NT, S, X>(acc, ring[d], xs + (i + d) * (kMvStep * 2), x_stride, a.T, lane);
+        multiply_block<FMT, GROUPS, NT, S, X>(acc, ring[d], xs + (i + d) * (kMvStep * 2), x_stride,
+                                                xp + (i + d) * kMvTokens, a.T, lane);
         advance(ring[d]);
       }
     }
@@ -324,7 +361,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[n][i] += (&s_red[1][0][0][0][0])[r * (NT * 128) + (n * 4 + i) * 32 + lane];
-      store_tile<X, NT>(a, tile, acc, s_unscale, lane);
+      store_tile<X, NT>(a, tile, acc, lane);
     }
     return;
   }
@@ -334,7 +371,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
     for (int d = 0; d < kMvDepth; ++d) {
       if (i + d >= total) break;
       if (tile < a.tiles)
-        multiply_block<FMT, GROUPS, NT, S, X>(acc, ring[d], xs + s * (kMvStep * 2), x_stride, a.T, lane);
+        multiply_block<FMT, GROUPS, NT, S, X>(acc, ring[d], xs + s * (kMvStep * 2), x_stride, xp + s * kMvTokens,
+                                                a.T, lane);
       advance(ring[d]);
       if (++s == ns) {
         finish();
@@ -485,15 +523,18 @@ cudaError_t launch_matvec(const MatvecShape& s, float limit, int scale_dtype, co
     while (a.cluster < kMvMaxCluster && a.tiles * a.cluster * 2 <= num_sms && a.steps >= 2 * kMvWarps * a.cluster)
       a.cluster *= 2;
   const int cta_k = ceil_div(a.steps, a.cluster) * kMvStep;
-  const int pass = std::max(1, std::min<int>(kMvTokens, kMvMaxSmem / (2 * cta_k + 64)));
+  // of a token: fp16 and its place among the powers
+  const int x_row = 2 * cta_k + 64, power = cta_k / kMvStep * kMvTokens * 4;
+  const int pass = std::max(1, std::min<int>(kMvTokens, (kMvMaxSmem - power) / x_row));
   const int cta_tiles = ceil_div(a.tiles, kMvWarps / a.warps_k);
   const int grid = a.cluster > 1 ? a.tiles * a.cluster : std::min(cta_tiles, num_sms);
   const size_t es = 2;
   for (int t0 = 0; t0 < T; t0 += pass) {
     a.T = std::min(pass, T - t0);
+    a.x_vec = aligned16(x) && ld_x % 8 == 0;
     a.x = static_cast<const uint8_t*>(x) + static_cast<size_t>(t0) * ld_x * es;
     a.y = static_cast<uint8_t*>(y) + static_cast<size_t>(t0) * a.out_cols * es;
-    const size_t smem = static_cast<size_t>(a.T) * (2 * cta_k + 64);
+    const size_t smem = static_cast<size_t>(a.T) * x_row + power;
     const cudaError_t e = dtype == MOE_BF16 ? run_format<__nv_bfloat16>(s.fmt, scale_dtype, s.group, a, grid, smem, st)
                                             : run_format<__half>(s.fmt, scale_dtype, s.group, a, grid, smem, st);
     if (e != cudaSuccess) return e;

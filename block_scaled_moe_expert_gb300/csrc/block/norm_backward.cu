@@ -7,80 +7,136 @@
 //
 // One pass over the rows: every input is read once and every output written
 // once; the row statistics are computed again from rows that are loaded
-// anyway, so the forward saves nothing. A block walks many rows and keeps the
-// column sums (weights, channel gate) of its rows; a second small kernel adds
-// the blocks' sums in block order, so the same call gives the same bits.
-// Bound by DRAM bandwidth.
+// anyway, so the forward saves nothing. A block walks many rows with the next
+// ones on their way (RowQueue) and keeps two column sums of its rows in
+// registers: sum_t gate inv G h, from which the weight's gradient (times
+// alpha g) and the channel gate's (times alpha act' w) both follow, and the
+// next weight's. A second small kernel adds the blocks' sums in block order,
+// so the same call gives the same bits. Bound by DRAM bandwidth.
 #include "norm_common.cuh"
 
 namespace bsmoe {
 
 namespace {
 
-enum { kSumWeight = 0, kSumNext = 1, kSumGate = 2 };
+enum { kDr = 0, kDy = 1, kR = 2, kH = 3, kGate = 4 };
+enum { kSumBlock = 0, kSumNext = 1 };
 
 __device__ __forceinline__ bool wants(const NormBackwardArgs& b, int which) {
-  if (which == kSumWeight) return b.d_weight != nullptr;
-  if (which == kSumNext) return b.d_next_weight != nullptr;
-  return b.f.gate_kind == MOE_GATE_CHANNEL;
+  if (which == kSumBlock) return b.d_weight != nullptr || b.f.gate_kind == MOE_GATE_CHANNEL;
+  return b.d_next_weight != nullptr;
 }
 __device__ __forceinline__ float* partial_row(const NormBackwardArgs& b, int which, int part) {
   return b.partials + (static_cast<size_t>(which) * kNormParts + part) * b.f.H;
 }
 
-template <typename T, int V, int CH, bool WARP>
-__global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs b) {
-  extern __shared__ float s_cols[];            // WARP: [H], the join of the block's warps
-  __shared__ float s_sum[2][2][2][32];
+template <typename T, int V, int CH, int STAGES, bool AFTER, bool NEXT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(NormBackwardArgs b) {
+  constexpr int ARRAYS = AFTER ? 5 : 3;
+  // the columns' factors stand in shared memory behind the ring (each thread
+  // its own): beside the column sums they would not fit into the registers
+  constexpr bool CACHED = STAGES > 0 && !WARP;
+  extern __shared__ __align__(16) uint8_t s_ring[];
+  __shared__ __align__(16) float s_sum[2][2][2][32];
+  const NormArgs& a = b.f;
+  RowQueue<T, V, CH, ARRAYS, STAGES> rows;
+  rows.H = a.H;
+  rows.threads = WARP ? 32 : blockDim.x;
+  rows.j = WARP ? threadIdx.x & 31 : threadIdx.x;
+  rows.src[kDr] = static_cast<const T*>(b.dr);
+  rows.src[kDy] = NEXT ? static_cast<const T*>(b.dy) : nullptr;
+  rows.src[kR] = NEXT ? static_cast<const T*>(a.r) : nullptr;
+  rows.ld[kDr] = b.ld_dr;
+  rows.ld[kDy] = b.ld_dy;
+  rows.ld[kR] = b.ld_r;
+  if constexpr (AFTER) {
+    rows.src[kH] = static_cast<const T*>(a.h);
+    rows.src[kGate] = a.gate_kind == MOE_GATE_ELEMENT ? static_cast<const T*>(a.gate) : nullptr;
+    rows.ld[kH] = a.ld_h;
+    rows.ld[kGate] = a.ld_gate;
+  }
+  if (!WARP)
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) (&s_sum[0][0][0][0])[i] = 0.f;
   pdl_wait();
   pdl_launch_dependents();
-  const NormArgs& a = b.f;
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int j = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int warp = threadIdx.x >> 5;
   const int per_block = WARP ? blockDim.x / 32 : 1;
-  const bool after = a.h != nullptr, next = a.next != 0;
-  const float inv_h = 1.f / static_cast<float>(a.H);
-  float sums[3][CH][V] = {};
-  int parity = 0;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + (WARP ? warp : 0); t < a.T;
-       t += static_cast<int64_t>(gridDim.x) * per_block, parity ^= 1) {
-    Pack<T, V> drp[CH], dyp[CH], rp[CH], hp[CH];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_block + (WARP ? warp : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+  rows.start(first, step, a.T, s_ring);
+
+  auto factor = [&](int c, float (&f)[V]) {  // w times the channel gate
+    load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c, f);
+    if (a.gate_kind == MOE_GATE_CHANNEL) times_channel_gate<T, V>(a, c, f);
+  };
+  float4* s_factor = reinterpret_cast<float4*>(s_ring + static_cast<size_t>(STAGES) * rows.stage_packs * 16) + rows.j;
+  auto put_factor = [&](int which, int i, const float (&f)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4)
+      s_factor[((which * CH + i) * (V / 4) + v / 4) * rows.threads] = make_float4(f[v], f[v + 1], f[v + 2], f[v + 3]);
+  };
+  auto get_factor = [&](int which, int i, int c, float (&f)[V]) {
+    if constexpr (CACHED) {
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        const float4 q = s_factor[((which * CH + i) * (V / 4) + v / 4) * rows.threads];
+        f[v] = q.x;
+        f[v + 1] = q.y;
+        f[v + 2] = q.z;
+        f[v + 3] = q.w;
+      }
+    } else if (which == kSumBlock) {
+      factor(c, f);
+    } else {
+      load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c, f);
+    }
+  };
+  if constexpr (CACHED) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = (i * tpr + j) * V;
+      const int c = rows.column(i);
       if (c >= a.H) continue;
-      if (b.dr != nullptr) drp[i] = load_pack<V>(static_cast<const T*>(b.dr) + t * b.ld_dr + c);
-      if (next) {
-        dyp[i] = load_pack<V>(static_cast<const T*>(b.dy) + t * b.ld_dy + c);
-        rp[i] = load_pack<V>(static_cast<const T*>(a.r) + t * b.ld_r + c);
+      float f[V];
+      if (AFTER) {
+        factor(c, f);
+        put_factor(kSumBlock, i, f);
       }
-      if (after) hp[i] = load_pack<V>(static_cast<const T*>(a.h) + t * a.ld_h + c);
+      if (NEXT) {
+        load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c, f);
+        put_factor(kSumNext, i, f);
+      }
     }
+  }
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  float sums[2][CH][V] = {};
+  if (!WARP) __syncthreads();  // s_sum is zero
+  int parity = 0;
+  for (int64_t t = first; t < a.T; t += step, parity ^= 1) {
+    rows.next();
     float G[CH][V];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (b.dr != nullptr && (i * tpr + j) * V < a.H) {
-        unpack(drp[i], G[i]);
+      if (b.dr != nullptr && rows.column(i) < a.H) {
+        unpack(rows.at(kDr, i), G[i]);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) G[i][e] = 0.f;
       }
     }
-    if (next) {
+    if constexpr (NEXT) {
       float ss[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = (i * tpr + j) * V;
+        const int c = rows.column(i);
         if (c >= a.H) continue;
-        float w[V], rf[V], dy[V];
-        load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c, w);
-        unpack(rp[i], rf);
-        unpack(dyp[i], dy);
+        float wn[V], rf[V], dy[V];
+        get_factor(kSumNext, i, c, wn);
+        unpack(rows.at(kR, i), rf);
+        unpack(rows.at(kDy, i), dy);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           ss[0] = fmaf(rf[e], rf[e], ss[0]);
-          ss[1] = fmaf(rf[e], w[e] * dy[e], ss[1]);
+          ss[1] = fmaf(rf[e], wn[e] * dy[e], ss[1]);
         }
       }
       row_sum<2, WARP>(ss, s_sum[parity][0]);
@@ -88,23 +144,24 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs b) 
       const float back = inv * inv * (inv * (ss[1] * inv_h));
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = (i * tpr + j) * V;
+        const int c = rows.column(i);
         if (c >= a.H) continue;
-        float w[V], rf[V], dy[V];
-        load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c, w);
-        unpack(rp[i], rf);
-        unpack(dyp[i], dy);
+        float wn[V], rf[V], dy[V];
+        get_factor(kSumNext, i, c, wn);
+        unpack(rows.at(kR, i), rf);
+        unpack(rows.at(kDy, i), dy);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          G[i][e] += inv * (w[e] * dy[e]) - rf[e] * back;
-          sums[kSumNext][i][e] = fmaf(dy[e], rf[e] * inv, sums[kSumNext][i][e]);
+          const float d = inv * dy[e];
+          G[i][e] += d * wn[e] - rf[e] * back;
+          sums[kSumNext][i][e] = fmaf(d, rf[e], sums[kSumNext][i][e]);
         }
       }
     }
     if (b.dx != nullptr) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = (i * tpr + j) * V;
+        const int c = rows.column(i);
         if (c >= a.H) continue;
         float o[V];
 #pragma unroll
@@ -112,85 +169,72 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs b) 
         store_pack(static_cast<T*>(b.dx) + t * a.H + c, pack<T, V>(o));
       }
     }
-    if (!after) continue;
-    // u = w gate G in place of G where the norm is applied; gates by column
-    // are read again for their gradient
-    const bool column_gate = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_ELEMENT;
-    const T* gate_row =
-        static_cast<const T*>(a.gate) + (a.gate_kind == MOE_GATE_CHANNEL ? 0 : t * a.ld_gate);
-    float gt = 1.f, gt_slope = 0.f;
-    if (a.gate_kind == MOE_GATE_TOKEN) {
-      gt = gate_value(a.gate_act, to_f32(gate_row[0]));
-      gt_slope = gate_slope(a.gate_act, gt);
-    }
-    float inv = 1.f, back = 0.f;
-    if (a.norm || a.gate_kind == MOE_GATE_TOKEN) {
-      float ss[2] = {0.f, 0.f};
+    if constexpr (AFTER) {
+      // a gate by element joins G here; its gradient takes the G without it
+      float gt = 1.f, gt_slope = 0.f;
+      if (a.gate_kind == MOE_GATE_TOKEN) {
+        gt = gate_value(a.gate_act, to_f32(static_cast<const T*>(a.gate)[t * a.ld_gate]));
+        gt_slope = gate_slope(a.gate_act, gt);
+      }
+      float inv = 1.f, back = 0.f;
+      if (a.norm || a.gate_kind == MOE_GATE_TOKEN) {
+        float ss[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int c = rows.column(i);
+          if (c >= a.H) continue;
+          float wa[V], hf[V], g[V];
+          get_factor(kSumBlock, i, c, wa);
+          unpack(rows.at(kH, i), hf);
+          if (a.gate_kind == MOE_GATE_ELEMENT) unpack(rows.at(kGate, i), g);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            float u = wa[e] * G[i][e];
+            if (a.gate_kind == MOE_GATE_ELEMENT) u *= gate_value(a.gate_act, g[e]);
+            ss[0] = fmaf(hf[e], hf[e], ss[0]);
+            ss[1] = fmaf(hf[e], u, ss[1]);
+          }
+        }
+        row_sum<2, WARP>(ss, s_sum[parity][1]);
+        if (a.norm) {
+          inv = rsqrtf(ss[0] * inv_h + a.eps);
+          back = inv * inv * (inv * (ss[1] * inv_h));
+        }
+        if (a.gate_kind == MOE_GATE_TOKEN && rows.j == 0)
+          static_cast<T*>(b.d_gate)[t] = from_f32<T>(gt_slope * (a.alpha * (inv * ss[1])));
+      }
+      const float scale = a.alpha * gt, scale_inv = scale * inv, scale_back = scale * back, gt_inv = gt * inv;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = (i * tpr + j) * V;
+        const int c = rows.column(i);
         if (c >= a.H) continue;
-        float w[V], hf[V];
-        load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c, w);
-        unpack(hp[i], hf);
-        if (column_gate) {
-          float g[V];
-          unpack(load_pack<V>(gate_row + c), g);
-#pragma unroll
-          for (int e = 0; e < V; ++e) w[e] *= gate_value(a.gate_act, g[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          ss[0] = fmaf(hf[e], hf[e], ss[0]);
-          ss[1] = fmaf(hf[e], w[e] * G[i][e], ss[1]);
-        }
-      }
-      row_sum<2, WARP>(ss, s_sum[parity][1]);
-      if (a.norm) {
-        inv = rsqrtf(ss[0] * inv_h + a.eps);
-        back = inv * inv * (inv * (ss[1] * inv_h));
-      }
-      if (a.gate_kind == MOE_GATE_TOKEN && j == 0)
-        static_cast<T*>(b.d_gate)[t] = from_f32<T>(gt_slope * (a.alpha * (inv * ss[1])));
-    }
-    const float scale = a.alpha * gt;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = (i * tpr + j) * V;
-      if (c >= a.H) continue;
-      float w[V], hf[V], g[V], o[V];
-      load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c, w);
-      unpack(hp[i], hf);
-      if (column_gate) {
-        unpack(load_pack<V>(gate_row + c), g);
-        float dg[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          g[e] = gate_value(a.gate_act, g[e]);
-          dg[e] = gate_slope(a.gate_act, g[e]) * (a.alpha * G[i][e] * (hf[e] * inv * w[e]));
-        }
+        float wa[V], hf[V], o[V];
+        get_factor(kSumBlock, i, c, wa);
+        unpack(rows.at(kH, i), hf);
         if (a.gate_kind == MOE_GATE_ELEMENT) {
+          float g[V], dg[V];
+          unpack(rows.at(kGate, i), g);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            g[e] = gate_value(a.gate_act, g[e]);
+            dg[e] = gate_slope(a.gate_act, g[e]) * (a.alpha * G[i][e] * (hf[e] * inv * wa[e]));
+            G[i][e] *= g[e];
+          }
           store_pack(static_cast<T*>(b.d_gate) + t * a.H + c, pack<T, V>(dg));
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) sums[kSumGate][i][e] += dg[e];
         }
-      } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[e] = 1.f;
+        for (int e = 0; e < V; ++e) {
+          o[e] = scale_inv * (wa[e] * G[i][e]) - hf[e] * scale_back;
+          sums[kSumBlock][i][e] = fmaf(gt_inv * G[i][e], hf[e], sums[kSumBlock][i][e]);
+        }
+        store_pack(static_cast<T*>(b.dh) + t * a.H + c, pack<T, V>(o));
       }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float gG = scale * (g[e] * G[i][e]);
-        o[e] = inv * (w[e] * gG) - scale * (hf[e] * back);
-        sums[kSumWeight][i][e] = fmaf(gG, hf[e] * inv, sums[kSumWeight][i][e]);
-      }
-      store_pack(static_cast<T*>(b.dh) + t * a.H + c, pack<T, V>(o));
     }
   }
 
+  float* s_cols = reinterpret_cast<float*>(s_ring);  // WARP: the join of the block's warps, behind the rows
 #pragma unroll
-  for (int which = 0; which < 3; ++which) {
+  for (int which = 0; which < 2; ++which) {
     if (!wants(b, which)) continue;
     float* part = partial_row(b, which, blockIdx.x);
     if (WARP) {  // the warps of the block in turn
@@ -199,7 +243,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs b) 
         if (warp != w) continue;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          const int c = (i * tpr + j) * V;
+          const int c = rows.column(i);
           if (c >= a.H) continue;
 #pragma unroll
           for (int e = 0; e < V; ++e) s_cols[c + e] = (w > 0 ? s_cols[c + e] : 0.f) + sums[which][i][e];
@@ -210,7 +254,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs b) 
     } else {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = (i * tpr + j) * V;
+        const int c = rows.column(i);
         if (c >= a.H) continue;
 #pragma unroll
         for (int e = 0; e < V; ++e) part[c + e] = sums[which][i][e];
@@ -223,22 +267,22 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs b) 
 // stand in shared memory (each thread its own columns).
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_backward_general_kernel(NormBackwardArgs b) {
-  extern __shared__ float s_cols[];  // [3][H]
+  extern __shared__ float s_cols[];  // [sums wanted][H]
   __shared__ float s_sum[2][2][2][32];
   pdl_wait();
   pdl_launch_dependents();
   const NormArgs& a = b.f;
   const bool after = a.h != nullptr, next = a.next != 0;
   const float inv_h = 1.f / static_cast<float>(a.H);
-  float* s_acc[3];
+  float* s_acc[2];
   {
     int n = 0;
-    for (int which = 0; which < 3; ++which) {
+    for (int which = 0; which < 2; ++which) {
       s_acc[which] = s_cols + static_cast<size_t>(n) * a.H;
       n += wants(b, which);
     }
   }
-  for (int which = 0; which < 3; ++which)
+  for (int which = 0; which < 2; ++which)
     if (wants(b, which))
       for (int c = threadIdx.x; c < a.H; c += blockDim.x) s_acc[which][c] = 0.f;
   const bool column_gate = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_ELEMENT;
@@ -307,48 +351,95 @@ __global__ void __launch_bounds__(1024) norm_backward_general_kernel(NormBackwar
       float g = 1.f;
       if (column_gate) {
         g = gate_value(a.gate_act, to_f32(gate[c]));
-        const float dg = gate_slope(a.gate_act, g) * (a.alpha * G * (hf * inv * w));
-        if (a.gate_kind == MOE_GATE_ELEMENT) static_cast<T*>(b.d_gate)[t * a.H + c] = from_f32<T>(dg);
-        else s_acc[kSumGate][c] += dg;
+        if (a.gate_kind == MOE_GATE_ELEMENT)
+          static_cast<T*>(b.d_gate)[t * a.H + c] =
+              from_f32<T>(gate_slope(a.gate_act, g) * (a.alpha * G * (hf * inv * w)));
       }
       const float gG = scale * (g * G);
-      if (b.d_weight != nullptr) s_acc[kSumWeight][c] = fmaf(gG, hf * inv, s_acc[kSumWeight][c]);
+      if (wants(b, kSumBlock))
+        s_acc[kSumBlock][c] =
+            fmaf(gt * inv * (a.gate_kind == MOE_GATE_ELEMENT ? g : 1.f) * G, hf, s_acc[kSumBlock][c]);
       static_cast<T*>(b.dh)[t * a.H + c] = from_f32<T>(inv * (w * gG) - scale * (hf * back));
     }
   }
-  for (int which = 0; which < 3; ++which)
+  for (int which = 0; which < 2; ++which)
     if (wants(b, which))
       for (int c = threadIdx.x; c < a.H; c += blockDim.x) partial_row(b, which, blockIdx.x)[c] = s_acc[which][c];
 }
 
 // Column sums over the blocks' parts, in part order within each of 8 strands
-// that are then added in order. grid (columns / 32, 3).
+// that are then added in order, and the gradients that follow from them. grid
+// (columns / 32, 2).
 template <typename T>
 __global__ void __launch_bounds__(256) column_sum_kernel(NormBackwardArgs b, int parts) {
   __shared__ float s[8][32];
   pdl_wait();
   pdl_launch_dependents();
+  const NormArgs& a = b.f;
   const int which = blockIdx.y;
   if (!wants(b, which)) return;
   const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < b.f.H)
+  if (c < a.H) {
+#pragma unroll 8
     for (int p = strand; p < parts; p += 8) v += partial_row(b, which, p)[c];
+  }
   s[strand][lane] = v;
   __syncthreads();
-  if (strand != 0 || c >= b.f.H) return;
+  if (strand != 0 || c >= a.H) return;
 #pragma unroll
   for (int i = 1; i < 8; ++i) v += s[i][lane];
-  void* out = which == kSumWeight ? b.d_weight : which == kSumNext ? b.d_next_weight : b.d_gate;
-  if (which != kSumGate && b.f.weight_f32) static_cast<float*>(out)[c] = v;
-  else static_cast<T*>(out)[c] = from_f32<T>(v);
+  auto store_weight = [&](void* out, float d) {
+    if (a.weight_f32) static_cast<float*>(out)[c] = d;
+    else static_cast<T*>(out)[c] = from_f32<T>(d);
+  };
+  if (which == kSumNext) {
+    store_weight(b.d_next_weight, v);
+    return;
+  }
+  v *= a.alpha;
+  float gate = 1.f;
+  if (a.gate_kind == MOE_GATE_CHANNEL) {
+    float w[1];
+    load_weight<T, 1>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c, w);
+    gate = gate_value(a.gate_act, to_f32(static_cast<const T*>(a.gate)[c]));
+    static_cast<T*>(b.d_gate)[c] = from_f32<T>(gate_slope(a.gate_act, gate) * w[0] * v);
+  }
+  if (b.d_weight != nullptr) store_weight(b.d_weight, gate * v);
 }
 
-template <typename T, int CH, bool WARP>
-cudaError_t run(const NormBackwardArgs& b, int grid, int threads, cudaStream_t st) {
-  return launch_kernel(true, norm_backward_kernel<T, kVec<T>, CH, WARP>, grid, threads,
-                       WARP ? sizeof(float) * b.f.H : 0, st, b);
+template <typename T, int V, int CH, int STAGES, bool WARP>
+cudaError_t run(const NormBackwardArgs& b, int threads, int num_sms, cudaStream_t st, int* parts) {
+  const NormArgs& a = b.f;
+  auto* k = a.h == nullptr ? norm_backward_kernel<T, V, CH, STAGES, false, true, WARP>
+            : a.next       ? norm_backward_kernel<T, V, CH, STAGES, true, true, WARP>
+                           : norm_backward_kernel<T, V, CH, STAGES, true, false, WARP>;
+  const int arrays = (b.dr != nullptr) + 2 * (a.next != 0) + (a.h != nullptr) + (a.gate_kind == MOE_GATE_ELEMENT);
+  size_t smem = static_cast<size_t>(STAGES) * arrays * CH * threads * sizeof(Pack<T, V>);
+  if (WARP) smem = std::max(smem, sizeof(float) * a.H);
+  else if (STAGES > 0) smem += sizeof(float) * 2 * CH * V * threads;
+  int blocks = std::max(1, 1024 / threads);
+  if (smem > 0) blocks = std::max(1, std::min<int>(blocks, kQueueSmem / smem));
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  *parts = std::min(std::min(ceil_div(a.T, WARP ? threads / 32 : 1), blocks * num_sms), kNormParts);
+  return launch_kernel(true, k, *parts, threads, smem, st, b);
+}
+
+template <typename T>
+cudaError_t run_general(const NormBackwardArgs& b, int num_sms, cudaStream_t st, int* parts) {
+  const bool block = b.d_weight != nullptr || b.f.gate_kind == MOE_GATE_CHANNEL;
+  const size_t smem = sizeof(float) * (block + (b.d_next_weight != nullptr)) * b.f.H;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_backward_general_kernel<T>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  *parts = std::min(std::min(b.f.T, num_sms), kNormParts);
+  return launch_kernel(true, norm_backward_general_kernel<T>, *parts, 1024, smem, st, b);
 }
 
 }  // namespace
@@ -356,6 +447,7 @@ cudaError_t run(const NormBackwardArgs& b, int grid, int threads, cudaStream_t s
 cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& b, int num_sms, cudaStream_t st) {
   return with_dtype(dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
+    constexpr int V = kVec<T>;
     const NormArgs& a = b.f;
     const bool vec = rows_vectorize<T>(a.H,
                                        {b.dr, b.dy, a.h, a.r, a.weight, a.next_weight,
@@ -363,31 +455,27 @@ cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& b, int num_s
                                         a.gate_kind == MOE_GATE_ELEMENT ? b.d_gate : nullptr},
                                        {b.ld_dr, b.ld_dy, a.ld_h, b.ld_r,
                                         a.gate_kind == MOE_GATE_ELEMENT ? a.ld_gate : 0});
-    const int packs = a.H / kVec<T>;
-    const int most = std::min(kNormParts, 2 * num_sms);
+    const int packs = vec ? a.H / V : a.H;
+    auto threads = [&](int ch) { return ceil_div(ceil_div(packs, ch), 32) * 32; };
     int parts = 0;
     cudaError_t e = cudaSuccess;
     if (a.T == 0) {
+    } else if (vec && packs <= 32) {
+      e = run<T, V, 1, 2, true>(b, 256, num_sms, st, &parts);
     } else if (vec && packs <= 64) {
-      parts = std::min(ceil_div(a.T, 8), most);
-      e = run<T, 2, true>(b, parts, 256, st);
+      e = run<T, V, 2, 2, true>(b, 256, num_sms, st, &parts);
     } else if (vec && packs <= 1024) {
-      parts = std::min(a.T, most);
-      const int threads = ceil_div(packs <= 512 ? packs : ceil_div(packs, 2), 32) * 32;
-      e = packs <= 512 ? run<T, 1, false>(b, parts, threads, st) : run<T, 2, false>(b, parts, threads, st);
+      e = run<T, V, 1, 2, false>(b, threads(1), num_sms, st, &parts);
+    } else if (!vec && packs <= 4096) {
+      e = run<T, 1, 4, 0, false>(b, threads(4), num_sms, st, &parts);
+    } else if (vec && packs <= 2048 && sizeof(T) == 4) {
+      if constexpr (sizeof(T) == 4) e = run<T, V, 2, 0, false>(b, threads(2), num_sms, st, &parts);
     } else {
-      parts = std::min(a.T, std::min(num_sms, kNormParts));
-      const int arrays = (b.d_weight != nullptr) + (b.d_next_weight != nullptr) + (a.gate_kind == MOE_GATE_CHANNEL);
-      const size_t smem = sizeof(float) * arrays * a.H;
-      if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(norm_backward_general_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
-      if (e == cudaSuccess)
-        e = launch_kernel(true, norm_backward_general_kernel<T>, parts, 1024, smem, st, b);
+      e = run_general<T>(b, num_sms, st, &parts);
     }
     if (e != cudaSuccess) return e;
     if (b.d_weight == nullptr && b.d_next_weight == nullptr && a.gate_kind != MOE_GATE_CHANNEL) return e;
-    return launch_kernel(true, column_sum_kernel<T>, dim3(ceil_div(a.H, 32), 3), 256, 0, st, b, parts);
+    return launch_kernel(true, column_sum_kernel<T>, dim3(ceil_div(a.H, 32), 2), 256, 0, st, b, parts);
   });
 }
 

@@ -20,164 +20,221 @@ namespace {
 
 constexpr int kPermThreads = 256;
 constexpr int kPermWarps = kPermThreads / 32;
-constexpr int kKGroup = 8;    // rows of a token in flight together
-constexpr int kZeroRows = 32;  // rows that a zero-fill block looks after
+constexpr int kPermBlocks = 4;  // blocks per SM that the registers are held to
+// Packs of rows that a lane has in flight.
+template <int V>
+constexpr int kPacks = V == 1 ? 16 : 4;
 
-// Sums v[0..7] over the block; valid in thread 0..7 as the return value.
-__device__ __forceinline__ float block_sum8(const float (&v)[kKGroup], float (*s)[kPermWarps]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();  // the previous use of s
-#pragma unroll
-  for (int j = 0; j < kKGroup; ++j) {
-    const float t = warp_sum(v[j]);
-    if (lane == 0) s[j][warp] = t;
-  }
-  __syncthreads();
-  float r = 0.f;
-  if (threadIdx.x < kKGroup)
-    for (int w = 0; w < kPermWarps; ++w) r += s[threadIdx.x][w];
-  return r;
+// A block holds kPermWarps / wpt tokens; the wpt warps of a token take turns
+// along its columns. A lane has KB experts of the token by U
+// packs of columns in flight.
+struct Where {
+  int64_t t;
+  int warp_in_token, token_in_block;
+};
+__device__ __forceinline__ Where locate(int wpt) {
+  const int warp = threadIdx.x >> 5;
+  return {static_cast<int64_t>(blockIdx.x) * (kPermWarps / wpt) + warp / wpt, warp % wpt, warp / wpt};
 }
 
-// grid (T + ceil(M / 32), column splits); the last blocks zero the rows that
-// belong to no slot.
-template <typename T, int V, bool W, bool DOTS>
-__global__ void __launch_bounds__(kPermThreads)
-place_kernel(PlaceArgs a) {
+// Sums the dots of KT rows over the warps of a token and stores them.
+template <int KT>
+__device__ __forceinline__ void store_dots(float (&dot)[KT], const Where& at, int wpt, bool live, float* dots, int K,
+                                           int k0, float (*s)[KT]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < KT; ++j) dot[j] = warp_sum(dot[j]);
+  if (wpt > 1) {
+    __syncthreads();
+    if (lane == 0) {
+#pragma unroll
+      for (int j = 0; j < KT; ++j) s[warp][j] = dot[j];
+    }
+    __syncthreads();
+    if (at.warp_in_token == 0) {
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+        for (int w = 1; w < wpt; ++w) dot[j] += s[warp + w][j];
+    }
+  }
+  if (live && at.warp_in_token == 0) {
+    float mine = 0.f;
+#pragma unroll
+    for (int j = 0; j < KT; ++j) mine = lane == j ? dot[j] : mine;
+    if (lane < KT && k0 + lane < K) dots[at.t * K + k0 + lane] = mine;
+  }
+}
+
+// rows null: the dots alone. grid ceil(T / tokens a block) + zero blocks: the
+// last blocks zero the rows that belong to no slot, 32 rows a warp.
+template <typename T, int V, int KB, int U, bool W, bool DOTS>
+__global__ void __launch_bounds__(kPermThreads, kPermBlocks) place_kernel(PlaceArgs a, int wpt, int token_blocks) {
+  __shared__ float s_dot[kPermWarps][KB];
   pdl_wait();
   pdl_launch_dependents();
-  const int H = a.H, K = a.p.K;
+  const int H = a.H, K = a.p.K, lane = threadIdx.x & 31;
   T* rows = static_cast<T*>(a.rows);
-  const int c0 = (blockIdx.y * kPermThreads + threadIdx.x) * V, cstep = gridDim.y * kPermThreads * V;
-  if (blockIdx.x >= a.p.T) {
-    const int r0 = (blockIdx.x - a.p.T) * kZeroRows;
+  if (static_cast<int>(blockIdx.x) >= token_blocks) {
+    const int r0 = (static_cast<int>(blockIdx.x) - token_blocks) * kPermWarps * 4 + (threadIdx.x >> 5) * 4;
     Pack<T, V> z;
 #pragma unroll
     for (int i = 0; i < V; ++i) z.e[i] = from_f32<T>(0.f);
-    for (int r = r0; r < min(r0 + kZeroRows, a.p.M); ++r) {
+    for (int r = r0; r < min(r0 + 4, a.p.M); ++r) {
       if (a.p.row_slot[r] >= 0) continue;
       T* dst = rows + static_cast<size_t>(r) * H;
-      for (int c = c0; c < H; c += cstep) store_pack(dst + c, z);
+      for (int c = lane * V; c < H; c += 32 * V) store_pack(dst + c, z);
     }
     return;
   }
-  const size_t t = blockIdx.x;
-  __shared__ int s_row[kMaxTopK];
-  __shared__ float s_w[kMaxTopK];
-  __shared__ float s_sum[kKGroup][kPermWarps];
-  if (threadIdx.x < K) {
-    s_row[threadIdx.x] = a.p.inv[t * K + threadIdx.x];
-    s_w[threadIdx.x] = W ? a.w[t * K + threadIdx.x] : 1.f;
+  const Where at = locate(wpt);
+  const bool live = at.t < a.p.T;
+  int my_row = -1;
+  float my_w = 0.f;
+  if (live && lane < K) {
+    my_row = a.p.inv[at.t * K + lane];
+    if (W) my_w = a.w[at.t * K + lane];
   }
-  __syncthreads();
-  const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
+  const T* x = static_cast<const T*>(a.x) + at.t * a.ld_x;
   const T* other = static_cast<const T*>(a.other);
-  for (int k0 = 0; k0 < K; k0 += kKGroup) {
-    float dot[kKGroup] = {};
-    for (int c = c0; c < H; c += cstep) {
-      const Pack<T, V> xp = load_pack<V>(x + c);
-      float xf[V];
-      if (W || DOTS) unpack(xp, xf);
-      Pack<T, V> op[kKGroup];
-      if (DOTS) {
+  for (int k0 = 0; k0 < K; k0 += KB) {
+    int row[KB];
+    float w[KB], dot[KB] = {};
 #pragma unroll
-        for (int j = 0; j < kKGroup; ++j)
-          if (k0 + j < K && s_row[k0 + j] >= 0)
-            op[j] = load_pack<V>(other + static_cast<size_t>(s_row[k0 + j]) * a.ld_other + c);
-      }
+    for (int j = 0; j < KB; ++j) {
+      row[j] = __shfl_sync(0xffffffffu, my_row, k0 + j);
+      if (k0 + j >= K) row[j] = -1;
+      w[j] = W ? __shfl_sync(0xffffffffu, my_w, k0 + j) : 1.f;
+    }
+    const int first = (at.warp_in_token * 32 * U + lane) * V, step = wpt * 32 * U * V;
+    for (int c = live ? first : H; c < H; c += step) {
+      Pack<T, V> xp[U], op[U][KB];
 #pragma unroll
-      for (int j = 0; j < kKGroup; ++j) {
-        if (k0 + j >= K || s_row[k0 + j] < 0) continue;
-        T* dst = rows + static_cast<size_t>(s_row[k0 + j]) * H + c;
-        if (W) {
-          float o[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = s_w[k0 + j] * xf[i];
-          store_pack(dst, pack<T, V>(o));
-        } else {
-          store_pack(dst, xp);
-        }
+      for (int u = 0; u < U; ++u) {
+        const int cu = c + u * 32 * V;
+        if (cu >= H) continue;
+        xp[u] = load_pack<V>(x + cu);
         if (DOTS) {
-          float of[V];
-          unpack(op[j], of);
 #pragma unroll
-          for (int i = 0; i < V; ++i) dot[j] = fmaf(xf[i], of[i], dot[j]);
+          for (int j = 0; j < KB; ++j)
+            if (row[j] >= 0) op[u][j] = load_pack<V>(other + static_cast<int64_t>(row[j]) * a.ld_other + cu);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int cu = c + u * 32 * V;
+        if (cu >= H) continue;
+        float xf[V];
+        if (W || DOTS) unpack(xp[u], xf);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (row[j] < 0) continue;
+          if (!DOTS || rows != nullptr) {
+            T* dst = rows + static_cast<int64_t>(row[j]) * H + cu;
+            if (W) {
+              float o[V];
+#pragma unroll
+              for (int i = 0; i < V; ++i) o[i] = w[j] * xf[i];
+              store_pack(dst, pack<T, V>(o));
+            } else {
+              store_pack(dst, xp[u]);
+            }
+          }
+          if (DOTS) {
+            float of[V];
+            unpack(op[u][j], of);
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[j] = fmaf(xf[i], of[i], dot[j]);
+          }
         }
       }
     }
-    if (DOTS) {
-      const float d = block_sum8(dot, s_sum);
-      if (threadIdx.x < kKGroup && k0 + threadIdx.x < K) a.dots[t * K + k0 + threadIdx.x] = d;
-    }
+    if (DOTS) store_dots<KB>(dot, at, wpt, live, a.dots, K, k0, s_dot);
   }
 }
 
-// grid (T, column splits)
-template <typename T, int V, bool W, bool DOTS>
-__global__ void __launch_bounds__(kPermThreads)
-gather_kernel(GatherArgs a) {
+// With DOTS, K <= KT (the dots ride along with the one pass over the rows);
+// without, KT = KB and any K.
+template <typename T, int V, int KT, int KB, int U, bool W, bool DOTS>
+__global__ void __launch_bounds__(kPermThreads, kPermBlocks) gather_kernel(GatherArgs a, int wpt) {
+  __shared__ float s_dot[kPermWarps][KT];
   pdl_wait();
   pdl_launch_dependents();
-  const int H = a.H, K = a.p.K;
-  const size_t t = blockIdx.x;
-  __shared__ int s_row[kMaxTopK];
-  __shared__ float s_w[kMaxTopK];
-  __shared__ float s_sum[kKGroup][kPermWarps];
-  if (threadIdx.x < K) {
-    s_row[threadIdx.x] = a.p.inv[t * K + threadIdx.x];
-    s_w[threadIdx.x] = W ? a.w[t * K + threadIdx.x] : 1.f;
+  const int H = a.H, K = a.p.K, lane = threadIdx.x & 31;
+  const Where at = locate(wpt);
+  const bool live = at.t < a.p.T;
+  int my_row = -1;
+  float my_w = 0.f;
+  if (live && lane < K) {
+    my_row = a.p.inv[at.t * K + lane];
+    if (W) my_w = a.w[at.t * K + lane];
   }
-  __syncthreads();
   const T* rows = static_cast<const T*>(a.rows);
-  const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
-  T* out = static_cast<T*>(a.out) + t * H;
-  const int c0 = (blockIdx.y * kPermThreads + threadIdx.x) * V, cstep = gridDim.y * kPermThreads * V;
-  // the columns of a block: all of them with dots (one block per token then)
-  float dots[DOTS ? kMaxTopK : 1] = {};
-  for (int c = c0; c < H; c += cstep) {
-    float acc[V] = {};
-    float xf[V];
-    if (DOTS) unpack(load_pack<V>(x + c), xf);
+  const T* x = static_cast<const T*>(a.x) + at.t * a.ld_x;
+  T* out = static_cast<T*>(a.out) + at.t * H;
+  float dot[KT] = {};
+  const int first = at.warp_in_token * 32 * U * V, step = wpt * 32 * U * V;
+  // (all lanes of a warp take the same number of steps: the shuffles need them)
+  for (int c0 = live ? first : H; c0 < H; c0 += step) {
+    const int c = c0 + lane * V;
+    float acc[U][V] = {}, xf[U][V];
+    auto add = [&](int k0, float* d) {  // KB experts from k0 on
+      int row[KB];
+      float w[KB];
 #pragma unroll
-    for (int k0 = 0; k0 < kMaxTopK; k0 += kKGroup) {
-      if (k0 >= K) break;
-      Pack<T, V> rp[kKGroup];
+      for (int j = 0; j < KB; ++j) {
+        row[j] = __shfl_sync(0xffffffffu, my_row, k0 + j);
+        if (k0 + j >= K) row[j] = -1;
+        w[j] = W ? __shfl_sync(0xffffffffu, my_w, k0 + j) : 1.f;
+      }
+      Pack<T, V> rp[U][KB];
 #pragma unroll
-      for (int j = 0; j < kKGroup; ++j)
-        if (k0 + j < K && s_row[k0 + j] >= 0)
-          rp[j] = load_pack<V>(rows + static_cast<size_t>(s_row[k0 + j]) * a.ld_rows + c);
+      for (int u = 0; u < U; ++u) {
+        const int cu = c + u * 32 * V;
 #pragma unroll
-      for (int j = 0; j < kKGroup; ++j) {
-        if (k0 + j >= K || s_row[k0 + j] < 0) continue;
-        float rf[V];
-        unpack(rp[j], rf);
+        for (int j = 0; j < KB; ++j)
+          if (row[j] >= 0 && cu < H) rp[u][j] = load_pack<V>(rows + static_cast<int64_t>(row[j]) * a.ld_rows + cu);
+      }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          acc[i] = W ? fmaf(s_w[k0 + j], rf[i], acc[i]) : acc[i] + rf[i];
-          if (DOTS) dots[k0 + j] = fmaf(xf[i], rf[i], dots[k0 + j]);
+      for (int u = 0; u < U; ++u) {
+        if (c + u * 32 * V >= H) continue;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (row[j] < 0) continue;
+          float rf[V];
+          unpack(rp[u][j], rf);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            acc[u][i] = W ? fmaf(w[j], rf[i], acc[u][i]) : acc[u][i] + rf[i];
+            if (DOTS) d[j] = fmaf(xf[u][i], rf[i], d[j]);
+          }
         }
       }
-    }
-    store_pack(out + c, pack<T, V>(acc));
-  }
-  if (DOTS) {
+    };
+    if constexpr (DOTS) {
 #pragma unroll
-    for (int k0 = 0; k0 < kMaxTopK; k0 += kKGroup) {
-      if (k0 >= K) break;
-      float v[kKGroup];
+      for (int u = 0; u < U; ++u)
+        if (c + u * 32 * V < H) unpack(load_pack<V>(x + c + u * 32 * V), xf[u]);
 #pragma unroll
-      for (int j = 0; j < kKGroup; ++j) v[j] = dots[DOTS ? k0 + j : 0];
-      const float d = block_sum8(v, s_sum);
-      if (threadIdx.x < kKGroup && k0 + threadIdx.x < K) a.dots[t * K + k0 + threadIdx.x] = d;
+      for (int k0 = 0; k0 < KT; k0 += KB)
+        if (k0 < K) add(k0, dot + k0);
+    } else {
+      for (int k0 = 0; k0 < K; k0 += KB) add(k0, nullptr);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int cu = c + u * 32 * V;
+      if (cu < H) store_pack(out + cu, pack<T, V>(acc[u]));
     }
   }
+  if (DOTS) store_dots<KT>(dot, at, wpt, live, a.dots, K, 0, s_dot);
 }
 
-// Column splits of a token's row: more blocks where the tokens alone do not
-// fill the GPU (a handful of tokens at decode).
-int column_splits(int T, int H, int V) {
-  const int full = ceil_div(H, kPermThreads * V);
-  return T >= 512 ? 1 : full;
+// Warps per token: one where the tokens alone give every SM its warps, more
+// (up to a block) for few tokens, as far as the row has work for them.
+int warps_per_token(int T, int H, int V) {
+  int wpt = 1;
+  while (wpt < kPermWarps && T * wpt < 152 * 128 && H > wpt * 32 * V) wpt *= 2;
+  return wpt;
 }
 
 template <typename T>
@@ -190,25 +247,48 @@ bool vec_ok(int H, std::initializer_list<const void*> ptrs, std::initializer_lis
   return true;
 }
 
-template <typename T, int V>
+template <typename T, int V, int KB, int U, bool W, bool DOTS>
 cudaError_t place(const PlaceArgs& a, cudaStream_t st) {
-  const int zero_blocks = ceil_div(a.p.M, kZeroRows);
-  const bool dots = a.dots != nullptr;
-  const dim3 grid(a.p.T + zero_blocks, dots ? 1 : column_splits(a.p.T, a.H, V));
-  auto* k = a.w == nullptr ? place_kernel<T, V, false, false>
-            : dots         ? place_kernel<T, V, true, true>
-                           : place_kernel<T, V, true, false>;
-  return launch_kernel(true, k, grid, kPermThreads, 0, st, a);
+  const int wpt = warps_per_token(a.p.T, a.H, V);
+  const int token_blocks = ceil_div(a.p.T, kPermWarps / wpt);
+  const int zero_blocks = a.rows != nullptr ? ceil_div(a.p.M, kPermWarps * 4) : 0;
+  return launch_kernel(true, place_kernel<T, V, KB, U, W, DOTS>, token_blocks + zero_blocks, kPermThreads, 0, st, a,
+                       wpt, token_blocks);
+}
+
+template <typename T, int V, int KT>
+cudaError_t gather(const GatherArgs& a, cudaStream_t st) {
+  constexpr int KB = KT < 4 ? KT : 4, U = kPacks<V> / KB;
+  const int wpt = warps_per_token(a.p.T, a.H, V);
+  auto* k = a.w == nullptr        ? gather_kernel<T, V, KB, KB, U, false, false>
+            : a.dots != nullptr ? gather_kernel<T, V, KT, KB, U, true, true>
+                                : gather_kernel<T, V, KB, KB, U, true, false>;
+  return launch_kernel(true, k, ceil_div(a.p.T, kPermWarps / wpt), kPermThreads, 0, st, a, wpt);
+}
+
+// Without dots only the token's own row is loaded: all its experts at a time.
+template <typename T, int V>
+cudaError_t place_k(const PlaceArgs& a, cudaStream_t st) {
+  if (a.dots != nullptr)
+    return a.p.K <= 2 ? place<T, V, 2, kPacks<V> / 2, true, true>(a, st)
+                      : place<T, V, 4, kPacks<V> / 4, true, true>(a, st);
+  if (a.w != nullptr) return place<T, V, 8, kPacks<V>, true, false>(a, st);
+  return place<T, V, 8, kPacks<V>, false, false>(a, st);
 }
 
 template <typename T, int V>
-cudaError_t gather(const GatherArgs& a, cudaStream_t st) {
-  const bool dots = a.dots != nullptr;
-  const dim3 grid(a.p.T, dots ? 1 : column_splits(a.p.T, a.H, V));
-  auto* k = a.w == nullptr ? gather_kernel<T, V, false, false>
-            : dots         ? gather_kernel<T, V, true, true>
-                           : gather_kernel<T, V, true, false>;
-  return launch_kernel(true, k, grid, kPermThreads, 0, st, a);
+cudaError_t gather_k(const GatherArgs& a, cudaStream_t st) {
+  if (a.dots != nullptr && a.p.K > 8) {
+    // the sums and the dots of many experts do not fit one pass's registers
+    GatherArgs sums = a;
+    sums.dots = nullptr;
+    const cudaError_t e = gather<T, V, 4>(sums, st);
+    if (e != cudaSuccess) return e;
+    return place_k<T, V>({a.x, a.ld_x, a.rows, a.ld_rows, a.w, nullptr, a.dots, a.H, a.p}, st);
+  }
+  if (a.p.K <= 2) return gather<T, V, 2>(a, st);
+  if (a.p.K <= 4 || a.dots == nullptr) return gather<T, V, 4>(a, st);
+  return gather<T, V, 8>(a, st);
 }
 
 }  // namespace
@@ -216,16 +296,16 @@ cudaError_t gather(const GatherArgs& a, cudaStream_t st) {
 cudaError_t launch_place(int dtype, const PlaceArgs& a, cudaStream_t st) {
   return with_dtype(dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
-    return vec_ok<T>(a.H, {a.x, a.other, a.rows}, {a.ld_x, a.ld_other}) ? place<T, kVec<T>>(a, st)
-                                                                        : place<T, 1>(a, st);
+    return vec_ok<T>(a.H, {a.x, a.other, a.rows}, {a.ld_x, a.ld_other}) ? place_k<T, kVec<T>>(a, st)
+                                                                        : place_k<T, 1>(a, st);
   });
 }
 
 cudaError_t launch_gather(int dtype, const GatherArgs& a, cudaStream_t st) {
   return with_dtype(dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
-    return vec_ok<T>(a.H, {a.rows, a.x, a.out}, {a.ld_rows, a.ld_x}) ? gather<T, kVec<T>>(a, st)
-                                                                     : gather<T, 1>(a, st);
+    return vec_ok<T>(a.H, {a.rows, a.x, a.out}, {a.ld_rows, a.ld_x}) ? gather_k<T, kVec<T>>(a, st)
+                                                                     : gather_k<T, 1>(a, st);
   });
 }
 
