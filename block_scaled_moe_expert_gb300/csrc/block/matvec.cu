@@ -35,9 +35,8 @@ constexpr int kMvWarps = 16;
 constexpr int kMvThreads = kMvWarps * 32;
 constexpr int kMvRows = 16;    // weight rows of a block (the instruction's M)
 constexpr int kMvStep = 128;   // k of a block
-constexpr int kMvDepth = 4;    // blocks in flight per warp
 constexpr int kMvTokens = 16;  // tokens of a pass, two N = 8 tiles
-constexpr int kMvMaxSmem = 184 * 1024;  // for x
+constexpr int kMvMaxSmem = 227 * 1024 - 18 * 1024;  // for x and the blocks in flight, beside the sums' join
 constexpr int kMvMaxCluster = 8;
 template <typename X>
 constexpr bool kScaledX = std::is_same<X, __nv_bfloat16>::value;
@@ -70,12 +69,12 @@ struct MvArgs {
   bool x_vec;  // rows of x allow 16-byte loads
 };
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
   asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The eight e2m1 codes of a word as fp16 pairs, in order.
@@ -120,32 +119,44 @@ __device__ __forceinline__ void int4_pairs(uint32_t word, __half2 zero, uint32_t
   }
 }
 
-// What a warp holds of one block.
+// What a lane holds of one block.
 template <int SW>
 struct Block {
   uint4 codes[2];
   uint32_t scale[SW];
 };
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// A block's way from global memory through a warp's ring.
+template <int BYTES>
+__device__ __forceinline__ void fetch_block(uint8_t* slot, const uint8_t* p, int lane) {
+  cp_async16(slot + lane * 16, p + lane * 16);
+  cp_async16(slot + 512 + lane * 16, p + 512 + lane * 16);
+  if (lane < (BYTES - kCodeBytes) / 16) cp_async16(slot + kCodeBytes + lane * 16, p + kCodeBytes + lane * 16);
+}
 template <int SW>
-__device__ __forceinline__ void load_block(Block<SW>& b, const uint8_t* p, int lane) {
-  b.codes[0] = __ldcs(reinterpret_cast<const uint4*>(p) + lane);
-  b.codes[1] = __ldcs(reinterpret_cast<const uint4*>(p) + 32 + lane);
-  const uint8_t* s = p + kCodeBytes + (lane >> 2) * (4 * SW);
+__device__ __forceinline__ void read_block(Block<SW>& b, const uint8_t* slot, int lane) {
+  b.codes[0] = *reinterpret_cast<const uint4*>(slot + lane * 16);
+  b.codes[1] = *reinterpret_cast<const uint4*>(slot + 512 + lane * 16);
+  const uint8_t* s = slot + kCodeBytes + (lane >> 2) * (4 * SW);
 #pragma unroll
   for (int i = 0; i < SW; i += 2) {
-    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(s) + i / 2);
+    const uint2 v = *reinterpret_cast<const uint2*>(s + 4 * i);
     b.scale[i] = v.x;
     b.scale[i + 1] = v.y;
   }
 }
 
-// acc += block x tokens. GROUPS: scale groups per block (4, 2 or 1). xs: the
-// tokens' rows at the block's k, x_scale: their powers for this block.
+// acc += block x tokens. GROUPS: scale groups per block (4, 2 or 1). xs: this
+// lane's part of its token's row at the block's k, x_scale: the tokens' powers
+// for this block.
 template <int FMT, int GROUPS, int NT, typename S, typename X, int SW>
-__device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<SW>& b, const uint8_t* xs,
-                                               int x_stride, const float* x_scale, int T, int lane) {
-  const int g = lane >> 2, q = lane & 3;
+__device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<SW>& b,
+                                               const uint8_t* const (&xs)[NT], const float* x_scale, int lane) {
+  const int q = lane & 3;
   float scale[2][4];
   if constexpr (FMT == MOE_Q_FP4) {
     ue8m0_scales(b.scale[0], scale[0]);
@@ -162,8 +173,7 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
     uint4 xv[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      xv[n] = (n * 8 + g < T) ? *reinterpret_cast<const uint4*>(xs + (n * 8 + g) * x_stride + i * 64 + q * 16)
-                              : make_uint4(0, 0, 0, 0);
+      xv[n] = *reinterpret_cast<const uint4*>(xs[n] + i * 64);
     const uint32_t w0 = (i & 1) ? b.codes[i >> 1].z : b.codes[i >> 1].x;
     const uint32_t w1 = (i & 1) ? b.codes[i >> 1].w : b.codes[i >> 1].y;
     const bool first = (i * GROUPS) % 4 == 0, last = ((i + 1) * GROUPS) % 4 == 0;
@@ -185,9 +195,9 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (first) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-      mma_16816(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y);
-      mma_16816(c[n], a0[2], a1[2], a0[3], a1[3], xv[n].z, xv[n].w);
+      if (first) mma_16816(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y, 0.f, 0.f, 0.f, 0.f);
+      else mma_16816(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y, c[n][0], c[n][1], c[n][2], c[n][3]);
+      mma_16816(c[n], a0[2], a1[2], a0[3], a1[3], xv[n].z, xv[n].w, c[n][0], c[n][1], c[n][2], c[n][3]);
       if (last) {
         if constexpr (kScaledX<X>) {
           c[n][0] *= back[n].x;
@@ -235,120 +245,160 @@ __device__ __forceinline__ void store_tile(const MvArgs& a, int tile, const floa
 
 // Tiles are dealt round by round to groups of warps_k warps; the warps of a
 // group (and the CTAs of a cluster, one tile each then) share the tile's K
-// range in order and their sums are added in that order.
-template <int FMT, int GROUPS, int NT, typename S, typename X>
+// range in order and their sums are added in that order. DEPTH: blocks that a
+// warp has in flight or in work.
+template <int FMT, int GROUPS, int NT, int DEPTH, typename S, typename X>
 __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   constexpr int SW = FMT == MOE_Q_FP4 ? 2 : 2 * GROUPS;
-  extern __shared__ __align__(16) uint8_t s_x[];
-  __shared__ float s_red[2][kMvWarps][NT][4][32];
+  constexpr int BYTES = block_bytes(FMT, kMvStep / GROUPS);
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  __shared__ float s_red[kMvWarps][NT][4][32];
+  __shared__ __align__(16) uint8_t s_zero[kMvStep * 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int first_step = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.cluster);
   const int cta_steps = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.cluster) - first_step;
   const int wk = warp % a.warps_k, group = warp / a.warps_k, groups = kMvWarps / a.warps_k;
   const int s0 = cta_steps * wk / a.warps_k, ns = cta_steps * (wk + 1) / a.warps_k - s0;
-  const int bytes = block_bytes(FMT, kMvStep / GROUPS);
   const int cluster_id = blockIdx.x / a.cluster, clusters = gridDim.x / a.cluster;
   const int tile0 = cluster_id * groups + group, tile_step = clusters * groups;
   const int rounds = (a.tiles - cluster_id * groups + tile_step - 1) / tile_step;  // of this CTA
+  uint8_t* ring = s_dyn + warp * (DEPTH * BYTES);
+  uint8_t* s_x = s_dyn + kMvWarps * DEPTH * BYTES;
   pdl_wait();
   pdl_launch_dependents();
 
-  Block<SW> ring[kMvDepth];
-  // cursor of the next block to load
-  int ld_tile = tile0, ld_s = 0;
-  auto advance = [&](Block<SW>& slot) {
-    if (ld_tile < a.tiles) {
-      load_block(slot, a.prepared + (static_cast<size_t>(ld_tile) * a.steps + first_step + s0 + ld_s) * bytes, lane);
-      if (++ld_s == ns) {
-        ld_s = 0;
-        ld_tile += tile_step;
+  // the next block to fetch, and its slot
+  int f_tile = tile0, f_s = 0, f_slot = 0;
+  const uint8_t* f_at = a.prepared + (static_cast<size_t>(tile0) * a.steps + first_step + s0) * BYTES;
+  const size_t tile_bytes = static_cast<size_t>(a.steps) * BYTES;
+  auto fetch = [&]() {
+    if (f_tile < a.tiles) {
+      fetch_block<BYTES>(ring + f_slot, f_at, lane);
+      f_at += BYTES;
+      if (++f_s == ns) {
+        f_s = 0;
+        f_tile += tile_step;
+        f_at += tile_step * tile_bytes - static_cast<size_t>(ns) * BYTES;
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    f_slot = f_slot + BYTES == DEPTH * BYTES ? 0 : f_slot + BYTES;
   };
 #pragma unroll
-  for (int d = 0; d < kMvDepth; ++d) advance(ring[d]);
+  for (int d = 0; d < DEPTH - 1; ++d) fetch();
 
   // x: this CTA's K range as fp16, rows 64 bytes apart modulo 128 (the four
   // 16-byte reads of two tokens fill the banks), then the powers [step][token]
   const int x_stride = cta_steps * kMvStep * 2 + 64;
   float* s_power = reinterpret_cast<float*>(s_x + static_cast<size_t>(a.T) * x_stride);
   const X* x = static_cast<const X*>(a.x);
-  for (int unit = tid >> 4; unit < a.T * cta_steps; unit += kMvThreads / 16) {
-    const int t = unit / cta_steps, step = unit - t * cta_steps;
-    const int at = step * kMvStep + (lane & 15) * 8, k = first_step * kMvStep + at;
-    Pack<X, 8> p;
-    if (a.x_vec && k < a.K) {
-      p = load_pack<8>(x + t * a.ld_x + k);
-    } else {
+  constexpr int kAhead = 8;  // loads in flight
+  for (int unit0 = tid >> 4; unit0 < a.T * cta_steps; unit0 += kAhead * (kMvThreads / 16)) {
+    Pack<X, 8> p[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p.e[i] = k < a.K ? x[t * a.ld_x + k + i] : from_f32<X>(0.f);
-    }
-    uint4 out;
-    if constexpr (kScaledX<X>) {
-      float f[8], m = 0.f;
-      unpack(p, f);
+    for (int j = 0; j < kAhead; ++j) {
+      const int unit = unit0 + j * (kMvThreads / 16);
+      if (unit >= a.T * cta_steps) continue;
+      const int t = unit / cta_steps, k = (first_step + unit - t * cta_steps) * kMvStep + (lane & 15) * 8;
+      if (a.x_vec && k < a.K) {
+        p[j] = load_pack<8>(x + t * a.ld_x + k);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fabsf(f[i]) < INFINITY ? fmaxf(m, fabsf(f[i])) : m;
-      const unsigned half = 0xFFFFu << (lane & 16);  // the units of a warp end apart
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
-      // 2^(14 - e) and back, e the exponent of m (at least -112: both are normal)
-      const int e = max(15, static_cast<int>(__float_as_uint(m) >> 23));
-      const float scale = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-      uint32_t* w = &out.x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(f[2 * i] * scale, f[2 * i + 1] * scale);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int i = 0; i < 8; ++i) p[j].e[i] = k < a.K ? x[t * a.ld_x + k + i] : from_f32<X>(0.f);
       }
-      if ((lane & 15) == 0) s_power[step * kMvTokens + t] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-    } else {
-      out = *reinterpret_cast<const uint4*>(&p);
     }
-    *reinterpret_cast<uint4*>(s_x + static_cast<size_t>(t) * x_stride + at * 2) = out;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int unit = unit0 + j * (kMvThreads / 16);
+      if (unit >= a.T * cta_steps) continue;
+      const int t = unit / cta_steps, step = unit - t * cta_steps;
+      uint4 out;
+      if constexpr (kScaledX<X>) {
+        float f[8], m = 0.f;
+        unpack(p[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fabsf(f[i]) < INFINITY ? fmaxf(m, fabsf(f[i])) : m;
+        const unsigned half = 0xFFFFu << (lane & 16);  // the units of a warp end apart
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
+        // 2^(14 - e) and back, e the exponent of m (at least -112: both are normal)
+        const int e = max(15, static_cast<int>(__float_as_uint(m) >> 23));
+        const float scale = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+        uint32_t* w = &out.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 h = __floats2half2_rn(f[2 * i] * scale, f[2 * i + 1] * scale);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if ((lane & 15) == 0) s_power[step * kMvTokens + t] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+      } else {
+        out = *reinterpret_cast<const uint4*>(&p[j]);
+      }
+      *reinterpret_cast<uint4*>(s_x + static_cast<size_t>(t) * x_stride + step * (kMvStep * 2) + (lane & 15) * 16) = out;
+    }
   }
+  // what the lanes of absent tokens read, at every step
+  if (tid < kMvStep * 2 / 16) reinterpret_cast<uint4*>(s_zero)[tid] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
-  const uint8_t* xs = s_x + s0 * (kMvStep * 2);
+  const uint8_t* xs[NT];  // this lane's token (in each N tile) at the warp's first block
+  int xs_step[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = n * 8 + (lane >> 2);
+    xs[n] = (t < a.T ? s_x + t * x_stride + s0 * (kMvStep * 2) : s_zero) + (lane & 3) * 16;
+    xs_step[n] = t < a.T ? kMvStep * 2 : 0;
+  }
   const float* xp = s_power + s0 * kMvTokens;
   float acc[NT][4] = {};
-  int tile = tile0, s = 0;
-  int parity = 0;
-  auto finish = [&]() {  // the tile's sums are complete in this warp
-    if (a.warps_k > 1) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s_red[parity][warp][n][i][lane] = acc[n][i];
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.warps_k * 32) : "memory");
-      if (wk == 0) {
-        for (int w = 1; w < a.warps_k; ++w)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] += s_red[parity][warp + w][n][i][lane];
-      }
-      parity ^= 1;
-    }
-    if (wk == 0 && a.cluster == 1 && tile < a.tiles) store_tile<X, NT>(a, tile, acc, lane);
+  int at_slot = 0;
+  auto multiply = [&](const uint8_t* const (&x_at)[NT], const float* p_at) {  // the next block of the ring
+    __syncwarp();  // every lane is done with the slot that is fetched into
+    fetch();
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    __syncwarp();  // every lane's share has arrived
+    Block<SW> b;
+    read_block(b, ring + at_slot, lane);
+    multiply_block<FMT, GROUPS, NT, S, X>(acc, b, x_at, p_at, lane);
+    at_slot = at_slot + BYTES == DEPTH * BYTES ? 0 : at_slot + BYTES;
   };
-  if (a.cluster > 1) {
-    // one tile: the whole CTA shares it
-    for (int i = 0; i < ns; i += kMvDepth) {
+  auto walk = [&]() {  // a tile's blocks of this warp
+    const uint8_t* x_at[NT];
 #pragma unroll
-      for (int d = 0; d < kMvDepth; ++d) {
-        if (i + d >= ns) break;
-        multiply_block<FMT, GROUPS, NT, S, X>(acc, ring[d], xs + (i + d) * (kMvStep * 2), x_stride,
-                                                xp + (i + d) * kMvTokens, a.T, lane);
-        advance(ring[d]);
-      }
+    for (int n = 0; n < NT; ++n) x_at[n] = xs[n];
+    const float* p_at = xp;
+    for (int s = 0; s < ns; ++s) {
+      multiply(x_at, p_at);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x_at[n] += xs_step[n];
+      p_at += kMvTokens;
     }
-    finish();
+  };
+  auto join = [&]() {  // the sums of the group's warps, in its first one
+    if (a.warps_k == 1) return;
+    const int bar = 1 + group, threads = a.warps_k * 32;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");  // the join before is read
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_red[warp][n][i][lane] = acc[n][i];
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+    if (wk == 0) {
+      for (int w = 1; w < a.warps_k; ++w)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] += s_red[warp + w][n][i][lane];
+    }
+  };
+  if (a.cluster > 1) {  // one tile, which the whole CTA shares
+    walk();
+    join();
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();  // rank 0 runs, and is done with its own sums
     if (warp == 0) {
-      float* to = cluster.map_shared_rank(&s_red[1][0][0][0][0], 0) + rank * (NT * 128);
+      float* to = cluster.map_shared_rank(&s_red[0][0][0][0], 0) + rank * (NT * 128);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -360,28 +410,17 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] += (&s_red[1][0][0][0][0])[r * (NT * 128) + (n * 4 + i) * 32 + lane];
-      store_tile<X, NT>(a, tile, acc, lane);
+          for (int i = 0; i < 4; ++i) acc[n][i] += (&s_red[0][0][0][0])[r * (NT * 128) + (n * 4 + i) * 32 + lane];
+      store_tile<X, NT>(a, tile0, acc, lane);
     }
     return;
   }
-  const int total = rounds * ns;
-  for (int i = 0; i < total; i += kMvDepth) {
+  for (int r = 0, tile = tile0; r < rounds; ++r, tile += tile_step) {
+    if (tile < a.tiles) walk();
+    join();
+    if (wk == 0 && tile < a.tiles) store_tile<X, NT>(a, tile, acc, lane);
 #pragma unroll
-    for (int d = 0; d < kMvDepth; ++d) {
-      if (i + d >= total) break;
-      if (tile < a.tiles)
-        multiply_block<FMT, GROUPS, NT, S, X>(acc, ring[d], xs + s * (kMvStep * 2), x_stride, xp + s * kMvTokens,
-                                                a.T, lane);
-      advance(ring[d]);
-      if (++s == ns) {
-        finish();
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-        s = 0;
-        tile += tile_step;
-      }
-    }
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
   }
 }
 
@@ -446,13 +485,18 @@ matvec_prepare_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
 
 int row_tiles(const MatvecShape& s) { return s.swiglu ? ceil_div(s.N / 2, 8) : ceil_div(s.N, kMvRows); }
 
-template <int FMT, int GROUPS, typename S, typename X>
-cudaError_t run(const MvArgs& a, int grid, size_t smem, cudaStream_t st) {
-  auto* k = a.T <= 8 ? matvec_kernel<FMT, GROUPS, 1, S, X> : matvec_kernel<FMT, GROUPS, 2, S, X>;
-  if (smem > 8 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+// Shared memory beside the ring: T tokens of x and their powers.
+size_t x_smem(const MvArgs& a) {
+  const size_t cta_steps = ceil_div(a.steps, a.cluster);
+  return a.T * (cta_steps * kMvStep * 2 + 64) + cta_steps * kMvTokens * 4;
+}
+
+template <int FMT, int GROUPS, int NT, int DEPTH, typename S, typename X>
+cudaError_t run(const MvArgs& a, int grid, cudaStream_t st) {
+  auto* k = matvec_kernel<FMT, GROUPS, NT, DEPTH, S, X>;
+  const size_t smem = kMvWarps * DEPTH * block_bytes(FMT, kMvStep / GROUPS) + x_smem(a);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = kMvThreads;
@@ -468,18 +512,39 @@ cudaError_t run(const MvArgs& a, int grid, size_t smem, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
+// As many tokens as fit beside a ring of at least 4 blocks in one pass, at most 16; 8 blocks where they fit.
+template <int FMT, int GROUPS, typename S, typename X>
+cudaError_t run_passes(MvArgs a, int T, int grid, cudaStream_t st) {
+  constexpr size_t ring = kMvWarps * block_bytes(FMT, kMvStep / GROUPS);
+  constexpr int kMost = 8, kLeast = 4;
+  a.T = std::min(T, kMvTokens);
+  while (a.T > 1 && kLeast * ring + x_smem(a) > kMvMaxSmem) --a.T;
+  const int pass = a.T;
+  const bool deep = kMost * ring + x_smem(a) <= kMvMaxSmem;
+  for (int t0 = 0; t0 < T; t0 += pass) {
+    a.T = std::min(pass, T - t0);
+    cudaError_t e;
+    if (a.T > 8) e = deep ? run<FMT, GROUPS, 2, kMost, S, X>(a, grid, st) : run<FMT, GROUPS, 2, kLeast, S, X>(a, grid, st);
+    else e = deep ? run<FMT, GROUPS, 1, kMost, S, X>(a, grid, st) : run<FMT, GROUPS, 1, kLeast, S, X>(a, grid, st);
+    if (e != cudaSuccess) return e;
+    a.x = static_cast<const X*>(a.x) + pass * a.ld_x;
+    a.y = static_cast<X*>(a.y) + static_cast<size_t>(pass) * a.out_cols;
+  }
+  return cudaSuccess;
+}
+
 template <int FMT, typename S, typename X>
-cudaError_t run_groups(int group, const MvArgs& a, int grid, size_t smem, cudaStream_t st) {
-  if (FMT == MOE_Q_FP4 || group == 32) return run<FMT, 4, S, X>(a, grid, smem, st);
-  if (group == 64) return run<FMT, FMT == MOE_Q_FP4 ? 4 : 2, S, X>(a, grid, smem, st);
-  return run<FMT, FMT == MOE_Q_FP4 ? 4 : 1, S, X>(a, grid, smem, st);
+cudaError_t run_groups(int group, const MvArgs& a, int T, int grid, cudaStream_t st) {
+  if (FMT == MOE_Q_FP4 || group == 32) return run_passes<FMT, 4, S, X>(a, T, grid, st);
+  if (group == 64) return run_passes<FMT, FMT == MOE_Q_FP4 ? 4 : 2, S, X>(a, T, grid, st);
+  return run_passes<FMT, FMT == MOE_Q_FP4 ? 4 : 1, S, X>(a, T, grid, st);
 }
 
 template <typename X>
-cudaError_t run_format(int fmt, int scale_dtype, int group, const MvArgs& a, int grid, size_t smem, cudaStream_t st) {
-  if (fmt == MOE_Q_FP4) return run_groups<MOE_Q_FP4, __half, X>(group, a, grid, smem, st);
-  if (scale_dtype == MOE_BF16) return run_groups<MOE_Q_INT4, __nv_bfloat16, X>(group, a, grid, smem, st);
-  return run_groups<MOE_Q_INT4, __half, X>(group, a, grid, smem, st);
+cudaError_t run_format(int fmt, int scale_dtype, int group, const MvArgs& a, int T, int grid, cudaStream_t st) {
+  if (fmt == MOE_Q_FP4) return run_groups<MOE_Q_FP4, __half, X>(group, a, T, grid, st);
+  if (scale_dtype == MOE_BF16) return run_groups<MOE_Q_INT4, __nv_bfloat16, X>(group, a, T, grid, st);
+  return run_groups<MOE_Q_INT4, __half, X>(group, a, T, grid, st);
 }
 
 }  // namespace
@@ -513,33 +578,31 @@ cudaError_t launch_matvec(const MatvecShape& s, float limit, int scale_dtype, co
   a.out_cols = s.swiglu ? s.N / 2 : s.N;
   a.limit = limit > 0.f && std::isfinite(limit) ? limit : 0.f;
   a.swiglu = s.swiglu != 0;
-  // K is shared by enough warps to give every SM a few rounds of tiles, and
-  // by the CTAs of a cluster where the tiles alone leave SMs idle.
+  // The warps that share a tile's K range: what makes the longest warp's way
+  // shortest, in blocks: its rounds of tiles, each its share of the K range and
+  // a join that costs about as much as a block and a half.
   a.cluster = 1;
   a.warps_k = 1;
-  while (a.warps_k < kMvWarps && a.tiles * a.warps_k < 4 * kMvWarps * num_sms && a.steps >= 4 * a.warps_k)
-    a.warps_k *= 2;
+  float best = INFINITY;
+  for (int wk = 1; wk <= kMvWarps && wk <= a.steps; wk *= 2) {
+    const float rounds = static_cast<float>(ceil_div(a.tiles, kMvWarps / wk * num_sms));
+    const float cost = rounds * (ceil_div(a.steps, wk) + (wk > 1 ? 1.5f : 0.f));
+    if (cost < best) {
+      best = cost;
+      a.warps_k = wk;
+    }
+  }
+  // and the CTAs of a cluster where the tiles alone leave SMs idle
   if (a.warps_k == kMvWarps)
     while (a.cluster < kMvMaxCluster && a.tiles * a.cluster * 2 <= num_sms && a.steps >= 2 * kMvWarps * a.cluster)
       a.cluster *= 2;
-  const int cta_k = ceil_div(a.steps, a.cluster) * kMvStep;
-  // of a token: fp16 and its place among the powers
-  const int x_row = 2 * cta_k + 64, power = cta_k / kMvStep * kMvTokens * 4;
-  const int pass = std::max(1, std::min<int>(kMvTokens, (kMvMaxSmem - power) / x_row));
   const int cta_tiles = ceil_div(a.tiles, kMvWarps / a.warps_k);
   const int grid = a.cluster > 1 ? a.tiles * a.cluster : std::min(cta_tiles, num_sms);
-  const size_t es = 2;
-  for (int t0 = 0; t0 < T; t0 += pass) {
-    a.T = std::min(pass, T - t0);
-    a.x_vec = aligned16(x) && ld_x % 8 == 0;
-    a.x = static_cast<const uint8_t*>(x) + static_cast<size_t>(t0) * ld_x * es;
-    a.y = static_cast<uint8_t*>(y) + static_cast<size_t>(t0) * a.out_cols * es;
-    const size_t smem = static_cast<size_t>(a.T) * x_row + power;
-    const cudaError_t e = dtype == MOE_BF16 ? run_format<__nv_bfloat16>(s.fmt, scale_dtype, s.group, a, grid, smem, st)
-                                            : run_format<__half>(s.fmt, scale_dtype, s.group, a, grid, smem, st);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  a.x = x;
+  a.y = y;
+  a.x_vec = aligned16(x) && ld_x % 8 == 0;
+  return dtype == MOE_BF16 ? run_format<__nv_bfloat16>(s.fmt, scale_dtype, s.group, a, T, grid, st)
+                           : run_format<__half>(s.fmt, scale_dtype, s.group, a, T, grid, st);
 }
 
 }  // namespace bsmoe
