@@ -30,14 +30,15 @@ __device__ __forceinline__ float* partial_row(const NormBackwardArgs& b, int whi
   return b.partials + (static_cast<size_t>(which) * kNormParts + part) * b.f.H;
 }
 
-template <typename T, int V, int CH, int STAGES, bool AFTER, bool NEXT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(NormBackwardArgs b) {
-  constexpr int ARRAYS = AFTER ? 5 : 3;
+// One row per warp (WARP) or per block. ELEMENT: a gate by element.
+template <typename T, int V, int CH, int STAGES, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 512) norm_backward_kernel(NormBackwardArgs b) {
+  constexpr int ARRAYS = AFTER ? ELEMENT ? 5 : 4 : 3;
   // the columns' factors stand in shared memory behind the ring (each thread
   // its own): beside the column sums they would not fit into the registers
   constexpr bool CACHED = STAGES > 0 && !WARP;
   extern __shared__ __align__(16) uint8_t s_ring[];
-  __shared__ __align__(16) float s_sum[2][2][2][32];
+  __shared__ float s_sum[2][2][2][32];
   const NormArgs& a = b.f;
   RowQueue<T, V, CH, ARRAYS, STAGES> rows;
   rows.H = a.H;
@@ -51,44 +52,42 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(NormBa
   rows.ld[kR] = b.ld_r;
   if constexpr (AFTER) {
     rows.src[kH] = static_cast<const T*>(a.h);
-    rows.src[kGate] = a.gate_kind == MOE_GATE_ELEMENT ? static_cast<const T*>(a.gate) : nullptr;
     rows.ld[kH] = a.ld_h;
-    rows.ld[kGate] = a.ld_gate;
+    if constexpr (ELEMENT) {
+      rows.src[kGate] = static_cast<const T*>(a.gate);
+      rows.ld[kGate] = a.ld_gate;
+    }
   }
-  if (!WARP)
-    for (int i = threadIdx.x; i < 256; i += blockDim.x) (&s_sum[0][0][0][0])[i] = 0.f;
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5;
   const int per_block = WARP ? blockDim.x / 32 : 1;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_block + (WARP ? warp : 0);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
-  rows.start(first, step, a.T, s_ring);
+  const int first = blockIdx.x * per_block + (WARP ? warp : 0), step = gridDim.x * per_block;
+  const int n = first < a.T ? (a.T - 1 - first) / step + 1 : 0;
+  rows.start(first, step, n, s_ring);
 
-  auto factor = [&](int c, float (&f)[V]) {  // w times the channel gate
-    load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c, f);
-    if (a.gate_kind == MOE_GATE_CHANNEL) times_channel_gate<T, V>(a, c, f);
+  auto factor = [&](int which, int c) {  // w times the channel gate, or the next w
+    if (which == kSumNext) return load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c);
+    Values<V> f = load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c);
+    if (a.gate_kind == MOE_GATE_CHANNEL) f = f * channel_gate<T, V>(a, c);
+    return f;
   };
   float4* s_factor = reinterpret_cast<float4*>(s_ring + static_cast<size_t>(STAGES) * rows.stage_packs * 16) + rows.j;
-  auto put_factor = [&](int which, int i, const float (&f)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; v += 4)
-      s_factor[((which * CH + i) * (V / 4) + v / 4) * rows.threads] = make_float4(f[v], f[v + 1], f[v + 2], f[v + 3]);
+  auto factor_at = [&](int which, int i, int v) -> float4& {
+    return s_factor[((which * CH + i) * (V / 4) + v / 4) * rows.threads];
   };
-  auto get_factor = [&](int which, int i, int c, float (&f)[V]) {
+  auto get_factor = [&](int which, int i, int c) {
     if constexpr (CACHED) {
+      Values<V> f;
 #pragma unroll
       for (int v = 0; v < V; v += 4) {
-        const float4 q = s_factor[((which * CH + i) * (V / 4) + v / 4) * rows.threads];
-        f[v] = q.x;
-        f[v + 1] = q.y;
-        f[v + 2] = q.z;
-        f[v + 3] = q.w;
+        const float4 q = factor_at(which, i, v);
+        f.set(v, make_float2(q.x, q.y));
+        f.set(v + 2, make_float2(q.z, q.w));
       }
-    } else if (which == kSumBlock) {
-      factor(c, f);
+      return f;
     } else {
-      load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c, f);
+      return factor(which, c);
     }
   };
   if constexpr (CACHED) {
@@ -96,143 +95,112 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(NormBa
     for (int i = 0; i < CH; ++i) {
       const int c = rows.column(i);
       if (c >= a.H) continue;
-      float f[V];
-      if (AFTER) {
-        factor(c, f);
-        put_factor(kSumBlock, i, f);
-      }
-      if (NEXT) {
-        load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c, f);
-        put_factor(kSumNext, i, f);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (which == kSumBlock ? !AFTER : !NEXT) continue;
+        const Values<V> f = factor(which, c);
+#pragma unroll
+        for (int v = 0; v < V; v += 4) factor_at(which, i, v) = make_float4(f.v[v], f.v[v + 1], f.v[v + 2], f.v[v + 3]);
       }
     }
   }
   const float inv_h = 1.f / static_cast<float>(a.H);
-  float sums[2][CH][V] = {};
-  if (!WARP) __syncthreads();  // s_sum is zero
-  int parity = 0;
-  for (int64_t t = first; t < a.T; t += step, parity ^= 1) {
+  Values<V> sums[2][CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) sums[0][i] = sums[1][i] = zeros<V>();
+  const int64_t out_step = static_cast<int64_t>(step) * a.H, out_first = static_cast<int64_t>(first) * a.H + rows.j * V;
+  T* dx_out = b.dx != nullptr ? static_cast<T*>(b.dx) + out_first : nullptr;
+  T* dh_out = static_cast<T*>(b.dh) + out_first;
+  T* dg_out = static_cast<T*>(b.d_gate) + (ELEMENT ? out_first : first);
+  const T* token_gate = static_cast<const T*>(a.gate) + first * a.ld_gate;
+  for (int k = 0; k < n; ++k) {
     rows.next();
-    float G[CH][V];
+    Values<V> G[CH];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if (b.dr != nullptr && rows.column(i) < a.H) {
-        unpack(rows.at(kDr, i), G[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) G[i][e] = 0.f;
-      }
-    }
+    for (int i = 0; i < CH; ++i)
+      G[i] = b.dr != nullptr && rows.column(i) < a.H ? values(rows.at(kDr, i)) : zeros<V>();
     if constexpr (NEXT) {
-      float ss[2] = {0.f, 0.f};
+      float2 rr = make_float2(0.f, 0.f), rd = rr;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = rows.column(i);
         if (c >= a.H) continue;
-        float wn[V], rf[V], dy[V];
-        get_factor(kSumNext, i, c, wn);
-        unpack(rows.at(kR, i), rf);
-        unpack(rows.at(kDy, i), dy);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          ss[0] = fmaf(rf[e], rf[e], ss[0]);
-          ss[1] = fmaf(rf[e], wn[e] * dy[e], ss[1]);
-        }
+        const Values<V> r = values(rows.at(kR, i)), dy = values(rows.at(kDy, i));
+        add_dot(rr, r, r);
+        add_dot(rd, r, get_factor(kSumNext, i, c) * dy);
       }
-      row_sum<2, WARP>(ss, s_sum[parity][0]);
-      const float inv = rsqrtf(ss[0] * inv_h + a.next_eps);
-      const float back = inv * inv * (inv * (ss[1] * inv_h));
+      float sum[2] = {rr.x + rr.y, rd.x + rd.y};
+      row_sum<2, WARP>(sum, s_sum[k & 1][0]);
+      const float inv = rsqrtf(sum[0] * inv_h + a.next_eps);
+      const float back = inv * inv * (inv * (sum[1] * inv_h));
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = rows.column(i);
         if (c >= a.H) continue;
-        float wn[V], rf[V], dy[V];
-        get_factor(kSumNext, i, c, wn);
-        unpack(rows.at(kR, i), rf);
-        unpack(rows.at(kDy, i), dy);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = inv * dy[e];
-          G[i][e] += d * wn[e] - rf[e] * back;
-          sums[kSumNext][i][e] = fmaf(d, rf[e], sums[kSumNext][i][e]);
-        }
+        const Values<V> r = values(rows.at(kR, i)), d = values(rows.at(kDy, i)) * inv;
+        G[i] = fma(r, -back, fma(d, get_factor(kSumNext, i, c), G[i]));
+        sums[kSumNext][i] = fma(d, r, sums[kSumNext][i]);
       }
     }
-    if (b.dx != nullptr) {
+    if (dx_out != nullptr) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = rows.column(i);
-        if (c >= a.H) continue;
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = a.beta * G[i][e];
-        store_pack(static_cast<T*>(b.dx) + t * a.H + c, pack<T, V>(o));
+        if (rows.column(i) >= a.H) continue;
+        store_pack(dx_out + i * rows.threads * V, pack<T, V>((a.beta != 1.f ? G[i] * a.beta : G[i]).v));
       }
+      dx_out += out_step;
     }
     if constexpr (AFTER) {
-      // a gate by element joins G here; its gradient takes the G without it
       float gt = 1.f, gt_slope = 0.f;
       if (a.gate_kind == MOE_GATE_TOKEN) {
-        gt = gate_value(a.gate_act, to_f32(static_cast<const T*>(a.gate)[t * a.ld_gate]));
+        gt = gate_value(a.gate_act, to_f32(*token_gate));
         gt_slope = gate_slope(a.gate_act, gt);
+        token_gate += step * a.ld_gate;
       }
       float inv = 1.f, back = 0.f;
       if (a.norm || a.gate_kind == MOE_GATE_TOKEN) {
-        float ss[2] = {0.f, 0.f};
+        float2 hh = make_float2(0.f, 0.f), hu = hh;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
           const int c = rows.column(i);
           if (c >= a.H) continue;
-          float wa[V], hf[V], g[V];
-          get_factor(kSumBlock, i, c, wa);
-          unpack(rows.at(kH, i), hf);
-          if (a.gate_kind == MOE_GATE_ELEMENT) unpack(rows.at(kGate, i), g);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            float u = wa[e] * G[i][e];
-            if (a.gate_kind == MOE_GATE_ELEMENT) u *= gate_value(a.gate_act, g[e]);
-            ss[0] = fmaf(hf[e], hf[e], ss[0]);
-            ss[1] = fmaf(hf[e], u, ss[1]);
-          }
+          const Values<V> h = values(rows.at(kH, i));
+          Values<V> u = get_factor(kSumBlock, i, c) * G[i];
+          if constexpr (ELEMENT) u = u * gate_values(a.gate_act, values(rows.at(kGate, i)));
+          add_dot(hh, h, h);
+          add_dot(hu, h, u);
         }
-        row_sum<2, WARP>(ss, s_sum[parity][1]);
+        float sum[2] = {hh.x + hh.y, hu.x + hu.y};
+        row_sum<2, WARP>(sum, s_sum[k & 1][1]);
         if (a.norm) {
-          inv = rsqrtf(ss[0] * inv_h + a.eps);
-          back = inv * inv * (inv * (ss[1] * inv_h));
+          inv = rsqrtf(sum[0] * inv_h + a.eps);
+          back = inv * inv * (inv * (sum[1] * inv_h));
         }
-        if (a.gate_kind == MOE_GATE_TOKEN && rows.j == 0)
-          static_cast<T*>(b.d_gate)[t] = from_f32<T>(gt_slope * (a.alpha * (inv * ss[1])));
+        if (a.gate_kind == MOE_GATE_TOKEN && rows.j == 0) *dg_out = from_f32<T>(gt_slope * (a.alpha * (inv * sum[1])));
       }
-      const float scale = a.alpha * gt, scale_inv = scale * inv, scale_back = scale * back, gt_inv = gt * inv;
+      const float scale = a.alpha * gt;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = rows.column(i);
         if (c >= a.H) continue;
-        float wa[V], hf[V], o[V];
-        get_factor(kSumBlock, i, c, wa);
-        unpack(rows.at(kH, i), hf);
-        if (a.gate_kind == MOE_GATE_ELEMENT) {
-          float g[V], dg[V];
-          unpack(rows.at(kGate, i), g);
+        const Values<V> h = values(rows.at(kH, i)), w = get_factor(kSumBlock, i, c);
+        if constexpr (ELEMENT) {
+          const Values<V> g = gate_values(a.gate_act, values(rows.at(kGate, i)));
+          Values<V> dg = G[i] * (h * (a.alpha * inv)) * w;
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            g[e] = gate_value(a.gate_act, g[e]);
-            dg[e] = gate_slope(a.gate_act, g[e]) * (a.alpha * G[i][e] * (hf[e] * inv * wa[e]));
-            G[i][e] *= g[e];
-          }
-          store_pack(static_cast<T*>(b.d_gate) + t * a.H + c, pack<T, V>(dg));
+          for (int e = 0; e < V; ++e) dg.v[e] *= gate_slope(a.gate_act, g.v[e]);
+          store_pack(dg_out + i * rows.threads * V, pack<T, V>(dg.v));
+          G[i] = G[i] * g;
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          o[e] = scale_inv * (wa[e] * G[i][e]) - hf[e] * scale_back;
-          sums[kSumBlock][i][e] = fmaf(gt_inv * G[i][e], hf[e], sums[kSumBlock][i][e]);
-        }
-        store_pack(static_cast<T*>(b.dh) + t * a.H + c, pack<T, V>(o));
+        sums[kSumBlock][i] = fma(G[i] * (gt * inv), h, sums[kSumBlock][i]);
+        store_pack(dh_out + i * rows.threads * V, pack<T, V>(fma(h, -scale * back, w * (G[i] * (scale * inv))).v));
       }
+      dh_out += out_step;
+      dg_out += ELEMENT ? out_step : step;
     }
   }
 
-  float* s_cols = reinterpret_cast<float*>(s_ring);  // WARP: the join of the block's warps, behind the rows
+  float* s_cols = reinterpret_cast<float*>(s_ring);  // WARP: the join of the block's warps, after the rows
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (!wants(b, which)) continue;
@@ -246,7 +214,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(NormBa
           const int c = rows.column(i);
           if (c >= a.H) continue;
 #pragma unroll
-          for (int e = 0; e < V; ++e) s_cols[c + e] = (w > 0 ? s_cols[c + e] : 0.f) + sums[which][i][e];
+          for (int e = 0; e < V; ++e) s_cols[c + e] = (w > 0 ? s_cols[c + e] : 0.f) + sums[which][i].v[e];
         }
       }
       __syncthreads();
@@ -257,7 +225,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_backward_kernel(NormBa
         const int c = rows.column(i);
         if (c >= a.H) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) part[c + e] = sums[which][i][e];
+        for (int e = 0; e < V; ++e) part[c + e] = sums[which][i].v[e];
       }
     }
   }
@@ -294,9 +262,7 @@ __global__ void __launch_bounds__(1024) norm_backward_general_kernel(NormBackwar
     const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
     const T* gate = static_cast<const T*>(a.gate) + (a.gate_kind == MOE_GATE_CHANNEL ? 0 : t * a.ld_gate);
     auto weight_at = [&](const void* w, int c) {
-      float f[1];
-      load_weight<T, 1>(w, a.weight_f32, a.w_offset, c, f);
-      return f[0];
+      return load_weight<T, 1>(w, a.weight_f32, a.w_offset, c).v[0];
     };
     float next_inv = 0.f, next_back = 0.f;
     if (next) {
@@ -367,12 +333,12 @@ __global__ void __launch_bounds__(1024) norm_backward_general_kernel(NormBackwar
       for (int c = threadIdx.x; c < a.H; c += blockDim.x) partial_row(b, which, blockIdx.x)[c] = s_acc[which][c];
 }
 
-// Column sums over the blocks' parts, in part order within each of 8 strands
+// Column sums over the blocks' parts, in part order within each of 32 strands
 // that are then added in order, and the gradients that follow from them. grid
 // (columns / 32, 2).
 template <typename T>
-__global__ void __launch_bounds__(256) column_sum_kernel(NormBackwardArgs b, int parts) {
-  __shared__ float s[8][32];
+__global__ void __launch_bounds__(1024) column_sum_kernel(NormBackwardArgs b, int parts) {
+  __shared__ float s[32][33];
   pdl_wait();
   pdl_launch_dependents();
   const NormArgs& a = b.f;
@@ -382,14 +348,14 @@ __global__ void __launch_bounds__(256) column_sum_kernel(NormBackwardArgs b, int
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < a.H) {
-#pragma unroll 8
-    for (int p = strand; p < parts; p += 8) v += partial_row(b, which, p)[c];
+#pragma unroll 4
+    for (int p = strand; p < parts; p += 32) v += partial_row(b, which, p)[c];
   }
   s[strand][lane] = v;
   __syncthreads();
   if (strand != 0 || c >= a.H) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v += s[i][lane];
+  for (int i = 1; i < 32; ++i) v += s[i][lane];
   auto store_weight = [&](void* out, float d) {
     if (a.weight_f32) static_cast<float*>(out)[c] = d;
     else static_cast<T*>(out)[c] = from_f32<T>(d);
@@ -401,10 +367,9 @@ __global__ void __launch_bounds__(256) column_sum_kernel(NormBackwardArgs b, int
   v *= a.alpha;
   float gate = 1.f;
   if (a.gate_kind == MOE_GATE_CHANNEL) {
-    float w[1];
-    load_weight<T, 1>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c, w);
+    const float w = load_weight<T, 1>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c).v[0];
     gate = gate_value(a.gate_act, to_f32(static_cast<const T*>(a.gate)[c]));
-    static_cast<T*>(b.d_gate)[c] = from_f32<T>(gate_slope(a.gate_act, gate) * w[0] * v);
+    static_cast<T*>(b.d_gate)[c] = from_f32<T>(gate_slope(a.gate_act, gate) * w * v);
   }
   if (b.d_weight != nullptr) store_weight(b.d_weight, gate * v);
 }
@@ -412,14 +377,17 @@ __global__ void __launch_bounds__(256) column_sum_kernel(NormBackwardArgs b, int
 template <typename T, int V, int CH, int STAGES, bool WARP>
 cudaError_t run(const NormBackwardArgs& b, int threads, int num_sms, cudaStream_t st, int* parts) {
   const NormArgs& a = b.f;
-  auto* k = a.h == nullptr ? norm_backward_kernel<T, V, CH, STAGES, false, true, WARP>
-            : a.next       ? norm_backward_kernel<T, V, CH, STAGES, true, true, WARP>
-                           : norm_backward_kernel<T, V, CH, STAGES, true, false, WARP>;
-  const int arrays = (b.dr != nullptr) + 2 * (a.next != 0) + (a.h != nullptr) + (a.gate_kind == MOE_GATE_ELEMENT);
+  const bool element = a.gate_kind == MOE_GATE_ELEMENT;
+  auto* k = a.h == nullptr ? norm_backward_kernel<T, V, CH, STAGES, false, true, false, WARP>
+            : a.next       ? (element ? norm_backward_kernel<T, V, CH, STAGES, true, true, true, WARP>
+                                      : norm_backward_kernel<T, V, CH, STAGES, true, true, false, WARP>)
+                           : (element ? norm_backward_kernel<T, V, CH, STAGES, true, false, true, WARP>
+                                      : norm_backward_kernel<T, V, CH, STAGES, true, false, false, WARP>);
+  const int arrays = (b.dr != nullptr) + 2 * (a.next != 0) + (a.h != nullptr) + element;
   size_t smem = static_cast<size_t>(STAGES) * arrays * CH * threads * sizeof(Pack<T, V>);
   if (WARP) smem = std::max(smem, sizeof(float) * a.H);
   else if (STAGES > 0) smem += sizeof(float) * 2 * CH * V * threads;
-  int blocks = std::max(1, 1024 / threads);
+  int blocks = std::max(1, 512 / threads);
   if (smem > 0) blocks = std::max(1, std::min<int>(blocks, kQueueSmem / smem));
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -464,18 +432,22 @@ cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& b, int num_s
       e = run<T, V, 1, 2, true>(b, 256, num_sms, st, &parts);
     } else if (vec && packs <= 64) {
       e = run<T, V, 2, 2, true>(b, 256, num_sms, st, &parts);
-    } else if (vec && packs <= 1024) {
+    } else if (vec && packs <= 256) {
       e = run<T, V, 1, 2, false>(b, threads(1), num_sms, st, &parts);
-    } else if (!vec && packs <= 4096) {
+    } else if (vec && packs <= 1024) {
+      e = run<T, V, 2, 2, false>(b, threads(2), num_sms, st, &parts);
+    } else if (!vec && packs <= 2048) {
       e = run<T, 1, 4, 0, false>(b, threads(4), num_sms, st, &parts);
+    } else if (!vec && packs <= 8192) {
+      e = run<T, 1, 16, 0, false>(b, threads(16), num_sms, st, &parts);
     } else if (vec && packs <= 2048 && sizeof(T) == 4) {
-      if constexpr (sizeof(T) == 4) e = run<T, V, 2, 0, false>(b, threads(2), num_sms, st, &parts);
+      if constexpr (sizeof(T) == 4) e = run<T, V, 4, 0, false>(b, threads(4), num_sms, st, &parts);
     } else {
       e = run_general<T>(b, num_sms, st, &parts);
     }
     if (e != cudaSuccess) return e;
     if (b.d_weight == nullptr && b.d_next_weight == nullptr && a.gate_kind != MOE_GATE_CHANNEL) return e;
-    return launch_kernel(true, column_sum_kernel<T>, dim3(ceil_div(a.H, 32), 2), 256, 0, st, b, parts);
+    return launch_kernel(true, column_sum_kernel<T>, dim3(ceil_div(a.H, 32), 2), 1024, 0, st, b, parts);
   });
 }
 

@@ -24,41 +24,42 @@ __device__ __forceinline__ void cp_async_wait() {
 // (STAGES = 0), a second time from the L1.
 template <typename T, int V, int CH, int ARRAYS, int STAGES>
 struct RowQueue {
-  const T* src[ARRAYS];  // null: absent
-  int64_t ld[ARRAYS];
+  const T* src[ARRAYS];  // null: absent; else, once started, this thread's first pack of the row to fetch
+  int64_t ld[ARRAYS];    // once started, the way to the block's next row
   int H, threads, j;
-  int64_t row, step, last;  // rows row, row + step, ... below last
+  int put_left;          // rows still to fetch
   // STAGES > 0: [STAGES][arrays present][CH][threads], at this thread
   Pack<T, V>* ring;
-  int64_t put_row;
   int stage_packs, put_at, get_at;
   int array_at[ARRAYS];
 
   __device__ __forceinline__ int column(int i) const { return (i * threads + j) * V; }
 
   __device__ __forceinline__ void put() {
-    if (put_row < last) {
+    if (put_left > 0) {
+      --put_left;
 #pragma unroll
       for (int a = 0; a < ARRAYS; ++a) {
         if (src[a] == nullptr) continue;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int c = column(i);
-          if (c < H) cp_async16(ring + put_at + array_at[a] + i * threads, src[a] + put_row * ld[a] + c);
-        }
+        for (int i = 0; i < CH; ++i)
+          if (column(i) < H) cp_async16(ring + put_at + array_at[a] + i * threads, src[a] + i * threads * V);
+        src[a] += ld[a];
       }
     }
-    put_row += step;
     cp_async_commit();
     put_at = put_at + stage_packs == STAGES * stage_packs ? 0 : put_at + stage_packs;
   }
 
-  __device__ __forceinline__ void start(int64_t first, int64_t step_, int64_t last_, void* smem) {
-    step = step_;
-    last = last_;
-    row = first - step;
+  // Rows first, first + step, ... (n of them).
+  __device__ __forceinline__ void start(int64_t first, int64_t step, int n, void* smem) {
+    put_left = n;
+#pragma unroll
+    for (int a = 0; a < ARRAYS; ++a) {
+      if (src[a] != nullptr) src[a] += (STAGES > 0 ? first : first - step) * ld[a] + j * V;
+      ld[a] *= step;
+    }
     if constexpr (STAGES > 0) {
-      put_row = first;
       int present = 0;
 #pragma unroll
       for (int a = 0; a < ARRAYS; ++a) {
@@ -77,49 +78,132 @@ struct RowQueue {
 
   // Moves on to the next row.
   __device__ __forceinline__ void next() {
-    row += step;
     if constexpr (STAGES > 0) {
       put();
       cp_async_wait<STAGES - 1>();
       get_at = get_at + stage_packs == STAGES * stage_packs ? 0 : get_at + stage_packs;
+    } else {
+#pragma unroll
+      for (int a = 0; a < ARRAYS; ++a)
+        if (src[a] != nullptr) src[a] += ld[a];
     }
   }
 
   // Pack i of an array that is present, of the row.
   __device__ __forceinline__ Pack<T, V> at(int a, int i) const {
     if constexpr (STAGES > 0) return ring[get_at + array_at[a] + i * threads];
-    else return load_pack<V>(src[a] + row * ld[a] + column(i));
+    else return load_pack<V>(src[a] + i * threads * V);
   }
 };
 
 // N sums over the threads of a row: a warp (WARP) or the whole block, with
-// one barrier. A scratch s (32 floats a value, zero behind the last warp) may
-// be written again once every thread has passed a later barrier: callers use
-// one per sum of a row and alternate by row.
+// one barrier. A scratch s may be written again once every thread has passed
+// a later barrier: callers use one per sum of a row and alternate by row.
 template <int N, bool WARP>
 __device__ __forceinline__ void row_sum(float (&v)[N], float (*s)[32]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
   if (WARP) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i][warp] = v[i];
   }
   __syncthreads();
-  const int quads = (blockDim.x + 127) >> 7;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q = 0; q < quads; ++q) {
-      const float4 p = *reinterpret_cast<const float4*>(&s[i][4 * q]);
-      t.x += p.x;
-      t.y += p.y;
-      t.z += p.z;
-      t.w += p.w;
-    }
-    v[i] = (t.x + t.y) + (t.z + t.w);
+    v[i] = warp_sum(lane < warps ? s[i][lane] : 0.f);
   }
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// V fp32 values of a pack, in pairs where there are pairs.
+template <int V>
+struct Values {
+  float v[V];
+  __device__ __forceinline__ float2 pair(int i) const { return make_float2(v[i], v[i + 1]); }
+  __device__ __forceinline__ void set(int i, float2 p) {
+    v[i] = p.x;
+    v[i + 1] = p.y;
+  }
+};
+template <int V>
+__device__ __forceinline__ Values<V> operator*(const Values<V>& a, const Values<V>& b) {
+  Values<V> d;
+  if constexpr (V == 1) {
+    d.v[0] = a.v[0] * b.v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) d.set(i, mul2(a.pair(i), b.pair(i)));
+  }
+  return d;
+}
+template <int V>
+__device__ __forceinline__ Values<V> operator*(const Values<V>& a, float s) {
+  Values<V> b;
+#pragma unroll
+  for (int i = 0; i < V; ++i) b.v[i] = s;
+  return a * b;
+}
+template <int V>
+__device__ __forceinline__ Values<V> fma(const Values<V>& a, const Values<V>& b, const Values<V>& c) {
+  Values<V> d;
+  if constexpr (V == 1) {
+    d.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) d.set(i, fma2(a.pair(i), b.pair(i), c.pair(i)));
+  }
+  return d;
+}
+template <int V>
+__device__ __forceinline__ Values<V> fma(const Values<V>& a, float s, const Values<V>& c) {
+  Values<V> b;
+#pragma unroll
+  for (int i = 0; i < V; ++i) b.v[i] = s;
+  return fma(a, b, c);
+}
+// A sum of products as two strands.
+template <int V>
+__device__ __forceinline__ void add_dot(float2& sum, const Values<V>& a, const Values<V>& b) {
+  if constexpr (V == 1) {
+    sum.x = fmaf(a.v[0], b.v[0], sum.x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) sum = fma2(a.pair(i), b.pair(i), sum);
+  }
+}
+template <int V>
+__device__ __forceinline__ Values<V> zeros() {
+  Values<V> z;
+#pragma unroll
+  for (int i = 0; i < V; ++i) z.v[i] = 0.f;
+  return z;
+}
+template <typename T, int V>
+__device__ __forceinline__ Values<V> values(const Pack<T, V>& p) {
+  Values<V> f;
+  unpack(p, f.v);
+  return f;
 }
 
 __device__ __forceinline__ float gate_value(int act, float v) {
@@ -136,32 +220,39 @@ __device__ __forceinline__ float gate_slope(int act, float g) {
 
 // w_offset + weight (1 without a weight) of columns c..c+V-1.
 template <typename T, int V>
-__device__ __forceinline__ void load_weight(const void* w, int w_f32, float offset, int c, float (&f)[V]) {
+__device__ __forceinline__ Values<V> load_weight(const void* w, int w_f32, float offset, int c) {
+  Values<V> f;
   if (w == nullptr) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = 1.f;
+    for (int i = 0; i < V; ++i) f.v[i] = 1.f;
   } else if (w_f32 && sizeof(T) != 4) {
     constexpr int V4 = V < 4 ? V : 4;
 #pragma unroll
     for (int i = 0; i < V; i += V4) {
       const Pack<float, V4> p = load_pack<V4>(static_cast<const float*>(w) + c + i);
 #pragma unroll
-      for (int j = 0; j < V4; ++j) f[i + j] = p.e[j] + offset;
+      for (int j = 0; j < V4; ++j) f.v[i + j] = p.e[j] + offset;
     }
   } else {
-    unpack(load_pack<V>(static_cast<const T*>(w) + c), f);
+    f = values(load_pack<V>(static_cast<const T*>(w) + c));
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] += offset;
+    for (int i = 0; i < V; ++i) f.v[i] += offset;
   }
+  return f;
 }
 
-// Times the channel gate's activation.
-template <typename T, int V>
-__device__ __forceinline__ void times_channel_gate(const NormArgs& a, int c, float (&f)[V]) {
-  float g[V];
-  unpack(load_pack<V>(static_cast<const T*>(a.gate) + c), g);
+// The gate's activation, V values of it.
+template <int V>
+__device__ __forceinline__ Values<V> gate_values(int act, Values<V> g) {
+  if (act != MOE_GATE_LINEAR) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] *= gate_value(a.gate_act, g[i]);
+    for (int i = 0; i < V; ++i) g.v[i] = gate_value(act, g.v[i]);
+  }
+  return g;
+}
+template <typename T, int V>
+__device__ __forceinline__ Values<V> channel_gate(const NormArgs& a, int c) {
+  return gate_values(a.gate_act, values(load_pack<V>(static_cast<const T*>(a.gate) + c)));
 }
 
 // Every operand allows 16-byte accesses (null pointers and unused strides of

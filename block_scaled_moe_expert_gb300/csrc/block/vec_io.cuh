@@ -37,16 +37,48 @@ template <int V, typename T>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& v) {
   *reinterpret_cast<Pack<T, V>*>(p) = v;
 }
+// Two 16-bit values of a word, and back: one instruction a value, one a pair.
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2(float2 v, __nv_bfloat16) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float2 v, __half) {
+  const __half2 h = __float22half2_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const Pack<T, V>& p, float (&f)[V]) {
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = to_f32(p.e[i]);
+    for (int i = 0; i < V; i += 2) {
+      const float2 v = unpack2(w[i / 2], T());
+      f[i] = v.x;
+      f[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f32(p.e[i]);
+  }
 }
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> pack(const float (&f)[V]) {
   Pack<T, V> p;
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&p);
 #pragma unroll
-  for (int i = 0; i < V; ++i) p.e[i] = from_f32<T>(f[i]);
+    for (int i = 0; i < V; i += 2) w[i / 2] = pack2(make_float2(f[i], f[i + 1]), T());
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.e[i] = from_f32<T>(f[i]);
+  }
   return p;
 }
 
