@@ -20,7 +20,8 @@ enum { kX = 0, kH = 1, kGate = 2 };
 // One row per warp (WARP) or per block. ELEMENT: a gate
 // by element.
 template <typename T, int V, int CH, int STAGES, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : CH * V <= 16 ? 1024 : 512, WARP ? 8 : 1) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 512, WARP ? 8 : V == 1 && CH <= 16 ? 2 : 1)
+    norm_kernel(NormArgs a) {
   constexpr int ARRAYS = AFTER ? ELEMENT ? 3 : 2 : 1;
   constexpr bool CACHED = CH * V <= 8;  // the columns' factors stay in registers
   extern __shared__ __align__(16) uint8_t s_ring[];
@@ -126,7 +127,7 @@ cudaError_t run(const NormArgs& a, int threads, int num_sms, cudaStream_t st) {
                            : (element ? norm_kernel<T, V, CH, STAGES, true, false, true, WARP>
                                       : norm_kernel<T, V, CH, STAGES, true, false, false, WARP>);
   const int arrays = a.h == nullptr ? 1 : element ? 3 : 2;
-  const size_t smem = static_cast<size_t>(STAGES) * arrays * CH * threads * sizeof(Pack<T, V>);
+  const size_t smem = queue_smem<T, V, CH, STAGES>(a.H, arrays, threads);
   // 1024 threads an SM (512 with many columns a thread), fewer blocks where
   // their rows in flight would not fit
   int blocks = std::max(1, (CH * V <= 16 ? 1024 : 512) / threads);
@@ -151,8 +152,9 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, int num_sms, cudaStream_t 
     const int packs = vec ? a.H / V : a.H;
     auto threads = [&](int ch) { return ceil_div(ceil_div(packs, ch), 32) * 32; };
     if (!vec) {
-      if (packs <= 2048) return run<T, 1, 4, 0, false>(a, threads(4), num_sms, st);
-      if (packs <= 8192) return run<T, 1, 16, 0, false>(a, threads(16), num_sms, st);
+      if (packs <= 1024) return run<T, 1, 4, 3, false>(a, threads(4), num_sms, st);
+      if (packs <= 4096) return run<T, 1, 8, 3, false>(a, threads(8), num_sms, st);
+      if (packs <= 8192) return run<T, 1, 16, 2, false>(a, threads(16), num_sms, st);
       return run<T, 1, 32, 0, false>(a, threads(32), num_sms, st);
     }
     if (packs <= 32) return run<T, V, 1, 4, true>(a, 128, num_sms, st);

@@ -32,11 +32,12 @@ __device__ __forceinline__ float* partial_row(const NormBackwardArgs& b, int whi
 
 // One row per warp (WARP) or per block. ELEMENT: a gate by element.
 template <typename T, int V, int CH, int STAGES, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512) norm_backward_kernel(NormBackwardArgs b) {
+__global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
+    norm_backward_kernel(NormBackwardArgs b) {
   constexpr int ARRAYS = AFTER ? ELEMENT ? 5 : 4 : 3;
   // the columns' factors stand in shared memory behind the ring (each thread
   // its own): beside the column sums they would not fit into the registers
-  constexpr bool CACHED = STAGES > 0 && !WARP;
+  constexpr bool CACHED = STAGES > 0 && V > 1 && !WARP;
   extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ float s_sum[2][2][2][32];
   const NormArgs& a = b.f;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_backward_kernel(NormBac
     if (a.gate_kind == MOE_GATE_CHANNEL) f = f * channel_gate<T, V>(a, c);
     return f;
   };
-  float4* s_factor = reinterpret_cast<float4*>(s_ring + static_cast<size_t>(STAGES) * rows.stage_packs * 16) + rows.j;
+  float4* s_factor = reinterpret_cast<float4*>(s_ring + static_cast<size_t>(STAGES) * rows.stage_bytes) + rows.j;
   auto factor_at = [&](int which, int i, int v) -> float4& {
     return s_factor[((which * CH + i) * (V / 4) + v / 4) * rows.threads];
   };
@@ -384,10 +385,10 @@ cudaError_t run(const NormBackwardArgs& b, int threads, int num_sms, cudaStream_
                            : (element ? norm_backward_kernel<T, V, CH, STAGES, true, false, true, WARP>
                                       : norm_backward_kernel<T, V, CH, STAGES, true, false, false, WARP>);
   const int arrays = (b.dr != nullptr) + 2 * (a.next != 0) + (a.h != nullptr) + element;
-  size_t smem = static_cast<size_t>(STAGES) * arrays * CH * threads * sizeof(Pack<T, V>);
+  size_t smem = queue_smem<T, V, CH, STAGES>(a.H, arrays, threads);
   if (WARP) smem = std::max(smem, sizeof(float) * a.H);
-  else if (STAGES > 0) smem += sizeof(float) * 2 * CH * V * threads;
-  int blocks = std::max(1, 512 / threads);
+  else if (STAGES > 0 && V > 1) smem += sizeof(float) * 2 * CH * V * threads;
+  int blocks = std::max(1, (V == 1 && CH <= 8 ? 1024 : 512) / threads);
   if (smem > 0) blocks = std::max(1, std::min<int>(blocks, kQueueSmem / smem));
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -436,8 +437,10 @@ cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& b, int num_s
       e = run<T, V, 1, 2, false>(b, threads(1), num_sms, st, &parts);
     } else if (vec && packs <= 1024) {
       e = run<T, V, 2, 2, false>(b, threads(2), num_sms, st, &parts);
-    } else if (!vec && packs <= 2048) {
-      e = run<T, 1, 4, 0, false>(b, threads(4), num_sms, st, &parts);
+    } else if (!vec && packs <= 1024) {
+      e = run<T, 1, 4, 2, false>(b, threads(4), num_sms, st, &parts);
+    } else if (!vec && packs <= 4096) {
+      e = run<T, 1, 8, 2, false>(b, threads(8), num_sms, st, &parts);
     } else if (!vec && packs <= 8192) {
       e = run<T, 1, 16, 0, false>(b, threads(16), num_sms, st, &parts);
     } else if (vec && packs <= 2048 && sizeof(T) == 4) {

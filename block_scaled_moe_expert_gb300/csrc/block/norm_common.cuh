@@ -15,23 +15,38 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The same, of only the first `bytes` bytes (the rest of the 16 become zero).
+__device__ __forceinline__ void cp_async16_part(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// Bytes of an array's stage for rows of any alignment: whole 16-byte chunks.
+__host__ __device__ constexpr int loose_row_bytes(int H, int size) { return (H * size + 15 + 15) / 16 * 16; }
+
 // Thread j of a row owns the packs j, j + threads, ... (CH of them) of every
-// row that its block (or warp) walks. With STAGES > 0 its packs of the next
-// STAGES - 1 rows are on their way into its own slots of shared memory while
-// it works on one: nobody else reads them, so there is no barrier in the
-// queue. Packs that asynchronous copies cannot carry (V = 1), or rows too
-// long for shared memory, are read from global memory where they are used
-// (STAGES = 0), a second time from the L1.
+// row that its block (or warp) walks, and with STAGES > 0 the next rows are on
+// their way into shared memory while it works on one.
+//   Packs (V > 1): each thread copies its own packs into its own slots, which
+// nobody else reads, so there is no barrier in the queue.
+//   Rows of any width and alignment (V = 1): the block copies the aligned
+// 16-byte chunks that hold the row, whatever they hold beside it (in front of
+// the row that is memory of the same allocation, which starts at a multiple of
+// 256 bytes; the last chunk is cut at the row's end), and the elements are read
+// where they lie in them; one barrier a row.
+//   STAGES = 0: rows that are too long for shared memory are read from global
+// memory where they are used, a second time from the L1.
 template <typename T, int V, int CH, int ARRAYS, int STAGES>
 struct RowQueue {
-  const T* src[ARRAYS];  // null: absent; else, once started, this thread's first pack of the row to fetch
+  static constexpr bool kLoose = V == 1 && STAGES > 0;
+  const T* src[ARRAYS];  // null: absent; else, once started, where the row to fetch starts (for this thread)
   int64_t ld[ARRAYS];    // once started, the way to the block's next row
   int H, threads, j;
   int put_left;          // rows still to fetch
-  // STAGES > 0: [STAGES][arrays present][CH][threads], at this thread
-  Pack<T, V>* ring;
-  int stage_packs, put_at, get_at;
+  // STAGES > 0, in bytes: [STAGES][arrays present][a row]
+  uint8_t* ring;
+  int stage_bytes, put_at, get_at;
   int array_at[ARRAYS];
+  int phase[ARRAYS], phase_step[ARRAYS];  // loose rows: where in its first chunk the row in work starts
 
   __device__ __forceinline__ int column(int i) const { return (i * threads + j) * V; }
 
@@ -41,14 +56,22 @@ struct RowQueue {
 #pragma unroll
       for (int a = 0; a < ARRAYS; ++a) {
         if (src[a] == nullptr) continue;
+        uint8_t* dst = ring + put_at + array_at[a];
+        if constexpr (kLoose) {
+          const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src[a]) & 15);
+          const uint8_t* p = reinterpret_cast<const uint8_t*>(src[a]) - skip;
+          const int bytes = skip + H * static_cast<int>(sizeof(T));
+          for (int at = j * 16; at < bytes; at += threads * 16) cp_async16_part(dst + at, p + at, min(16, bytes - at));
+        } else {
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-          if (column(i) < H) cp_async16(ring + put_at + array_at[a] + i * threads, src[a] + i * threads * V);
+          for (int i = 0; i < CH; ++i)
+            if (column(i) < H) cp_async16(dst + i * threads * 16, src[a] + i * threads * V);
+        }
         src[a] += ld[a];
       }
     }
     cp_async_commit();
-    put_at = put_at + stage_packs == STAGES * stage_packs ? 0 : put_at + stage_packs;
+    put_at = put_at + stage_bytes == STAGES * stage_bytes ? 0 : put_at + stage_bytes;
   }
 
   // Rows first, first + step, ... (n of them).
@@ -56,21 +79,26 @@ struct RowQueue {
     put_left = n;
 #pragma unroll
     for (int a = 0; a < ARRAYS; ++a) {
-      if (src[a] != nullptr) src[a] += (STAGES > 0 ? first : first - step) * ld[a] + j * V;
+      if (src[a] != nullptr) src[a] += (STAGES > 0 ? first : first - step) * ld[a] + (kLoose ? 0 : j * V);
       ld[a] *= step;
     }
     if constexpr (STAGES > 0) {
+      const int row_bytes = kLoose ? loose_row_bytes(H, sizeof(T)) : CH * threads * 16;
       int present = 0;
 #pragma unroll
       for (int a = 0; a < ARRAYS; ++a) {
-        array_at[a] = present * CH * threads;
+        array_at[a] = present * row_bytes;
         present += src[a] != nullptr;
+        if constexpr (kLoose) {
+          phase_step[a] = static_cast<int>((ld[a] * static_cast<int64_t>(sizeof(T))) & 15);
+          phase[a] = static_cast<int>(reinterpret_cast<uintptr_t>(src[a]) & 15) - phase_step[a];
+        }
       }
-      stage_packs = present * CH * threads;
+      stage_bytes = present * row_bytes;
       // (a warp's row has its own ring)
-      ring = static_cast<Pack<T, V>*>(smem) + (threadIdx.x / threads) * (STAGES * stage_packs) + j;
+      ring = static_cast<uint8_t*>(smem) + (threadIdx.x / threads) * (STAGES * stage_bytes) + (kLoose ? 0 : j * 16);
       put_at = 0;
-      get_at = -stage_packs;
+      get_at = -stage_bytes;
 #pragma unroll
       for (int s = 0; s < STAGES - 1; ++s) put();
     }
@@ -78,23 +106,38 @@ struct RowQueue {
 
   // Moves on to the next row.
   __device__ __forceinline__ void next() {
-    if constexpr (STAGES > 0) {
+    if constexpr (kLoose) {
+      cp_async_wait<STAGES - 2>();
+      __syncthreads();  // the row is here, and nobody reads the one before, whose place the next fetch takes
+      put();
+#pragma unroll
+      for (int a = 0; a < ARRAYS; ++a) phase[a] = (phase[a] + phase_step[a]) & 15;
+    } else if constexpr (STAGES > 0) {
       put();
       cp_async_wait<STAGES - 1>();
-      get_at = get_at + stage_packs == STAGES * stage_packs ? 0 : get_at + stage_packs;
     } else {
 #pragma unroll
       for (int a = 0; a < ARRAYS; ++a)
         if (src[a] != nullptr) src[a] += ld[a];
     }
+    if constexpr (STAGES > 0) get_at = get_at + stage_bytes == STAGES * stage_bytes ? 0 : get_at + stage_bytes;
   }
 
   // Pack i of an array that is present, of the row.
   __device__ __forceinline__ Pack<T, V> at(int a, int i) const {
-    if constexpr (STAGES > 0) return ring[get_at + array_at[a] + i * threads];
+    if constexpr (kLoose)
+      return *reinterpret_cast<const Pack<T, V>*>(ring + get_at + array_at[a] + phase[a] + column(i) * sizeof(T));
+    else if constexpr (STAGES > 0) return *reinterpret_cast<const Pack<T, V>*>(ring + get_at + array_at[a] + i * threads * 16);
     else return load_pack<V>(src[a] + i * threads * V);
   }
 };
+
+// Shared memory of a queue's rows of one block.
+template <typename T, int V, int CH, int STAGES>
+size_t queue_smem(int H, int arrays, int threads) {
+  if (STAGES == 0) return 0;
+  return static_cast<size_t>(STAGES) * arrays * (V == 1 ? loose_row_bytes(H, sizeof(T)) : CH * threads * 16);
+}
 
 // N sums over the threads of a row: a warp (WARP) or the whole block, with
 // one barrier. A scratch s may be written again once every thread has passed
