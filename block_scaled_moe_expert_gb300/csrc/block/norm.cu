@@ -19,16 +19,15 @@ enum { kX = 0, kH = 1, kGate = 2 };
 
 // One row per warp (WARP) or per block. ELEMENT: a gate
 // by element.
-template <typename T, int V, int CH, int STAGES, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
+template <typename T, int V, int CH, int STAGES, int THREADS, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 512, WARP ? 8 : V == 1 && CH <= 16 ? 2 : 1)
     norm_kernel(NormArgs a) {
   constexpr int ARRAYS = AFTER ? ELEMENT ? 3 : 2 : 1;
   constexpr bool CACHED = CH * V <= 8;  // the columns' factors stay in registers
   extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ float s_sum[2][2][1][32];  // by the row's parity: a row's sums do not wait for the row before
-  RowQueue<T, V, CH, ARRAYS, STAGES> rows;
+  RowQueue<T, V, CH, ARRAYS, STAGES, WARP ? 32 : THREADS> rows;
   rows.H = a.H;
-  rows.threads = WARP ? 32 : blockDim.x;
   rows.j = WARP ? threadIdx.x & 31 : threadIdx.x;
   rows.src[kX] = static_cast<const T*>(a.x);
   rows.ld[kX] = a.ld_x;
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 51
         if (a.beta != 1.f) x = x * a.beta;
         if constexpr (ELEMENT) r[i] = r[i] * gate_values(a.gate_act, values(rows.at(kGate, i)));
         r[i] = fma(r[i] * scale, CACHED ? wa[i] : factor(c), x);
-        store_pack(r_out + i * rows.threads * V, pack<T, V>(r[i].v));
+        store_pack(r_out + i * rows.threads() * V, pack<T, V>(r[i].v));
       }
     } else {
 #pragma unroll
@@ -112,20 +111,20 @@ __global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 51
         const int c = rows.column(i);
         if (c >= a.H) continue;
         const Values<V> w = CACHED ? wn[i] : load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c);
-        store_pack(y_out + i * rows.threads * V, pack<T, V>((r[i] * scale * w).v));
+        store_pack(y_out + i * rows.threads() * V, pack<T, V>((r[i] * scale * w).v));
       }
     }
   }
 }
 
-template <typename T, int V, int CH, int STAGES, bool WARP>
+template <typename T, int V, int CH, int STAGES, bool WARP, int THREADS = 0>
 cudaError_t run(const NormArgs& a, int threads, int num_sms, cudaStream_t st) {
   const bool element = a.gate_kind == MOE_GATE_ELEMENT;
-  auto* k = a.h == nullptr ? norm_kernel<T, V, CH, STAGES, false, true, false, WARP>
-            : a.next       ? (element ? norm_kernel<T, V, CH, STAGES, true, true, true, WARP>
-                                      : norm_kernel<T, V, CH, STAGES, true, true, false, WARP>)
-                           : (element ? norm_kernel<T, V, CH, STAGES, true, false, true, WARP>
-                                      : norm_kernel<T, V, CH, STAGES, true, false, false, WARP>);
+  auto* k = a.h == nullptr ? norm_kernel<T, V, CH, STAGES, THREADS, false, true, false, WARP>
+            : a.next       ? (element ? norm_kernel<T, V, CH, STAGES, THREADS, true, true, true, WARP>
+                                      : norm_kernel<T, V, CH, STAGES, THREADS, true, true, false, WARP>)
+                           : (element ? norm_kernel<T, V, CH, STAGES, THREADS, true, false, true, WARP>
+                                      : norm_kernel<T, V, CH, STAGES, THREADS, true, false, false, WARP>);
   const int arrays = a.h == nullptr ? 1 : element ? 3 : 2;
   const size_t smem = queue_smem<T, V, CH, STAGES>(a.H, arrays, threads);
   // 1024 threads an SM (512 with many columns a thread), fewer blocks where
@@ -152,10 +151,11 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, int num_sms, cudaStream_t 
     const int packs = vec ? a.H / V : a.H;
     auto threads = [&](int ch) { return ceil_div(ceil_div(packs, ch), 32) * 32; };
     if (!vec) {
-      if (packs <= 1024) return run<T, 1, 4, 3, false>(a, threads(4), num_sms, st);
-      if (packs <= 4096) return run<T, 1, 8, 3, false>(a, threads(8), num_sms, st);
-      if (packs <= 8192) return run<T, 1, 16, 2, false>(a, threads(16), num_sms, st);
-      return run<T, 1, 32, 0, false>(a, threads(32), num_sms, st);
+      if (packs <= 1024) return run<T, 1, 4, 3, false, 256>(a, 256, num_sms, st);
+      if (packs <= 2048) return run<T, 1, 8, 3, false, 256>(a, 256, num_sms, st);
+      if (packs <= 4096) return run<T, 1, 8, 3, false, 512>(a, 512, num_sms, st);
+      if (packs <= 8192) return run<T, 1, 16, 2, false, 512>(a, 512, num_sms, st);
+      return run<T, 1, 32, 0, false, 512>(a, 512, num_sms, st);
     }
     if (packs <= 32) return run<T, V, 1, 4, true>(a, 128, num_sms, st);
     if (packs <= 64) return run<T, V, 2, 4, true>(a, 128, num_sms, st);

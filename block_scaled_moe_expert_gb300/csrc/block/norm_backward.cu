@@ -31,19 +31,18 @@ __device__ __forceinline__ float* partial_row(const NormBackwardArgs& b, int whi
 }
 
 // One row per warp (WARP) or per block. ELEMENT: a gate by element.
-template <typename T, int V, int CH, int STAGES, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
+template <typename T, int V, int CH, int STAGES, int THREADS, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
     norm_backward_kernel(NormBackwardArgs b) {
   constexpr int ARRAYS = AFTER ? ELEMENT ? 5 : 4 : 3;
   // the columns' factors stand in shared memory behind the ring (each thread
   // its own): beside the column sums they would not fit into the registers
-  constexpr bool CACHED = STAGES > 0 && V > 1 && !WARP;
+  constexpr bool CACHED = STAGES > 0 && !WARP;
   extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ float s_sum[2][2][2][32];
   const NormArgs& a = b.f;
-  RowQueue<T, V, CH, ARRAYS, STAGES> rows;
+  RowQueue<T, V, CH, ARRAYS, STAGES, WARP ? 32 : THREADS> rows;
   rows.H = a.H;
-  rows.threads = WARP ? 32 : blockDim.x;
   rows.j = WARP ? threadIdx.x & 31 : threadIdx.x;
   rows.src[kDr] = static_cast<const T*>(b.dr);
   rows.src[kDy] = NEXT ? static_cast<const T*>(b.dy) : nullptr;
@@ -73,18 +72,20 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
     if (a.gate_kind == MOE_GATE_CHANNEL) f = f * channel_gate<T, V>(a, c);
     return f;
   };
-  float4* s_factor = reinterpret_cast<float4*>(s_ring + static_cast<size_t>(STAGES) * rows.stage_bytes) + rows.j;
-  auto factor_at = [&](int which, int i, int v) -> float4& {
-    return s_factor[((which * CH + i) * (V / 4) + v / 4) * rows.threads];
+  constexpr int F = V > 1 ? 4 : 1;  // floats of a factor that move together
+  using FactorPack = Pack<float, F>;
+  FactorPack* s_factor = reinterpret_cast<FactorPack*>(s_ring + static_cast<size_t>(STAGES) * rows.stage_bytes) + rows.j;
+  auto factor_at = [&](int which, int i, int v) -> FactorPack& {
+    return s_factor[((which * CH + i) * (V / F) + v / F) * rows.threads()];
   };
   auto get_factor = [&](int which, int i, int c) {
     if constexpr (CACHED) {
       Values<V> f;
 #pragma unroll
-      for (int v = 0; v < V; v += 4) {
-        const float4 q = factor_at(which, i, v);
-        f.set(v, make_float2(q.x, q.y));
-        f.set(v + 2, make_float2(q.z, q.w));
+      for (int v = 0; v < V; v += F) {
+        const FactorPack q = factor_at(which, i, v);
+#pragma unroll
+        for (int e = 0; e < F; ++e) f.v[v + e] = q.e[e];
       }
       return f;
     } else {
@@ -101,7 +102,12 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
         if (which == kSumBlock ? !AFTER : !NEXT) continue;
         const Values<V> f = factor(which, c);
 #pragma unroll
-        for (int v = 0; v < V; v += 4) factor_at(which, i, v) = make_float4(f.v[v], f.v[v + 1], f.v[v + 2], f.v[v + 3]);
+        for (int v = 0; v < V; v += F) {
+          FactorPack q;
+#pragma unroll
+          for (int e = 0; e < F; ++e) q.e[e] = f.v[v + e];
+          factor_at(which, i, v) = q;
+        }
       }
     }
   }
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         if (rows.column(i) >= a.H) continue;
-        store_pack(dx_out + i * rows.threads * V, pack<T, V>((a.beta != 1.f ? G[i] * a.beta : G[i]).v));
+        store_pack(dx_out + i * rows.threads() * V, pack<T, V>((a.beta != 1.f ? G[i] * a.beta : G[i]).v));
       }
       dx_out += out_step;
     }
@@ -190,11 +196,11 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
           Values<V> dg = G[i] * (h * (a.alpha * inv)) * w;
 #pragma unroll
           for (int e = 0; e < V; ++e) dg.v[e] *= gate_slope(a.gate_act, g.v[e]);
-          store_pack(dg_out + i * rows.threads * V, pack<T, V>(dg.v));
+          store_pack(dg_out + i * rows.threads() * V, pack<T, V>(dg.v));
           G[i] = G[i] * g;
         }
         sums[kSumBlock][i] = fma(G[i] * (gt * inv), h, sums[kSumBlock][i]);
-        store_pack(dh_out + i * rows.threads * V, pack<T, V>(fma(h, -scale * back, w * (G[i] * (scale * inv))).v));
+        store_pack(dh_out + i * rows.threads() * V, pack<T, V>(fma(h, -scale * back, w * (G[i] * (scale * inv))).v));
       }
       dh_out += out_step;
       dg_out += ELEMENT ? out_step : step;
@@ -375,19 +381,19 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(NormBackwardArgs b, in
   if (b.d_weight != nullptr) store_weight(b.d_weight, gate * v);
 }
 
-template <typename T, int V, int CH, int STAGES, bool WARP>
+template <typename T, int V, int CH, int STAGES, bool WARP, int THREADS = 0>
 cudaError_t run(const NormBackwardArgs& b, int threads, int num_sms, cudaStream_t st, int* parts) {
   const NormArgs& a = b.f;
   const bool element = a.gate_kind == MOE_GATE_ELEMENT;
-  auto* k = a.h == nullptr ? norm_backward_kernel<T, V, CH, STAGES, false, true, false, WARP>
-            : a.next       ? (element ? norm_backward_kernel<T, V, CH, STAGES, true, true, true, WARP>
-                                      : norm_backward_kernel<T, V, CH, STAGES, true, true, false, WARP>)
-                           : (element ? norm_backward_kernel<T, V, CH, STAGES, true, false, true, WARP>
-                                      : norm_backward_kernel<T, V, CH, STAGES, true, false, false, WARP>);
+  auto* k = a.h == nullptr ? norm_backward_kernel<T, V, CH, STAGES, THREADS, false, true, false, WARP>
+            : a.next       ? (element ? norm_backward_kernel<T, V, CH, STAGES, THREADS, true, true, true, WARP>
+                                      : norm_backward_kernel<T, V, CH, STAGES, THREADS, true, true, false, WARP>)
+                           : (element ? norm_backward_kernel<T, V, CH, STAGES, THREADS, true, false, true, WARP>
+                                      : norm_backward_kernel<T, V, CH, STAGES, THREADS, true, false, false, WARP>);
   const int arrays = (b.dr != nullptr) + 2 * (a.next != 0) + (a.h != nullptr) + element;
   size_t smem = queue_smem<T, V, CH, STAGES>(a.H, arrays, threads);
   if (WARP) smem = std::max(smem, sizeof(float) * a.H);
-  else if (STAGES > 0 && V > 1) smem += sizeof(float) * 2 * CH * V * threads;
+  else if (STAGES > 0) smem += sizeof(float) * 2 * CH * V * threads;
   int blocks = std::max(1, (V == 1 && CH <= 8 ? 1024 : 512) / threads);
   if (smem > 0) blocks = std::max(1, std::min<int>(blocks, kQueueSmem / smem));
   if (smem > 40 * 1024) {
@@ -438,11 +444,13 @@ cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& b, int num_s
     } else if (vec && packs <= 1024) {
       e = run<T, V, 2, 2, false>(b, threads(2), num_sms, st, &parts);
     } else if (!vec && packs <= 1024) {
-      e = run<T, 1, 4, 2, false>(b, threads(4), num_sms, st, &parts);
+      e = run<T, 1, 4, 2, false, 256>(b, 256, num_sms, st, &parts);
+    } else if (!vec && packs <= 2048) {
+      e = run<T, 1, 8, 2, false, 256>(b, 256, num_sms, st, &parts);
     } else if (!vec && packs <= 4096) {
-      e = run<T, 1, 8, 2, false>(b, threads(8), num_sms, st, &parts);
+      e = run<T, 1, 8, 2, false, 512>(b, 512, num_sms, st, &parts);
     } else if (!vec && packs <= 8192) {
-      e = run<T, 1, 16, 0, false>(b, threads(16), num_sms, st, &parts);
+      e = run<T, 1, 16, 0, false, 512>(b, 512, num_sms, st, &parts);
     } else if (vec && packs <= 2048 && sizeof(T) == 4) {
       if constexpr (sizeof(T) == 4) e = run<T, V, 4, 0, false>(b, threads(4), num_sms, st, &parts);
     } else {

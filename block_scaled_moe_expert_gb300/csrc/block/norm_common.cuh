@@ -35,12 +35,14 @@ __host__ __device__ constexpr int loose_row_bytes(int H, int size) { return (H *
 // where they lie in them; one barrier a row.
 //   STAGES = 0: rows that are too long for shared memory are read from global
 // memory where they are used, a second time from the L1.
-template <typename T, int V, int CH, int ARRAYS, int STAGES>
+// THREADS: of a row, where the kernel is compiled for their number (an
+// element's place is then a constant away from the thread's), else 0.
+template <typename T, int V, int CH, int ARRAYS, int STAGES, int THREADS>
 struct RowQueue {
   static constexpr bool kLoose = V == 1 && STAGES > 0;
   const T* src[ARRAYS];  // null: absent; else, once started, where the row to fetch starts (for this thread)
   int64_t ld[ARRAYS];    // once started, the way to the block's next row
-  int H, threads, j;
+  int H, j;
   int put_left;          // rows still to fetch
   // STAGES > 0, in bytes: [STAGES][arrays present][a row]
   uint8_t* ring;
@@ -48,7 +50,8 @@ struct RowQueue {
   int array_at[ARRAYS];
   int phase[ARRAYS], phase_step[ARRAYS];  // loose rows: where in its first chunk the row in work starts
 
-  __device__ __forceinline__ int column(int i) const { return (i * threads + j) * V; }
+  __device__ __forceinline__ int threads() const { return THREADS > 0 ? THREADS : static_cast<int>(blockDim.x); }
+  __device__ __forceinline__ int column(int i) const { return (i * threads() + j) * V; }
 
   __device__ __forceinline__ void put() {
     if (put_left > 0) {
@@ -61,11 +64,11 @@ struct RowQueue {
           const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src[a]) & 15);
           const uint8_t* p = reinterpret_cast<const uint8_t*>(src[a]) - skip;
           const int bytes = skip + H * static_cast<int>(sizeof(T));
-          for (int at = j * 16; at < bytes; at += threads * 16) cp_async16_part(dst + at, p + at, min(16, bytes - at));
+          for (int at = j * 16; at < bytes; at += threads() * 16) cp_async16_part(dst + at, p + at, min(16, bytes - at));
         } else {
 #pragma unroll
           for (int i = 0; i < CH; ++i)
-            if (column(i) < H) cp_async16(dst + i * threads * 16, src[a] + i * threads * V);
+            if (column(i) < H) cp_async16(dst + i * threads() * 16, src[a] + i * threads() * V);
         }
         src[a] += ld[a];
       }
@@ -83,7 +86,7 @@ struct RowQueue {
       ld[a] *= step;
     }
     if constexpr (STAGES > 0) {
-      const int row_bytes = kLoose ? loose_row_bytes(H, sizeof(T)) : CH * threads * 16;
+      const int row_bytes = kLoose ? loose_row_bytes(H, sizeof(T)) : CH * threads() * 16;
       int present = 0;
 #pragma unroll
       for (int a = 0; a < ARRAYS; ++a) {
@@ -96,7 +99,7 @@ struct RowQueue {
       }
       stage_bytes = present * row_bytes;
       // (a warp's row has its own ring)
-      ring = static_cast<uint8_t*>(smem) + (threadIdx.x / threads) * (STAGES * stage_bytes) + (kLoose ? 0 : j * 16);
+      ring = static_cast<uint8_t*>(smem) + (threadIdx.x / threads()) * (STAGES * stage_bytes) + (kLoose ? 0 : j * 16);
       put_at = 0;
       get_at = -stage_bytes;
 #pragma unroll
@@ -127,8 +130,8 @@ struct RowQueue {
   __device__ __forceinline__ Pack<T, V> at(int a, int i) const {
     if constexpr (kLoose)
       return *reinterpret_cast<const Pack<T, V>*>(ring + get_at + array_at[a] + phase[a] + column(i) * sizeof(T));
-    else if constexpr (STAGES > 0) return *reinterpret_cast<const Pack<T, V>*>(ring + get_at + array_at[a] + i * threads * 16);
-    else return load_pack<V>(src[a] + i * threads * V);
+    else if constexpr (STAGES > 0) return *reinterpret_cast<const Pack<T, V>*>(ring + get_at + array_at[a] + i * threads() * 16);
+    else return load_pack<V>(src[a] + i * threads() * V);
   }
 };
 
