@@ -6,7 +6,6 @@
 // kernel. No arithmetic and no device code. The entry points come from the
 // library that `binding` loads, by address.
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/as_strided.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -151,8 +150,15 @@ struct Plan {
   int T, E, K, align;
   Tensor counts, offsets, inv, row_slot;  // made when asked for
 
-  Tensor part(Tensor& view, size_t at, std::initializer_list<int64_t> sizes, std::initializer_list<int64_t> strides) {
-    if (!view.defined()) view = at::as_strided(buffer, sizes, strides, static_cast<int64_t>(at / 4));
+  // A contiguous part of the buffer, without the dispatcher's way to a view
+  // (whole numbers have no gradient).
+  Tensor part(Tensor& view, size_t at, std::initializer_list<int64_t> sizes) {
+    if (!view.defined()) {
+      view = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
+      c10::TensorImpl* t = view.unsafeGetTensorImpl();
+      t->set_storage_offset(static_cast<int64_t>(at / 4));
+      t->set_sizes_contiguous(sizes);
+    }
     return view;
   }
 };
@@ -430,11 +436,11 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
       .def_readonly("K", &Plan::K)
       .def_readonly("align", &Plan::align)
       .def_property_readonly("row_capacity", [](const Plan& p) { return p.layout.row_capacity; })
-      .def_property_readonly("counts", [](Plan& p) { return p.part(p.counts, p.layout.counts, {p.E}, {1}); })
-      .def_property_readonly("offsets", [](Plan& p) { return p.part(p.offsets, p.layout.offsets, {p.E + 1}, {1}); })
-      .def_property_readonly("inv", [](Plan& p) { return p.part(p.inv, p.layout.inv, {p.T, p.K}, {p.K, 1}); })
+      .def_property_readonly("counts", [](Plan& p) { return p.part(p.counts, p.layout.counts, {p.E}); })
+      .def_property_readonly("offsets", [](Plan& p) { return p.part(p.offsets, p.layout.offsets, {p.E + 1}); })
+      .def_property_readonly("inv", [](Plan& p) { return p.part(p.inv, p.layout.inv, {p.T, p.K}); })
       .def_property_readonly("row_slot", [](Plan& p) {
-        return p.part(p.row_slot, p.layout.row_slot, {p.layout.row_capacity}, {1});
+        return p.part(p.row_slot, p.layout.row_slot, {p.layout.row_capacity});
       });
   m.def("sort_tokens", wrap_pybind_function(sort_tokens));
   m.def("move_rows", wrap_pybind_function(move_rows));
