@@ -104,19 +104,29 @@ __device__ __forceinline__ void ue8m0_scales(uint32_t word, float (&s)[4]) {
 }
 // The eight codes of a word minus zero as fp16 pairs: with the bits of 1024
 // above a code the half is 1024 + code, or 1024 + 16 code where the code sits
-// four bits up; both differences are exact. zero: 1024 + z.
-__device__ __forceinline__ void int4_pairs(uint32_t word, __half2 zero, uint32_t (&h)[4]) {
-  const __half2 up = __float2half2_rn(0.0625f);
-  const __half2 zero16 = __hsub2(__float2half2_rn(960.f), zero);  // -(64 + z)
-#pragma unroll
-  for (int p = 0; p < 4; p += 2) {
-    const uint32_t w = word >> (4 * p);
-    const uint32_t a = (w & 0x000F000Fu) | 0x64006400u, b = (w & 0x00F000F0u) | 0x64006400u;
-    const __half2 va = __hsub2(*reinterpret_cast<const __half2*>(&a), zero);
-    const __half2 vb = __hfma2(*reinterpret_cast<const __half2*>(&b), up, zero16);
-    h[p] = *reinterpret_cast<const uint32_t*>(&va);
-    h[p + 1] = *reinterpret_cast<const uint32_t*>(&vb);
-  }
+// four bits up; both differences are exact. zero: 1024 + z, zero16: -(64 + z).
+// (In PTX: from the half intrinsics the compiler made 20 cycles a word, not 13.)
+__device__ __forceinline__ uint32_t code_bits(uint32_t word, uint32_t mask) {
+  uint32_t d;  // (word & mask) | 0x64006400
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(word), "r"(mask), "r"(0x64006400u));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ void int4_pairs(uint32_t word, uint32_t zero, uint32_t zero16, uint32_t (&h)[4]) {
+  const uint32_t up = word >> 8, sixteenth = 0x2C002C00u;
+  h[0] = half2_sub(code_bits(word, 0x000F000Fu), zero);
+  h[1] = half2_fma(code_bits(word, 0x00F000F0u), sixteenth, zero16);
+  h[2] = half2_sub(code_bits(up, 0x000F000Fu), zero);
+  h[3] = half2_fma(code_bits(up, 0x00F000F0u), sixteenth, zero16);
 }
 
 // What a lane holds of one block.
@@ -125,10 +135,6 @@ struct Block {
   uint4 codes[2];
   uint32_t scale[SW];
 };
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
 
 // A block's way from global memory through a warp's ring.
 template <int BYTES>
@@ -187,8 +193,9 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
       s1 = scale[1][i];
     } else {
       const uint32_t sz0 = b.scale[2 * grp], sz1 = b.scale[2 * grp + 1];
-      int4_pairs(w0, __half2half2(__ushort_as_half(sz0 >> 16)), a0);
-      int4_pairs(w1, __half2half2(__ushort_as_half(sz1 >> 16)), a1);
+      const uint32_t z0 = __byte_perm(sz0, 0, 0x3232), z1 = __byte_perm(sz1, 0, 0x3232);
+      int4_pairs(w0, z0, half2_sub(0x63806380u, z0), a0);  // 960 - (1024 + z)
+      int4_pairs(w1, z1, half2_sub(0x63806380u, z1), a1);
       const uint16_t h0 = sz0 & 0xFFFF, h1 = sz1 & 0xFFFF;
       s0 = to_f32(*reinterpret_cast<const S*>(&h0));
       s1 = to_f32(*reinterpret_cast<const S*>(&h1));
@@ -199,16 +206,17 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
       else mma_16816(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y, c[n][0], c[n][1], c[n][2], c[n][3]);
       mma_16816(c[n], a0[2], a1[2], a0[3], a1[3], xv[n].z, xv[n].w, c[n][0], c[n][1], c[n][2], c[n][3]);
       if (last) {
+        float2 lo = make_float2(c[n][0], c[n][1]), hi = make_float2(c[n][2], c[n][3]);
         if constexpr (kScaledX<X>) {
-          c[n][0] *= back[n].x;
-          c[n][1] *= back[n].y;
-          c[n][2] *= back[n].x;
-          c[n][3] *= back[n].y;
+          lo = mul2(lo, back[n]);
+          hi = mul2(hi, back[n]);
         }
-        acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
-        acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
-        acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
-        acc[n][3] = fmaf(s1, c[n][3], acc[n][3]);
+        lo = fma2(lo, make_float2(s0, s0), make_float2(acc[n][0], acc[n][1]));
+        hi = fma2(hi, make_float2(s1, s1), make_float2(acc[n][2], acc[n][3]));
+        acc[n][0] = lo.x;
+        acc[n][1] = lo.y;
+        acc[n][2] = hi.x;
+        acc[n][3] = hi.y;
       }
     }
   }
@@ -254,7 +262,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   extern __shared__ __align__(16) uint8_t s_dyn[];
   __shared__ float s_red[kMvWarps][NT][4][32];
   __shared__ __align__(16) uint8_t s_zero[kMvStep * 2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same for the warp's lanes, as the compiler now knows
   const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int first_step = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.cluster);
   const int cta_steps = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.cluster) - first_step;
@@ -265,8 +274,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   const int rounds = (a.tiles - cluster_id * groups + tile_step - 1) / tile_step;  // of this CTA
   uint8_t* ring = s_dyn + warp * (DEPTH * BYTES);
   uint8_t* s_x = s_dyn + kMvWarps * DEPTH * BYTES;
-  pdl_wait();
-  pdl_launch_dependents();
 
   // the next block to fetch, and its slot
   int f_tile = tile0, f_s = 0, f_slot = 0;
@@ -282,11 +289,16 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
         f_at += tile_step * tile_bytes - static_cast<size_t>(ns) * BYTES;
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_async_commit();
     f_slot = f_slot + BYTES == DEPTH * BYTES ? 0 : f_slot + BYTES;
   };
 #pragma unroll
   for (int d = 0; d < DEPTH - 1; ++d) fetch();
+  // The weights are on their way before the kernel in front has finished: they
+  // were laid out before it (the layout kernel lets nothing start before its
+  // end). x and y are touched after it.
+  pdl_wait();
+  pdl_launch_dependents();
 
   // x: this CTA's K range as fp16, rows 64 bytes apart modulo 128 (the four
   // 16-byte reads of two tokens fill the banks), then the powers [step][token]
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   auto multiply = [&](const uint8_t* const (&x_at)[NT], const float* p_at) {  // the next block of the ring
     __syncwarp();  // every lane is done with the slot that is fetched into
     fetch();
-    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    cp_async_wait<DEPTH - 1>();
     __syncwarp();  // every lane's share has arrived
     Block<SW> b;
     read_block(b, ring + at_slot, lane);
@@ -432,8 +444,7 @@ __global__ void __launch_bounds__(256)
 matvec_prepare_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scale,
                       const uint8_t* __restrict__ zero, uint8_t* __restrict__ out, int N, int K, int group,
                       bool swiglu, int steps) {
-  pdl_wait();
-  pdl_launch_dependents();
+  // no early launch of dependents: moe_matvec fetches the weights without waiting
   const int tile = blockIdx.x, step = blockIdx.y;
   const int bytes = block_bytes(FMT, group), per_row = (K + group - 1) / group;
   uint8_t* dst = out + (static_cast<size_t>(tile) * steps + step) * bytes;
@@ -502,13 +513,15 @@ cudaError_t run(const MvArgs& a, int grid, cudaStream_t st) {
   cfg.blockDim = kMvThreads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = a.cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 

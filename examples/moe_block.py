@@ -104,7 +104,7 @@ def train(steps=5, T=512, H=256, I=128, E=8, K=2):
         loss = ((y - target).float() ** 2).mean()
         loss.backward()
         opt.step()
-        losses.append(float(loss))
+        losses.append(float(loss.detach()))
     return losses
 
 
