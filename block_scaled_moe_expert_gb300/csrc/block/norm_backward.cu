@@ -12,7 +12,11 @@
 // registers: sum_t gate inv G h, from which the weight's gradient (times
 // alpha g) and the channel gate's (times alpha act' w) both follow, and the
 // next weight's. A second small kernel adds the blocks' sums in block order,
-// so the same call gives the same bits. Bound by DRAM bandwidth.
+// so the same call gives the same bits. A row needs one barrier: G is linear in
+// dr, w dy and r, so the sums that dh needs are taken for the three apart,
+// beside the sums that G needs,
+//   sum h w g G = sum h w g dr + inv_r sum h w g (w' dy) - back sum h w g r.
+// Bound by DRAM bandwidth.
 #include "norm_common.cuh"
 
 namespace bsmoe {
@@ -32,14 +36,15 @@ __device__ __forceinline__ float* partial_row(const NormBackwardArgs& b, int whi
 
 // One row per warp (WARP) or per block. ELEMENT: a gate by element.
 template <typename T, int V, int CH, int STAGES, int THREADS, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) ? 2 : 1)
     norm_backward_kernel(NormBackwardArgs b) {
   constexpr int ARRAYS = AFTER ? ELEMENT ? 5 : 4 : 3;
   // the columns' factors stand in shared memory behind the ring (each thread
   // its own): beside the column sums they would not fit into the registers
   constexpr bool CACHED = STAGES > 0 && !WARP;
   extern __shared__ __align__(16) uint8_t s_ring[];
-  __shared__ float s_sum[2][2][2][32];
+  constexpr int SUMS = AFTER ? NEXT ? 8 : 2 : 2;
+  __shared__ __align__(16) float s_sum[2][SUMS * 16];  // by the row's parity
   const NormArgs& a = b.f;
   RowQueue<T, V, CH, ARRAYS, STAGES, WARP ? 32 : THREADS> rows;
   rows.H = a.H;
@@ -111,6 +116,10 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
       }
     }
   }
+  if (!WARP) {
+    for (int i = threadIdx.x; i < 2 * SUMS * 16; i += blockDim.x) (&s_sum[0][0])[i] = 0.f;
+    __syncthreads();
+  }
   const float inv_h = 1.f / static_cast<float>(a.H);
   Values<V> sums[2][CH];
 #pragma unroll
@@ -120,91 +129,92 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, V == 1 && CH <= 8 ? 2 : 1)
   T* dh_out = static_cast<T*>(b.dh) + out_first;
   T* dg_out = static_cast<T*>(b.d_gate) + (ELEMENT ? out_first : first);
   const T* token_gate = static_cast<const T*>(a.gate) + first * a.ld_gate;
+  const bool has_dr = b.dr != nullptr;
   for (int k = 0; k < n; ++k) {
     rows.next();
-    Values<V> G[CH];
+    float2 rr = make_float2(0.f, 0.f), rd = rr, hh = rr, h_dr = rr, h_dy = rr, h_r = rr;
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
-      G[i] = b.dr != nullptr && rows.column(i) < a.H ? values(rows.at(kDr, i)) : zeros<V>();
-    if constexpr (NEXT) {
-      float2 rr = make_float2(0.f, 0.f), rd = rr;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = rows.column(i);
-        if (c >= a.H) continue;
-        const Values<V> r = values(rows.at(kR, i)), dy = values(rows.at(kDy, i));
+    for (int i = 0; i < CH; ++i) {
+      const int c = rows.column(i);
+      if (c >= a.H) continue;
+      Values<V> r, d;
+      if constexpr (NEXT) {
+        r = values(rows.at(kR, i));
+        d = get_factor(kSumNext, i, c) * values(rows.at(kDy, i));
         add_dot(rr, r, r);
-        add_dot(rd, r, get_factor(kSumNext, i, c) * dy);
+        add_dot(rd, r, d);
       }
-      float sum[2] = {rr.x + rr.y, rd.x + rd.y};
-      row_sum<2, WARP>(sum, s_sum[k & 1][0]);
-      const float inv = rsqrtf(sum[0] * inv_h + a.next_eps);
-      const float back = inv * inv * (inv * (sum[1] * inv_h));
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = rows.column(i);
-        if (c >= a.H) continue;
-        const Values<V> r = values(rows.at(kR, i)), d = values(rows.at(kDy, i)) * inv;
-        G[i] = fma(r, -back, fma(d, get_factor(kSumNext, i, c), G[i]));
-        sums[kSumNext][i] = fma(d, r, sums[kSumNext][i]);
+      if constexpr (AFTER) {
+        const Values<V> h = values(rows.at(kH, i));
+        Values<V> u = h * get_factor(kSumBlock, i, c);
+        if constexpr (ELEMENT) u = u * gate_values(a.gate_act, values(rows.at(kGate, i)));
+        add_dot(hh, h, h);
+        if (has_dr) add_dot(h_dr, u, values(rows.at(kDr, i)));
+        if constexpr (NEXT) {
+          add_dot(h_dy, u, d);
+          add_dot(h_r, u, r);
+        }
       }
     }
-    if (dx_out != nullptr) {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        if (rows.column(i) >= a.H) continue;
-        store_pack(dx_out + i * rows.threads() * V, pack<T, V>((a.beta != 1.f ? G[i] * a.beta : G[i]).v));
-      }
-      dx_out += out_step;
+    float inv_r = 0.f, back_r = 0.f, inv = 1.f, back = 0.f, h_G = 0.f;
+    if constexpr (AFTER && NEXT) {
+      float v[8] = {rr.x + rr.y, rd.x + rd.y, hh.x + hh.y, h_dr.x + h_dr.y, h_dy.x + h_dy.y, h_r.x + h_r.y, 0.f, 0.f};
+      row_sums<8, WARP>(v, s_sum[k & 1]);
+      inv_r = rsqrtf(v[0] * inv_h + a.next_eps);
+      back_r = inv_r * inv_r * (inv_r * (v[1] * inv_h));
+      inv = rsqrtf(v[2] * inv_h + a.eps);
+      h_G = fmaf(-back_r, v[5], fmaf(inv_r, v[4], v[3]));
+    } else if constexpr (NEXT) {
+      float v[2] = {rr.x + rr.y, rd.x + rd.y};
+      row_sums<2, WARP>(v, s_sum[k & 1]);
+      inv_r = rsqrtf(v[0] * inv_h + a.next_eps);
+      back_r = inv_r * inv_r * (inv_r * (v[1] * inv_h));
+    } else {
+      float v[2] = {hh.x + hh.y, h_dr.x + h_dr.y};
+      row_sums<2, WARP>(v, s_sum[k & 1]);
+      inv = rsqrtf(v[0] * inv_h + a.eps);
+      h_G = v[1];
     }
+    float gt = 1.f;
     if constexpr (AFTER) {
-      float gt = 1.f, gt_slope = 0.f;
+      if (!a.norm) inv = 1.f;
+      else back = inv * inv * (inv * (h_G * inv_h));
       if (a.gate_kind == MOE_GATE_TOKEN) {
         gt = gate_value(a.gate_act, to_f32(*token_gate));
-        gt_slope = gate_slope(a.gate_act, gt);
         token_gate += step * a.ld_gate;
+        if (rows.j == 0) *dg_out = from_f32<T>(gate_slope(a.gate_act, gt) * (a.alpha * (inv * h_G)));
       }
-      float inv = 1.f, back = 0.f;
-      if (a.norm || a.gate_kind == MOE_GATE_TOKEN) {
-        float2 hh = make_float2(0.f, 0.f), hu = hh;
+    }
+    const float scale = a.alpha * gt;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int c = rows.column(i);
-          if (c >= a.H) continue;
-          const Values<V> h = values(rows.at(kH, i));
-          Values<V> u = get_factor(kSumBlock, i, c) * G[i];
-          if constexpr (ELEMENT) u = u * gate_values(a.gate_act, values(rows.at(kGate, i)));
-          add_dot(hh, h, h);
-          add_dot(hu, h, u);
-        }
-        float sum[2] = {hh.x + hh.y, hu.x + hu.y};
-        row_sum<2, WARP>(sum, s_sum[k & 1][1]);
-        if (a.norm) {
-          inv = rsqrtf(sum[0] * inv_h + a.eps);
-          back = inv * inv * (inv * (sum[1] * inv_h));
-        }
-        if (a.gate_kind == MOE_GATE_TOKEN && rows.j == 0) *dg_out = from_f32<T>(gt_slope * (a.alpha * (inv * sum[1])));
+    for (int i = 0; i < CH; ++i) {
+      const int c = rows.column(i);
+      if (c >= a.H) continue;
+      Values<V> G = has_dr ? values(rows.at(kDr, i)) : zeros<V>();
+      if constexpr (NEXT) {
+        const Values<V> r = values(rows.at(kR, i)), d = values(rows.at(kDy, i)) * inv_r;
+        G = fma(r, -back_r, fma(d, get_factor(kSumNext, i, c), G));
+        sums[kSumNext][i] = fma(d, r, sums[kSumNext][i]);
       }
-      const float scale = a.alpha * gt;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = rows.column(i);
-        if (c >= a.H) continue;
+      if (dx_out != nullptr)
+        store_pack(dx_out + i * rows.threads() * V, pack<T, V>((a.beta != 1.f ? G * a.beta : G).v));
+      if constexpr (AFTER) {
         const Values<V> h = values(rows.at(kH, i)), w = get_factor(kSumBlock, i, c);
-        if constexpr (ELEMENT) {
+        if constexpr (ELEMENT) {  // its gradient takes the G without it
           const Values<V> g = gate_values(a.gate_act, values(rows.at(kGate, i)));
-          Values<V> dg = G[i] * (h * (a.alpha * inv)) * w;
+          Values<V> dg = G * (h * (a.alpha * inv)) * w;
 #pragma unroll
           for (int e = 0; e < V; ++e) dg.v[e] *= gate_slope(a.gate_act, g.v[e]);
           store_pack(dg_out + i * rows.threads() * V, pack<T, V>(dg.v));
-          G[i] = G[i] * g;
+          G = G * g;
         }
-        sums[kSumBlock][i] = fma(G[i] * (gt * inv), h, sums[kSumBlock][i]);
-        store_pack(dh_out + i * rows.threads() * V, pack<T, V>(fma(h, -scale * back, w * (G[i] * (scale * inv))).v));
+        sums[kSumBlock][i] = fma(G * (gt * inv), h, sums[kSumBlock][i]);
+        store_pack(dh_out + i * rows.threads() * V, pack<T, V>(fma(h, -scale * back, w * (G * (scale * inv))).v));
       }
-      dh_out += out_step;
-      dg_out += ELEMENT ? out_step : step;
     }
+    if (dx_out != nullptr) dx_out += out_step;
+    dh_out += out_step;
+    dg_out += ELEMENT ? out_step : step;
   }
 
   float* s_cols = reinterpret_cast<float*>(s_ring);  // WARP: the join of the block's warps, after the rows

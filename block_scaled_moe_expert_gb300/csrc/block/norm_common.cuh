@@ -153,6 +153,45 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*s)[32]) {
   }
 }
 
+// P sums (1, 2, 4 or 8) over the threads of a row at the price of about two: in
+// the first steps the lanes halve the values between them, so that a lane ends
+// with one value's sum over its warp; one barrier. s: [P][16] floats of the
+// block, zero behind its last warp, used again two rows on at the earliest (see
+// row_sum).
+template <int P, bool WARP>
+__device__ __forceinline__ void row_sums(float (&v)[P], float* s) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = 32 / P;  // that share a value
+  int o = 16;
+#pragma unroll
+  for (int half = P / 2; half > 0; half /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  float t = v[0];
+#pragma unroll
+  for (int x = kLanes / 2; x > 0; x /= 2) t += __shfl_xor_sync(0xffffffffu, t, x);
+  if (!WARP) {
+    if (lane % kLanes == 0) s[lane / kLanes * 16 + (threadIdx.x >> 5)] = t;
+    __syncthreads();
+    constexpr int kEach = P >= 2 ? 16 / kLanes > 0 ? 16 / kLanes : 1 : 1;
+    t = 0.f;
+    if (lane % kLanes < 16 / kEach) {
+      const Pack<float, kEach> p = load_pack<kEach>(s + lane / kLanes * 16 + lane % kLanes * kEach);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) t += p.e[i];
+    }
+#pragma unroll
+    for (int x = kLanes / 2; x > 0; x /= 2) t += __shfl_xor_sync(0xffffffffu, t, x);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * kLanes);
+}
+
 // V fp32 values of a pack, in pairs where there are pairs.
 template <int V>
 struct Values {
