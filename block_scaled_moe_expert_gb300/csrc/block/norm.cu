@@ -19,14 +19,18 @@ enum { kX = 0, kH = 1, kGate = 2 };
 
 // One row per warp (WARP) or per block. ELEMENT: a gate
 // by element.
-template <typename T, int V, int CH, int STAGES, int THREADS, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 512, WARP ? 8 : V == 1 && CH <= 16 ? 2 : 1)
+template <typename T, int V, int CH, int STAGES, int THREADS, bool AFTER, bool NEXT, bool ELEMENT, bool WARP, bool SHIFT>
+__global__ void __launch_bounds__(WARP ? 128 : THREADS > 0 ? THREADS : CH * V <= 16 ? 1024 : 512,
+                  WARP ? 8 : THREADS > 0 && CH <= 16 ? 1024 / (THREADS + !THREADS) : 1)
     norm_kernel(NormArgs a) {
   constexpr int ARRAYS = AFTER ? ELEMENT ? 3 : 2 : 1;
-  constexpr bool CACHED = CH * V <= 8;  // the columns' factors stay in registers
+  // the columns' factors stay in registers, or for many columns of loose rows
+  // (each a branch on the weights' type to load) in shared memory behind the
+  // ring, each thread its own
+  constexpr bool CACHED = CH * V <= 8, SHARED = !CACHED && V == 1 && STAGES > 0;
   extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ float s_sum[2][2][1][32];  // by the row's parity: a row's sums do not wait for the row before
-  RowQueue<T, V, CH, ARRAYS, STAGES, WARP ? 32 : THREADS> rows;
+  RowQueue<T, V, CH, ARRAYS, STAGES, WARP ? 32 : THREADS, SHIFT> rows;
   rows.H = a.H;
   rows.j = WARP ? threadIdx.x & 31 : threadIdx.x;
   rows.src[kX] = static_cast<const T*>(a.x);
@@ -44,27 +48,57 @@ __global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 51
   const int per_block = WARP ? blockDim.x / 32 : 1;
   const int first = blockIdx.x * per_block + (WARP ? threadIdx.x >> 5 : 0), step = gridDim.x * per_block;
   const int n = first < a.T ? (a.T - 1 - first) / step + 1 : 0;
+  rows.set_shift(AFTER ? a.r : a.y, first);
   rows.start(first, step, n, s_ring);
 
   auto factor = [&](int c) {  // alpha w g of the columns
-    Values<V> f = load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c);
-    if (a.gate_kind == MOE_GATE_CHANNEL) f = f * channel_gate<T, V>(a, c);
-    return f * a.alpha;
+    return column_factor<SHIFT, V>(
+        c, a.H,
+        [&](int at) {
+          Values<V> f = load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, at);
+          if (a.gate_kind == MOE_GATE_CHANNEL) f = f * channel_gate<T, V>(a, at);
+          return f * a.alpha;
+        },
+        [&](int at) {
+          const float w = load_weight<T, 1>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, at).v[0];
+          return a.alpha * (a.gate_kind == MOE_GATE_CHANNEL ? w * channel_gate<T, 1>(a, at).v[0] : w);
+        });
   };
-  Values<V> wa[CH], wn[CH];
-  if (CACHED) {
+  auto next_factor = [&](int c) {
+    return column_factor<SHIFT, V>(
+        c, a.H, [&](int at) { return load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, at); },
+        [&](int at) { return load_weight<T, 1>(a.next_weight, a.weight_f32, a.w_offset, at).v[0]; });
+  };
+  Values<V> wa[CACHED ? CH : 1], wn[CACHED ? CH : 1];
+  Values<V>* s_factor = reinterpret_cast<Values<V>*>(s_ring + (SHARED ? STAGES * rows.stage_bytes : 0)) + rows.j;
+  if (CACHED || SHARED) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = rows.column(i);
-      if (c >= a.H) continue;
-      if (AFTER) wa[i] = factor(c);
-      if (NEXT) wn[i] = load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c);
+      if (!rows.in(i)) continue;
+      if constexpr (CACHED) {
+        if (AFTER) wa[i] = factor(c);
+        if (NEXT) wn[i] = next_factor(c);
+      } else {
+        if (AFTER) s_factor[i * rows.threads()] = factor(c);
+        if (NEXT) s_factor[(CH + i) * rows.threads()] = next_factor(c);
+      }
     }
   }
+  auto factor_of = [&](int i, int c) {
+    if constexpr (CACHED) return wa[i];
+    else if constexpr (SHARED) return s_factor[i * rows.threads()];
+    else return factor(c);
+  };
+  auto next_factor_of = [&](int i, int c) {
+    if constexpr (CACHED) return wn[i];
+    else if constexpr (SHARED) return s_factor[(CH + i) * rows.threads()];
+    else return next_factor(c);
+  };
   const float inv_h = 1.f / static_cast<float>(a.H);
   const int64_t out_step = static_cast<int64_t>(step) * a.H;
-  T* r_out = static_cast<T*>(a.r) + static_cast<int64_t>(first) * a.H + rows.j * V;
-  T* y_out = static_cast<T*>(a.y) + static_cast<int64_t>(first) * a.H + rows.j * V;
+  T* r_out = static_cast<T*>(a.r) + static_cast<int64_t>(first) * a.H + rows.j * V - rows.shift;
+  T* y_out = static_cast<T*>(a.y) + static_cast<int64_t>(first) * a.H + rows.j * V - rows.shift;
   const T* token_gate = static_cast<const T*>(a.gate) + first * a.ld_gate;
   for (int k = 0; k < n; ++k, r_out += out_step, y_out += out_step) {
     rows.next();
@@ -72,7 +106,7 @@ __global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 51
     if constexpr (AFTER) {
       float scale = 1.f;
 #pragma unroll
-      for (int i = 0; i < CH; ++i) r[i] = rows.column(i) < a.H ? values(rows.at(kH, i)) : zeros<V>();
+      for (int i = 0; i < CH; ++i) r[i] = rows.in(i) ? row_values(rows, kH, i) : zeros<V>();
       if (a.norm) {
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
@@ -88,16 +122,16 @@ __global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 51
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = rows.column(i);
-        if (c >= a.H) continue;
-        Values<V> x = values(rows.at(kX, i));
+        if (!rows.in(i)) continue;
+        Values<V> x = row_values(rows, kX, i);
         if (a.beta != 1.f) x = x * a.beta;
-        if constexpr (ELEMENT) r[i] = r[i] * gate_values(a.gate_act, values(rows.at(kGate, i)));
-        r[i] = fma(r[i] * scale, CACHED ? wa[i] : factor(c), x);
-        store_pack(r_out + i * rows.threads() * V, pack<T, V>(r[i].v));
+        if constexpr (ELEMENT) r[i] = r[i] * gate_values(a.gate_act, row_values(rows, kGate, i));
+        r[i] = fma(r[i] * scale, factor_of(i, c), x);
+        store_values(rows, r_out, i, r[i]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) r[i] = rows.column(i) < a.H ? values(rows.at(kX, i)) : zeros<V>();
+      for (int i = 0; i < CH; ++i) r[i] = rows.in(i) ? row_values(rows, kX, i) : zeros<V>();
     }
     if constexpr (NEXT) {
       float2 ss = make_float2(0.f, 0.f);
@@ -109,24 +143,24 @@ __global__ void __launch_bounds__(WARP ? 128 : V > 1 && CH * V <= 16 ? 1024 : 51
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = rows.column(i);
-        if (c >= a.H) continue;
-        const Values<V> w = CACHED ? wn[i] : load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c);
-        store_pack(y_out + i * rows.threads() * V, pack<T, V>((r[i] * scale * w).v));
+        if (!rows.in(i)) continue;
+        store_values(rows, y_out, i, r[i] * scale * next_factor_of(i, c));
       }
     }
   }
 }
 
-template <typename T, int V, int CH, int STAGES, bool WARP, int THREADS = 0>
+template <typename T, int V, int CH, int STAGES, bool WARP, int THREADS = 0, bool SHIFT = false>
 cudaError_t run(const NormArgs& a, int threads, int num_sms, cudaStream_t st) {
   const bool element = a.gate_kind == MOE_GATE_ELEMENT;
-  auto* k = a.h == nullptr ? norm_kernel<T, V, CH, STAGES, THREADS, false, true, false, WARP>
-            : a.next       ? (element ? norm_kernel<T, V, CH, STAGES, THREADS, true, true, true, WARP>
-                                      : norm_kernel<T, V, CH, STAGES, THREADS, true, true, false, WARP>)
-                           : (element ? norm_kernel<T, V, CH, STAGES, THREADS, true, false, true, WARP>
-                                      : norm_kernel<T, V, CH, STAGES, THREADS, true, false, false, WARP>);
+  auto* k = a.h == nullptr ? norm_kernel<T, V, CH, STAGES, THREADS, false, true, false, WARP, SHIFT>
+            : a.next       ? (element ? norm_kernel<T, V, CH, STAGES, THREADS, true, true, true, WARP, SHIFT>
+                                      : norm_kernel<T, V, CH, STAGES, THREADS, true, true, false, WARP, SHIFT>)
+                           : (element ? norm_kernel<T, V, CH, STAGES, THREADS, true, false, true, WARP, SHIFT>
+                                      : norm_kernel<T, V, CH, STAGES, THREADS, true, false, false, WARP, SHIFT>);
   const int arrays = a.h == nullptr ? 1 : element ? 3 : 2;
-  const size_t smem = queue_smem<T, V, CH, STAGES>(a.H, arrays, threads);
+  size_t smem = queue_smem<T, V, CH, STAGES>(a.H, arrays, threads);
+  if (V == 1 && STAGES > 0 && CH > 8) smem += sizeof(float) * 2 * CH * threads;
   // 1024 threads an SM (512 with many columns a thread), fewer blocks where
   // their rows in flight would not fit
   int blocks = std::max(1, (CH * V <= 16 ? 1024 : 512) / threads);
@@ -135,7 +169,9 @@ cudaError_t run(const NormArgs& a, int threads, int num_sms, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const int grid = std::min(ceil_div(a.T, WARP ? threads / 32 : 1), blocks * num_sms);
+  const int rows = ceil_div(a.T, WARP ? threads / 32 : 1);
+  int grid = std::min(rows, blocks * num_sms);
+  if (SHIFT) grid = shifted_grid(grid, rows);
   return launch_kernel(true, k, grid, threads, smem, st, a);
 }
 
@@ -148,14 +184,23 @@ cudaError_t launch_norm(int dtype, const NormArgs& a, int num_sms, cudaStream_t 
         a.H, {a.x, a.h, a.weight, a.next_weight, a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate, a.r, a.y},
         {a.ld_x, a.ld_h, a.gate_kind == MOE_GATE_ELEMENT ? a.ld_gate : 0});
     constexpr int V = kVec<T>;
-    const int packs = vec ? a.H / V : a.H;
+    const bool shift =
+        !vec && rows_shift_alike<T>(a.T, a.H, {a.x, a.h, a.gate_kind == MOE_GATE_ELEMENT ? a.gate : nullptr, a.r, a.y},
+                                    {a.ld_x, a.h != nullptr ? a.ld_h : a.H, a.gate_kind == MOE_GATE_ELEMENT ? a.ld_gate : a.H});
+    // (the last packs of a shifted row reach at most V - 1 elements beyond it)
+    const int packs = vec ? a.H / V : shift ? ceil_div(a.H + V - 1, V) : a.H;
     auto threads = [&](int ch) { return ceil_div(ceil_div(packs, ch), 32) * 32; };
+    if (shift && packs <= 1024) return run<T, V, 1, 4, false, 0, true>(a, threads(1), num_sms, st);
+    if constexpr (sizeof(T) == 4)
+      if (shift && packs <= 2048) return run<T, V, 2, 2, false, 0, true>(a, threads(2), num_sms, st);
     if (!vec) {
-      if (packs <= 1024) return run<T, 1, 4, 3, false, 256>(a, 256, num_sms, st);
-      if (packs <= 2048) return run<T, 1, 8, 3, false, 256>(a, 256, num_sms, st);
-      if (packs <= 4096) return run<T, 1, 8, 3, false, 512>(a, 512, num_sms, st);
-      if (packs <= 8192) return run<T, 1, 16, 2, false, 512>(a, 512, num_sms, st);
-      return run<T, 1, 32, 0, false, 512>(a, 512, num_sms, st);
+      if (a.H <= 1024) return run<T, 1, 4, 3, false, 256>(a, 256, num_sms, st);
+      if (a.H <= 2048) return run<T, 1, 8, 3, false, 256>(a, 256, num_sms, st);
+      if (a.H <= 4096) return run<T, 1, 16, 3, false, 256>(a, 256, num_sms, st);
+      if (a.H > 8192) return run<T, 1, 32, 0, false, 512>(a, 512, num_sms, st);
+      // three arrays' rows of 8192 fp32 columns do not fit into shared memory
+      if constexpr (sizeof(T) == 4) return run<T, 1, 16, 0, false, 512>(a, 512, num_sms, st);
+      else return run<T, 1, 16, 2, false, 512>(a, 512, num_sms, st);
     }
     if (packs <= 32) return run<T, V, 1, 4, true>(a, 128, num_sms, st);
     if (packs <= 64) return run<T, V, 2, 4, true>(a, 128, num_sms, st);

@@ -35,8 +35,8 @@ __device__ __forceinline__ float* partial_row(const NormBackwardArgs& b, int whi
 }
 
 // One row per warp (WARP) or per block. ELEMENT: a gate by element.
-template <typename T, int V, int CH, int STAGES, int THREADS, bool AFTER, bool NEXT, bool ELEMENT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) ? 2 : 1)
+template <typename T, int V, int CH, int STAGES, int THREADS, bool AFTER, bool NEXT, bool ELEMENT, bool WARP, bool SHIFT>
+__global__ void __launch_bounds__(WARP ? 256 : THREADS > 0 ? THREADS : 512, WARP ? 2 : THREADS == 256 ? CH <= 8 ? 4 : 3 : 1)
     norm_backward_kernel(NormBackwardArgs b) {
   constexpr int ARRAYS = AFTER ? ELEMENT ? 5 : 4 : 3;
   // the columns' factors stand in shared memory behind the ring (each thread
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
   constexpr int SUMS = AFTER ? NEXT ? 8 : 2 : 2;
   __shared__ __align__(16) float s_sum[2][SUMS * 16];  // by the row's parity
   const NormArgs& a = b.f;
-  RowQueue<T, V, CH, ARRAYS, STAGES, WARP ? 32 : THREADS> rows;
+  RowQueue<T, V, CH, ARRAYS, STAGES, WARP ? 32 : THREADS, SHIFT> rows;
   rows.H = a.H;
   rows.j = WARP ? threadIdx.x & 31 : threadIdx.x;
   rows.src[kDr] = static_cast<const T*>(b.dr);
@@ -69,13 +69,22 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
   const int per_block = WARP ? blockDim.x / 32 : 1;
   const int first = blockIdx.x * per_block + (WARP ? warp : 0), step = gridDim.x * per_block;
   const int n = first < a.T ? (a.T - 1 - first) / step + 1 : 0;
+  rows.set_shift(AFTER ? b.dh : b.dx, first);
   rows.start(first, step, n, s_ring);
 
   auto factor = [&](int which, int c) {  // w times the channel gate, or the next w
-    if (which == kSumNext) return load_weight<T, V>(a.next_weight, a.weight_f32, a.w_offset, c);
-    Values<V> f = load_weight<T, V>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c);
-    if (a.gate_kind == MOE_GATE_CHANNEL) f = f * channel_gate<T, V>(a, c);
-    return f;
+    const void* weight = which == kSumNext ? a.next_weight : a.norm ? a.weight : nullptr;
+    const bool gated = which == kSumBlock && a.gate_kind == MOE_GATE_CHANNEL;
+    return column_factor<SHIFT, V>(
+        c, a.H,
+        [&](int at) {
+          const Values<V> f = load_weight<T, V>(weight, a.weight_f32, a.w_offset, at);
+          return gated ? f * channel_gate<T, V>(a, at) : f;
+        },
+        [&](int at) {
+          const float f = load_weight<T, 1>(weight, a.weight_f32, a.w_offset, at).v[0];
+          return gated ? f * channel_gate<T, 1>(a, at).v[0] : f;
+        });
   };
   constexpr int F = V > 1 ? 4 : 1;  // floats of a factor that move together
   using FactorPack = Pack<float, F>;
@@ -101,7 +110,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = rows.column(i);
-      if (c >= a.H) continue;
+      if (!rows.in(i)) continue;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         if (which == kSumBlock ? !AFTER : !NEXT) continue;
@@ -124,7 +133,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
   Values<V> sums[2][CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) sums[0][i] = sums[1][i] = zeros<V>();
-  const int64_t out_step = static_cast<int64_t>(step) * a.H, out_first = static_cast<int64_t>(first) * a.H + rows.j * V;
+  const int64_t out_step = static_cast<int64_t>(step) * a.H, out_first = static_cast<int64_t>(first) * a.H + rows.j * V - rows.shift;
   T* dx_out = b.dx != nullptr ? static_cast<T*>(b.dx) + out_first : nullptr;
   T* dh_out = static_cast<T*>(b.dh) + out_first;
   T* dg_out = static_cast<T*>(b.d_gate) + (ELEMENT ? out_first : first);
@@ -136,20 +145,20 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = rows.column(i);
-      if (c >= a.H) continue;
+      if (!rows.in(i)) continue;
       Values<V> r, d;
       if constexpr (NEXT) {
-        r = values(rows.at(kR, i));
-        d = get_factor(kSumNext, i, c) * values(rows.at(kDy, i));
+        r = row_values(rows, kR, i);
+        d = get_factor(kSumNext, i, c) * row_values(rows, kDy, i);
         add_dot(rr, r, r);
         add_dot(rd, r, d);
       }
       if constexpr (AFTER) {
-        const Values<V> h = values(rows.at(kH, i));
+        const Values<V> h = row_values(rows, kH, i);
         Values<V> u = h * get_factor(kSumBlock, i, c);
-        if constexpr (ELEMENT) u = u * gate_values(a.gate_act, values(rows.at(kGate, i)));
+        if constexpr (ELEMENT) u = u * gate_values(a.gate_act, row_values(rows, kGate, i));
         add_dot(hh, h, h);
-        if (has_dr) add_dot(h_dr, u, values(rows.at(kDr, i)));
+        if (has_dr) add_dot(h_dr, u, row_values(rows, kDr, i));
         if constexpr (NEXT) {
           add_dot(h_dy, u, d);
           add_dot(h_r, u, r);
@@ -189,27 +198,27 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = rows.column(i);
-      if (c >= a.H) continue;
-      Values<V> G = has_dr ? values(rows.at(kDr, i)) : zeros<V>();
+      if (!rows.in(i)) continue;
+      Values<V> G = has_dr ? row_values(rows, kDr, i) : zeros<V>();
       if constexpr (NEXT) {
-        const Values<V> r = values(rows.at(kR, i)), d = values(rows.at(kDy, i)) * inv_r;
+        const Values<V> r = row_values(rows, kR, i), d = row_values(rows, kDy, i) * inv_r;
         G = fma(r, -back_r, fma(d, get_factor(kSumNext, i, c), G));
         sums[kSumNext][i] = fma(d, r, sums[kSumNext][i]);
       }
       if (dx_out != nullptr)
-        store_pack(dx_out + i * rows.threads() * V, pack<T, V>((a.beta != 1.f ? G * a.beta : G).v));
+        store_values(rows, dx_out, i, a.beta != 1.f ? G * a.beta : G);
       if constexpr (AFTER) {
-        const Values<V> h = values(rows.at(kH, i)), w = get_factor(kSumBlock, i, c);
+        const Values<V> h = row_values(rows, kH, i), w = get_factor(kSumBlock, i, c);
         if constexpr (ELEMENT) {  // its gradient takes the G without it
-          const Values<V> g = gate_values(a.gate_act, values(rows.at(kGate, i)));
+          const Values<V> g = gate_values(a.gate_act, row_values(rows, kGate, i));
           Values<V> dg = G * (h * (a.alpha * inv)) * w;
 #pragma unroll
           for (int e = 0; e < V; ++e) dg.v[e] *= gate_slope(a.gate_act, g.v[e]);
-          store_pack(dg_out + i * rows.threads() * V, pack<T, V>(dg.v));
+          store_values(rows, dg_out, i, dg);
           G = G * g;
         }
         sums[kSumBlock][i] = fma(G * (gt * inv), h, sums[kSumBlock][i]);
-        store_pack(dh_out + i * rows.threads() * V, pack<T, V>(fma(h, -scale * back, w * (G * (scale * inv))).v));
+        store_values(rows, dh_out, i, fma(h, -scale * back, w * (G * (scale * inv))));
       }
     }
     if (dx_out != nullptr) dx_out += out_step;
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
           const int c = rows.column(i);
-          if (c >= a.H) continue;
+          if (!rows.in(i)) continue;
 #pragma unroll
           for (int e = 0; e < V; ++e) s_cols[c + e] = (w > 0 ? s_cols[c + e] : 0.f) + sums[which][i].v[e];
         }
@@ -240,9 +249,10 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP || (V == 1 && CH <= 8) 
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = rows.column(i);
-        if (c >= a.H) continue;
+        if (!rows.in(i)) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) part[c + e] = sums[which][i].v[e];
+        for (int e = 0; e < V; ++e)
+          if (!SHIFT || (c + e >= 0 && c + e < a.H)) part[c + e] = sums[which][i].v[e];
       }
     }
   }
@@ -363,11 +373,14 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(NormBackwardArgs b, in
   if (!wants(b, which)) return;
   const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < a.H) {
-#pragma unroll 4
-    for (int p = strand; p < parts; p += 32) v += partial_row(b, which, p)[c];
+  float v = 0.f, part[(kNormParts + 31) / 32];  // loaded together: one load's latency
+#pragma unroll
+  for (int i = 0; i < (kNormParts + 31) / 32; ++i) {
+    const int p = strand + 32 * i;
+    part[i] = p < parts && c < a.H ? partial_row(b, which, p)[c] : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < (kNormParts + 31) / 32; ++i) v += part[i];
   s[strand][lane] = v;
   __syncthreads();
   if (strand != 0 || c >= a.H) return;
@@ -391,26 +404,28 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(NormBackwardArgs b, in
   if (b.d_weight != nullptr) store_weight(b.d_weight, gate * v);
 }
 
-template <typename T, int V, int CH, int STAGES, bool WARP, int THREADS = 0>
+template <typename T, int V, int CH, int STAGES, bool WARP, int THREADS = 0, bool SHIFT = false>
 cudaError_t run(const NormBackwardArgs& b, int threads, int num_sms, cudaStream_t st, int* parts) {
   const NormArgs& a = b.f;
   const bool element = a.gate_kind == MOE_GATE_ELEMENT;
-  auto* k = a.h == nullptr ? norm_backward_kernel<T, V, CH, STAGES, THREADS, false, true, false, WARP>
-            : a.next       ? (element ? norm_backward_kernel<T, V, CH, STAGES, THREADS, true, true, true, WARP>
-                                      : norm_backward_kernel<T, V, CH, STAGES, THREADS, true, true, false, WARP>)
-                           : (element ? norm_backward_kernel<T, V, CH, STAGES, THREADS, true, false, true, WARP>
-                                      : norm_backward_kernel<T, V, CH, STAGES, THREADS, true, false, false, WARP>);
+  auto* k = a.h == nullptr ? norm_backward_kernel<T, V, CH, STAGES, THREADS, false, true, false, WARP, SHIFT>
+            : a.next       ? (element ? norm_backward_kernel<T, V, CH, STAGES, THREADS, true, true, true, WARP, SHIFT>
+                                      : norm_backward_kernel<T, V, CH, STAGES, THREADS, true, true, false, WARP, SHIFT>)
+                           : (element ? norm_backward_kernel<T, V, CH, STAGES, THREADS, true, false, true, WARP, SHIFT>
+                                      : norm_backward_kernel<T, V, CH, STAGES, THREADS, true, false, false, WARP, SHIFT>);
   const int arrays = (b.dr != nullptr) + 2 * (a.next != 0) + (a.h != nullptr) + element;
   size_t smem = queue_smem<T, V, CH, STAGES>(a.H, arrays, threads);
   if (WARP) smem = std::max(smem, sizeof(float) * a.H);
   else if (STAGES > 0) smem += sizeof(float) * 2 * CH * V * threads;
-  int blocks = std::max(1, (V == 1 && CH <= 8 ? 1024 : 512) / threads);
+  int blocks = std::max(1, (THREADS == 256 ? CH <= 8 ? 1024 : 768 : 512) / threads);
   if (smem > 0) blocks = std::max(1, std::min<int>(blocks, kQueueSmem / smem));
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  *parts = std::min(std::min(ceil_div(a.T, WARP ? threads / 32 : 1), blocks * num_sms), kNormParts);
+  const int rows = ceil_div(a.T, WARP ? threads / 32 : 1);
+  *parts = std::min(std::min(rows, blocks * num_sms), kNormParts);
+  if (SHIFT) *parts = shifted_grid(*parts, rows);
   return launch_kernel(true, k, *parts, threads, smem, st, b);
 }
 
@@ -440,11 +455,24 @@ cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& b, int num_s
                                         a.gate_kind == MOE_GATE_ELEMENT ? b.d_gate : nullptr},
                                        {b.ld_dr, b.ld_dy, a.ld_h, b.ld_r,
                                         a.gate_kind == MOE_GATE_ELEMENT ? a.ld_gate : 0});
-    const int packs = vec ? a.H / V : a.H;
+    const bool shift =
+        !vec && rows_shift_alike<T>(a.T, a.H,
+                                    {b.dr, b.dy, a.h, a.next ? a.r : nullptr, b.dx, b.dh,
+                                     a.gate_kind == MOE_GATE_ELEMENT ? a.gate : nullptr,
+                                     a.gate_kind == MOE_GATE_ELEMENT ? b.d_gate : nullptr},
+                                    {b.dr != nullptr ? b.ld_dr : a.H, a.next ? b.ld_dy : a.H,
+                                     a.h != nullptr ? a.ld_h : a.H, a.next ? b.ld_r : a.H,
+                                     a.gate_kind == MOE_GATE_ELEMENT ? a.ld_gate : a.H});
+    // (the last packs of a shifted row reach at most V - 1 elements beyond it)
+    const int packs = vec ? a.H / V : shift ? ceil_div(a.H + V - 1, V) : a.H;
     auto threads = [&](int ch) { return ceil_div(ceil_div(packs, ch), 32) * 32; };
     int parts = 0;
     cudaError_t e = cudaSuccess;
     if (a.T == 0) {
+    } else if (shift && packs <= 256) {
+      e = run<T, V, 1, 2, false, 0, true>(b, threads(1), num_sms, st, &parts);
+    } else if (shift && packs <= 1024) {
+      e = run<T, V, 2, 2, false, 0, true>(b, threads(2), num_sms, st, &parts);
     } else if (vec && packs <= 32) {
       e = run<T, V, 1, 2, true>(b, 256, num_sms, st, &parts);
     } else if (vec && packs <= 64) {
@@ -453,13 +481,13 @@ cudaError_t launch_norm_backward(int dtype, const NormBackwardArgs& b, int num_s
       e = run<T, V, 1, 2, false>(b, threads(1), num_sms, st, &parts);
     } else if (vec && packs <= 1024) {
       e = run<T, V, 2, 2, false>(b, threads(2), num_sms, st, &parts);
-    } else if (!vec && packs <= 1024) {
+    } else if (!vec && a.H <= 1024) {
       e = run<T, 1, 4, 2, false, 256>(b, 256, num_sms, st, &parts);
-    } else if (!vec && packs <= 2048) {
+    } else if (!vec && a.H <= 2048) {
       e = run<T, 1, 8, 2, false, 256>(b, 256, num_sms, st, &parts);
-    } else if (!vec && packs <= 4096) {
-      e = run<T, 1, 8, 2, false, 512>(b, 512, num_sms, st, &parts);
-    } else if (!vec && packs <= 8192) {
+    } else if (!vec && a.H <= 4096) {
+      e = run<T, 1, 16, 2, false, 256>(b, 256, num_sms, st, &parts);
+    } else if (!vec && a.H <= 8192) {
       e = run<T, 1, 16, 0, false, 512>(b, 512, num_sms, st, &parts);
     } else if (vec && packs <= 2048 && sizeof(T) == 4) {
       if constexpr (sizeof(T) == 4) e = run<T, V, 4, 0, false>(b, threads(4), num_sms, st, &parts);

@@ -19,6 +19,12 @@ __host__ __device__ constexpr int loose_row_bytes(int H, int size) { return (H *
 // their way into shared memory while it works on one.
 //   Packs (V > 1): each thread copies its own packs into its own slots, which
 // nobody else reads, so there is no barrier in the queue.
+//   Packs of shifted rows (SHIFT): rows of a width that is no multiple of a pack
+// start anywhere in a 16-byte chunk, but contiguous rows of one width and type
+// all start at the same place of theirs, and rows a multiple of 8 apart start
+// alike. The packs are then the aligned chunks: `shift` elements of the first
+// belong to the row in front, the last is cut at the row's end, and their
+// values outside the row count as zero.
 //   Rows of any width and alignment (V = 1): the block copies the aligned
 // 16-byte chunks that hold the row, whatever they hold beside it (in front of
 // the row that is memory of the same allocation, which starts at a multiple of
@@ -28,12 +34,13 @@ __host__ __device__ constexpr int loose_row_bytes(int H, int size) { return (H *
 // memory where they are used, a second time from the L1.
 // THREADS: of a row, where the kernel is compiled for their number (an
 // element's place is then a constant away from the thread's), else 0.
-template <typename T, int V, int CH, int ARRAYS, int STAGES, int THREADS>
+template <typename T, int V, int CH, int ARRAYS, int STAGES, int THREADS, bool SHIFT>
 struct RowQueue {
   static constexpr bool kLoose = V == 1 && STAGES > 0;
   const T* src[ARRAYS];  // null: absent; else, once started, where the row to fetch starts (for this thread)
   int64_t ld[ARRAYS];    // once started, the way to the block's next row
   int H, j;
+  int shift = 0;         // see SHIFT
   int put_left;          // rows still to fetch
   // STAGES > 0, in bytes: [STAGES][arrays present][a row]
   uint8_t* ring;
@@ -42,7 +49,11 @@ struct RowQueue {
   int phase[ARRAYS], phase_step[ARRAYS];  // loose rows: where in its first chunk the row in work starts
 
   __device__ __forceinline__ int threads() const { return THREADS > 0 ? THREADS : static_cast<int>(blockDim.x); }
-  __device__ __forceinline__ int column(int i) const { return (i * threads() + j) * V; }
+  // Pack i's place in the row's chunks, its first column, whether the row has it, whether it has all of it.
+  __device__ __forceinline__ int place(int i) const { return (i * threads() + j) * V; }
+  __device__ __forceinline__ int column(int i) const { return SHIFT ? place(i) - shift : place(i); }
+  __device__ __forceinline__ bool in(int i) const { return column(i) < H; }
+  __device__ __forceinline__ bool whole(int i) const { return !SHIFT || (column(i) >= 0 && column(i) + V <= H); }
 
   __device__ __forceinline__ void put() {
     if (put_left > 0) {
@@ -59,7 +70,12 @@ struct RowQueue {
         } else {
 #pragma unroll
           for (int i = 0; i < CH; ++i)
-            if (column(i) < H) cp_async16(dst + i * threads() * 16, src[a] + i * threads() * V);
+            if (in(i)) {
+              if constexpr (SHIFT)
+                cp_async16_part(dst + i * threads() * 16, src[a] + i * threads() * V,
+                                min(16, (H - column(i)) * static_cast<int>(sizeof(T))));
+              else cp_async16(dst + i * threads() * 16, src[a] + i * threads() * V);
+            }
         }
         src[a] += ld[a];
       }
@@ -68,12 +84,18 @@ struct RowQueue {
     put_at = put_at + stage_bytes == STAGES * stage_bytes ? 0 : put_at + stage_bytes;
   }
 
+  // Where the rows first, first + step, ... of a contiguous array start in their first chunk.
+  __device__ __forceinline__ void set_shift(const void* array, int64_t first) {
+    if constexpr (SHIFT)
+      shift = static_cast<int>((reinterpret_cast<uintptr_t>(array) + first * H * sizeof(T)) & 15) / static_cast<int>(sizeof(T));
+  }
+
   // Rows first, first + step, ... (n of them).
   __device__ __forceinline__ void start(int64_t first, int64_t step, int n, void* smem) {
     put_left = n;
 #pragma unroll
     for (int a = 0; a < ARRAYS; ++a) {
-      if (src[a] != nullptr) src[a] += (STAGES > 0 ? first : first - step) * ld[a] + (kLoose ? 0 : j * V);
+      if (src[a] != nullptr) src[a] += (STAGES > 0 ? first : first - step) * ld[a] + (kLoose ? 0 : j * V) - shift;
       ld[a] *= step;
     }
     if constexpr (STAGES > 0) {
@@ -274,6 +296,30 @@ __device__ __forceinline__ float gate_slope(int act, float g) {
   return 1.f;
 }
 
+// Values of a pack that the row has, zero outside it.
+template <typename Q>
+__device__ __forceinline__ auto row_values(const Q& rows, int a, int i) {
+  auto f = values(rows.at(a, i));
+  if (!rows.whole(i)) {
+#pragma unroll
+    for (int e = 0; e < static_cast<int>(sizeof(f.v) / sizeof(float)); ++e)
+      f.v[e] = rows.column(i) + e >= 0 && rows.column(i) + e < rows.H ? f.v[e] : 0.f;
+  }
+  return f;
+}
+// Stores what the row has of pack i; out: this thread's first pack.
+template <typename Q, typename T, int V>
+__device__ __forceinline__ void store_values(const Q& rows, T* out, int i, const Values<V>& f) {
+  out += i * rows.threads() * V;
+  if (rows.whole(i)) {
+    store_pack(out, pack<T, V>(f.v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (rows.column(i) + e >= 0 && rows.column(i) + e < rows.H) out[e] = from_f32<T>(f.v[e]);
+  }
+}
+
 // w_offset + weight (1 without a weight) of columns c..c+V-1.
 template <typename T, int V>
 __device__ __forceinline__ Values<V> load_weight(const void* w, int w_f32, float offset, int c) {
@@ -311,6 +357,20 @@ __device__ __forceinline__ Values<V> channel_gate(const NormArgs& a, int c) {
   return gate_values(a.gate_act, values(load_pack<V>(static_cast<const T*>(a.gate) + c)));
 }
 
+// A factor of the columns of a pack: V at a time, or one by one where the
+// pack may reach beyond the row (zero there).
+template <bool SHIFT, int V, typename Wide, typename One>
+__device__ __forceinline__ Values<V> column_factor(int c, int H, const Wide& wide, const One& one) {
+  if constexpr (!SHIFT) {
+    return wide(c);
+  } else {
+    Values<V> f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) f.v[e] = c + e >= 0 && c + e < H ? one(c + e) : 0.f;
+    return f;
+  }
+}
+
 // Every operand allows 16-byte accesses (null pointers and unused strides of
 // 0 pass).
 template <typename T>
@@ -322,6 +382,25 @@ bool rows_vectorize(int H, std::initializer_list<const void*> ptrs, std::initial
     if (l % kVec<T>) return false;
   return true;
 }
+
+// The operands [T, H] start at the same place of a 16-byte chunk in every row
+// (see SHIFT; null pointers pass, and the width for an absent one's stride).
+template <typename T>
+bool rows_shift_alike(int n, int H, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
+  int phase = -1;
+  for (const void* p : ptrs) {
+    if (p == nullptr) continue;
+    const int at = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    if (phase >= 0 && at != phase) return false;
+    phase = at;
+  }
+  for (const int64_t l : lds)
+    if (n > 1 && ((l - H) * static_cast<int64_t>(sizeof(T))) % 16) return false;
+  return true;
+}
+
+// Blocks that walk more than one row each take rows a multiple of 8 apart.
+inline int shifted_grid(int grid, int rows) { return grid < rows ? std::min(rows, std::max(8, grid / 8 * 8)) : grid; }
 
 // Shared memory of an SM that the blocks' rows in flight share.
 constexpr int kQueueSmem = 220 * 1024;

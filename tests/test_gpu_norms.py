@@ -116,6 +116,32 @@ def test_sums_over_many_tokens_repeat_bit_for_bit():
         C.check(o, e, m, 3 * steps(1024, 5000))
 
 
+@pytest.mark.parametrize("dtype", C.DTYPES)
+@pytest.mark.parametrize("T,H", [(1003, 1001), (2500, 37), (640, 2049), (900, 4091), (333, 8185), (320, 8190)])
+def test_odd_widths_over_many_tokens(T, H, dtype):
+    """Every row starts at another place of a 16-byte chunk, and a block walks
+    several rows; strided operands start elsewhere than contiguous ones."""
+    x, h, dr, dy, w, nw, gate, kw, _ = after_case(T, H, dtype, 44)  # element gate, norm, next norm
+    assert gate.shape == (T, H) and w is not None and nw is not None
+    args = (w, gate, kw["gate_act"], kw["alpha"], kw["beta"], EPS, kw["weight_offset"], True)
+    er, mr = O.norm_after(x, h, *args), O.norm_after(x, h, *args, mag=True)
+    s = 1 / torch.sqrt((er * er).mean(1, keepdim=True) + EPS)
+    ey = O.norm(er, nw, EPS, kw["weight_offset"])
+    my = s * (nw.double() + kw["weight_offset"]).abs() * mr + ey.abs() * (1 + (mr * mr).mean(1, keepdim=True).sqrt() * s)
+    r = None
+    for xs, hs in ((x, h), (C.strided(x, 3), h), (x, C.strided(h, 8, 1))):
+        r, y = M.norm_after(xs, hs, w, **kw)
+        C.check(r, er, mr, steps(H))
+        C.check(y, ey, my, steps(H))
+    kw.pop("next_weight")
+    want = O.norm_after_backward(dr, h, *args, dy, r, nw, EPS)
+    mags = O.norm_after_backward(dr, h, *args, dy, r, nw, EPS, mag=True)
+    for ds, hs in ((dr, h), (C.strided(dr, 5), h), (dr, C.strided(h, 16, 2))):
+        got = M.norm_after_backward(ds, hs, w, dy=dy, r=r, next_weight=nw, **kw)
+        for o, e, m in zip(got, want, mags):
+            C.check(o, e, m, 3 * steps(H, T))
+
+
 @pytest.mark.parametrize("H", [512, 1024, 1000, 1001])
 def test_strided_misaligned_and_broadcast_rows(H):
     g = C.gen(H)
