@@ -11,6 +11,15 @@
 // read each token's row up to K times, and its K visits lie too far apart in
 // expert order for the L2 to keep it. Bound by DRAM bandwidth. Sums over k
 // run in ascending k in fp32, without atomics, and round once.
+//
+// Measured (bf16, of 6.8 TB/s for a plain copy): place, 8192 tokens of 7168
+// columns, K = 8, into 128-row groups 230 us, 6.6 TB/s (nearly all of it
+// writes); gather with weights, 8192 of 2880, K = 4 40 us, 5.8 TB/s; place with
+// dots, 4096 of 4096, K = 2 27 us, 6.2 TB/s; gather with dots of unaligned fp32
+// rows, 3001 of 1001, K = 5 23 us, 3.4 TB/s: there each lane's loads are 4 bytes
+// and the 64 registers hold 16 of them. Registers are held to four blocks an
+// SM: with more packs in flight a lane and fewer warps the gather of 2880
+// columns took 59 us, with six blocks (and spills) 108.
 #include "block_internal.cuh"
 #include "../ptx.cuh"
 
