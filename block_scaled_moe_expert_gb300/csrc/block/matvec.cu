@@ -13,6 +13,14 @@
 // become fp16 in registers, exactly; the group scale multiplies the group's
 // fp32 sums.
 //
+// Measured, a call among others: FP4 131072 x 4096, one token 43 us, 6.6 TB/s,
+// 97% of a plain copy's rate; FP4 4096 x 7168 with SwiGLU, one token 5.9 us;
+// INT4 28671 x 4096, 7 tokens 15 us, 4.1 TB/s, where the fixed 4 us of launch,
+// staging and joining and the conversion of the codes (13 cycles a word of
+// eight, FP4 8) take their part. Without the ring in shared memory (blocks
+// loaded into registers four ahead) the first took 88 us: the scoreboard makes
+// a warp wait for more than the block it needs.
+//
 // x is staged in shared memory as fp16. The 128 elements of a bf16 row that
 // meet one block are scaled by a power of two that brings their largest finite
 // value to [2^14, 2^15): fp16 then holds every element exactly down to 2^-29

@@ -9,6 +9,13 @@
 // Bound by DRAM bandwidth (by latency for a few tokens). A block walks many
 // rows with the next ones on their way (RowQueue), and keeps its columns'
 // factors alpha w g and w_next in registers. Sums in fp32 by a fixed tree.
+//
+// Measured (bf16): norm_after with channel gate and next norm, 8192 rows of
+// 7168 columns, 75 us, 6.3 TB/s, 92% of a plain copy's rate; of 2001 columns 28
+// us, 4.7 TB/s. One thread a pack (896 a row) and one block an SM: with two
+// packs a thread the factors do not fit into the registers and the same rows
+// took 200 us. Instructions count: packed fp32 pairs and one conversion
+// instruction a pair took 110 us to 80.
 #include "norm_common.cuh"
 
 namespace bsmoe {
