@@ -46,6 +46,13 @@ __device__ __forceinline__ Where locate(int wpt) {
   return {static_cast<int64_t>(blockIdx.x) * (kPermWarps / wpt) + warp / wpt, warp % wpt, warp / wpt};
 }
 
+// The row of slot (t, lane), -1 where it has none. A plan that does not belong
+// to the call moves nothing out of the rows' range.
+__device__ __forceinline__ int slot_row(const SortPlan& p, int64_t t, int lane) {
+  const int row = p.inv[t * p.K + lane];
+  return static_cast<unsigned>(row) < static_cast<unsigned>(p.M) ? row : -1;
+}
+
 // Sums the dots of KT rows over the warps of a token and stores them.
 template <int KT>
 __device__ __forceinline__ void store_dots(float (&dot)[KT], const Where& at, int wpt, bool live, float* dots, int K,
@@ -100,7 +107,7 @@ __global__ void __launch_bounds__(kPermThreads, kPermBlocks) place_kernel(PlaceA
   int my_row = -1;
   float my_w = 0.f;
   if (live && lane < K) {
-    my_row = a.p.inv[at.t * K + lane];
+    my_row = slot_row(a.p, at.t, lane);
     if (W) my_w = a.w[at.t * K + lane];
   }
   const T* x = static_cast<const T*>(a.x) + at.t * a.ld_x;
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kPermThreads, kPermBlocks) gather_kernel(Gathe
   int my_row = -1;
   float my_w = 0.f;
   if (live && lane < K) {
-    my_row = a.p.inv[at.t * K + lane];
+    my_row = slot_row(a.p, at.t, lane);
     if (W) my_w = a.w[at.t * K + lane];
   }
   const T* rows = static_cast<const T*>(a.rows);

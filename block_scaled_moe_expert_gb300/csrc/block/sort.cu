@@ -204,10 +204,46 @@ bool sort_layout(int T, int E, int K, int row_align, moe_sort_layout* out) {
   return true;
 }
 
+namespace {
+
+constexpr size_t kSortMaxSmem = sizeof(int) * (kSortWarps + 3) * (kMaxExperts + 1);
+
+// Clusters of 16 CTAs need a GPC with that many SMs: asked once.
+bool wide_clusters_fit() {
+  static const bool fit = [] {
+    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSortMaxSmem)) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = 16;
+    cfg.blockDim = kSortThreads;
+    cfg.dynamicSmemBytes = kSortMaxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    return clusters > 0;
+  }();
+  return fit;
+}
+
+}  // namespace
+
 cudaError_t launch_sort(const int32_t* topk_idx, const SortPlan& p, cudaStream_t st) {
   // one CTA with a warp per 32 slots (and a thread per expert); a cluster of
   // full CTAs for large batches
-  const int cluster = p.S <= kSortOneCta ? 1 : p.S < kSortWide ? 8 : 16;
+  const int cluster = p.S <= kSortOneCta ? 1 : p.S >= kSortWide && wide_clusters_fit() ? 16 : 8;
   const int count_warps = cluster > 1 ? kSortWarps : std::max(1, std::min(kSortWarps, ceil_div(p.S, 32)));
   const int range = ceil_div(ceil_div(p.S, cluster * count_warps), 32) * 32;
   const int threads = std::max(count_warps, ceil_div(p.E + 1, 32)) * 32;
@@ -215,10 +251,6 @@ cudaError_t launch_sort(const int32_t* topk_idx, const SortPlan& p, cudaStream_t
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  if (cluster > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -129,6 +129,24 @@ def test_special_values_move_unchanged():
     assert int(out.isnan().sum()) == 1
 
 
+def test_a_plan_of_another_call_moves_nothing_out_of_range():
+    """Slots whose row is outside the rows count as skipped."""
+    T, H, E, K = 9, 72, 4, 3
+    plan, w, x, rows = make(T, H, E, K, 2, 0, torch.float32)
+    want_drows, want_dw = M.unpermute_tokens_backward(x, plan, rows, w)
+    keep = torch.ones(T, K, dtype=torch.bool, device="cuda")
+    for (t, k), row in (((0, 0), plan.row_capacity), ((3, 2), 2 ** 31 - 1), ((8, 1), -2 ** 31), ((5, 0), -7)):
+        lost = int(plan.inv[t, k])
+        plan.inv[t, k] = row
+        keep[t, k] = False
+        want_drows[lost] = 0
+        plan.row_slot[lost] = -1
+    inv = torch.where(keep, plan.inv, torch.full_like(plan.inv, -1))
+    C.check(M.unpermute_tokens(rows, plan, w), O.gather(rows, w, inv), O.gather(rows, w, inv, mag=True), K + 1)
+    drows, dw = M.unpermute_tokens_backward(x, plan, rows, w)
+    assert torch.equal(drows, want_drows) and torch.equal(dw, torch.where(keep, want_dw, torch.zeros_like(want_dw)))
+
+
 def test_offsets_beyond_32_bits():
     """Rows whose element offsets pass 2^31 (8 GB of rows)."""
     H, T, K, E = 65536, 8224, 4, 4
