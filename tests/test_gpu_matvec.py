@@ -158,6 +158,22 @@ def test_strides_streams_and_graphs():
     assert M.matvec(x[:0], prepared).shape == (0, 1000)
 
 
+def test_weights_beyond_4_gb():
+    """The last rows of a matrix whose byte offsets pass 2^32."""
+    N, K, n = 270001, 32768, 37
+    g = C.gen(14)
+    last = make_weights(g, "fp4", n, K)
+    last["w_scale"].clamp_(max=119)
+    w = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    scale = torch.full((N, K // 32), 119, dtype=torch.uint8, device="cuda")
+    w[-n:], scale[-n:] = last["w"], last["w_scale"]
+    assert w.numel() > 2 ** 32
+    x = C.randn(g, 2, K, dtype=torch.bfloat16)
+    out = M.matvec(x, M.prepare_matvec(dict(fmt="fp4", N=N, K=K, w=w, w_scale=scale)))
+    check(x, last, out[:, -n:].contiguous())
+    assert int(torch.count_nonzero(out[:, :-n])) == 0
+
+
 def test_one_matrix_of_the_experts_fp4_weights():
     """The checkpoint layout is that of the experts' FP4 weights."""
     from block_scaled_moe_expert_gb300 import workloads as W

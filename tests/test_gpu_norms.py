@@ -165,6 +165,30 @@ def test_strided_misaligned_and_broadcast_rows(H):
     assert torch.equal(M.norm_after(x, h, gate=token), M.norm_after(x, h, gate=token.contiguous()))
 
 
+def test_offsets_beyond_32_bits():
+    """Rows whose element offsets pass 2^31: the last rows as a call of their own."""
+    T, H, n = 263000, 8192, 40
+    assert T * H > 2 ** 31
+    g = C.gen(6)
+    tail = C.randn(g, n, H, dtype=torch.bfloat16)
+    w = C.randn(g, H, dtype=torch.bfloat16)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = tail
+    r, y = M.norm_after(x, x, w, next_weight=w)
+    want_r, want_y = M.norm_after(tail, tail, w, next_weight=w)
+    assert torch.equal(r[-n:], want_r) and torch.equal(y[-n:], want_y)
+    assert int(torch.count_nonzero(y[:-n])) == 0
+    del y
+    dx, dh, dw, _, dn = M.norm_after_backward(x, x, w, dy=x, r=r, next_weight=w)
+    want = M.norm_after_backward(tail, tail, w, dy=tail, r=want_r, next_weight=w)
+    assert torch.equal(dx[-n:], want[0]) and torch.equal(dh[-n:], want[1])
+    # the same terms, shared out to other blocks
+    args = (w, None, "none", 1.0, 1.0, 1e-6, 0.0, True, tail, want_r, w, 1e-6)
+    mags = O.norm_after_backward(tail, tail, *args, mag=True)
+    for o, e, m in zip((dw, dn), O.norm_after_backward(tail, tail, *args)[2::2], mags[2::2]):
+        C.check(o, e, m, 3 * steps(H, T))
+
+
 def test_no_tokens():
     for H in (64, 33):
         x = torch.zeros(0, H, dtype=torch.bfloat16, device="cuda")
