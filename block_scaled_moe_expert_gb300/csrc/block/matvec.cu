@@ -22,10 +22,14 @@
 // a warp wait for more than the block it needs.
 //
 // x is staged in shared memory as fp16. The 128 elements of a bf16 row that
-// meet one block are scaled by a power of two that brings their largest finite
-// value to [2^14, 2^15): fp16 then holds every element exactly down to 2^-29
-// of the largest, and below that with an error under 2^-40 of the largest, far
-// below the fp32 sums' own. The power is taken back on each group's sums.
+// meet one block are scaled by an even power of two that brings their largest
+// finite value to [2^13, 2^15): fp16 then holds every element exactly down to
+// 2^-29 of the largest, and below that with an error under 2^-38 of the largest,
+// far below the fp32 sums' own. The power is taken back on each group's sums: a
+// negative one before the group's scale is applied (the sums of small elements
+// are exact there down to the subnormals), a positive one half before and half
+// after, so that what the scale brings back into range does not leave it on the
+// way.
 #include <cooperative_groups.h>
 #include <cmath>
 #include <type_traits>
@@ -165,8 +169,8 @@ __device__ __forceinline__ void read_block(Block<SW>& b, const uint8_t* slot, in
 }
 
 // acc += block x tokens. GROUPS: scale groups per block (4, 2 or 1). xs: this
-// lane's part of its token's row at the block's k, x_scale: the tokens' powers
-// for this block.
+// lane's part of its token's row at the block's k, x_scale: what of the tokens'
+// powers comes before the scale for this block.
 template <int FMT, int GROUPS, int NT, typename S, typename X, int SW>
 __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<SW>& b,
                                                const uint8_t* const (&xs)[NT], const float* x_scale, int lane) {
@@ -176,10 +180,13 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
     ue8m0_scales(b.scale[0], scale[0]);
     ue8m0_scales(b.scale[1], scale[1]);
   }
-  float2 back[NT];
+  float2 before[NT], after[NT];
   if constexpr (kScaledX<X>) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) back[n] = *reinterpret_cast<const float2*>(x_scale + n * 8 + 2 * q);
+    for (int n = 0; n < NT; ++n) {
+      before[n] = *reinterpret_cast<const float2*>(x_scale + n * 8 + 2 * q);
+      after[n] = make_float2(fmaxf(before[n].x, 1.f), fmaxf(before[n].y, 1.f));
+    }
   }
   float c[NT][4];
 #pragma unroll
@@ -215,12 +222,14 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
       mma_16816(c[n], a0[2], a1[2], a0[3], a1[3], xv[n].z, xv[n].w, c[n][0], c[n][1], c[n][2], c[n][3]);
       if (last) {
         float2 lo = make_float2(c[n][0], c[n][1]), hi = make_float2(c[n][2], c[n][3]);
+        const float2 sum_lo = make_float2(acc[n][0], acc[n][1]), sum_hi = make_float2(acc[n][2], acc[n][3]);
         if constexpr (kScaledX<X>) {
-          lo = mul2(lo, back[n]);
-          hi = mul2(hi, back[n]);
+          lo = fma2(mul2(mul2(lo, before[n]), make_float2(s0, s0)), after[n], sum_lo);
+          hi = fma2(mul2(mul2(hi, before[n]), make_float2(s1, s1)), after[n], sum_hi);
+        } else {
+          lo = fma2(lo, make_float2(s0, s0), sum_lo);
+          hi = fma2(hi, make_float2(s1, s1), sum_hi);
         }
-        lo = fma2(lo, make_float2(s0, s0), make_float2(acc[n][0], acc[n][1]));
-        hi = fma2(hi, make_float2(s1, s1), make_float2(acc[n][2], acc[n][3]));
         acc[n][0] = lo.x;
         acc[n][1] = lo.y;
         acc[n][2] = hi.x;
@@ -342,8 +351,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
         const unsigned half = 0xFFFFu << (lane & 16);  // the units of a warp end apart
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
-        // 2^(14 - e) and back, e the exponent of m (at least -112: both are normal)
-        const int e = max(15, static_cast<int>(__float_as_uint(m) >> 23));
+        // 2^(14 - e), e the exponent of m or the even one above it (at least
+        // -112), and 2^(e - 14) to take it back, or its root if that is above 1:
+        // all are normal
+        const int e = max(15, static_cast<int>(__float_as_uint(m) >> 23) | 1), back = e - 141;
         const float scale = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
         uint32_t* w = &out.x;
 #pragma unroll
@@ -351,7 +362,8 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
           const __half2 h = __floats2half2_rn(f[2 * i] * scale, f[2 * i + 1] * scale);
           w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        if ((lane & 15) == 0) s_power[step * kMvTokens + t] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+        if ((lane & 15) == 0)
+          s_power[step * kMvTokens + t] = __uint_as_float(static_cast<uint32_t>(127 + (back > 0 ? back / 2 : back)) << 23);
       } else {
         out = *reinterpret_cast<const uint4*>(&p[j]);
       }
