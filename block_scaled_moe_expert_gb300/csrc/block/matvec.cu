@@ -13,8 +13,8 @@
 // become fp16 in registers, exactly; the group scale multiplies the group's
 // fp32 sums.
 //
-// Measured, a call among others: FP4 131072 x 4096, one token 43 us, 6.6 TB/s,
-// 97% of a plain copy's rate; FP4 4096 x 7168 with SwiGLU, one token 5.9 us;
+// Measured, a call among others: FP4 131072 x 4096, one token 43.7 us, 6.5 TB/s,
+// 96% of a plain copy's rate; FP4 4096 x 7168 with SwiGLU, one token 6.2 us;
 // INT4 28671 x 4096, 7 tokens 15 us, 4.1 TB/s, where the fixed 4 us of launch,
 // staging and joining and the conversion of the codes (13 cycles a word of
 // eight, FP4 8) take their part. Without the ring in shared memory (blocks
@@ -22,14 +22,16 @@
 // a warp wait for more than the block it needs.
 //
 // x is staged in shared memory as fp16. The 128 elements of a bf16 row that
-// meet one block are scaled by an even power of two that brings their largest
-// finite value to [2^13, 2^15): fp16 then holds every element exactly down to
-// 2^-29 of the largest, and below that with an error under 2^-38 of the largest,
-// far below the fp32 sums' own. The power is taken back on each group's sums: a
-// negative one before the group's scale is applied (the sums of small elements
-// are exact there down to the subnormals), a positive one half before and half
-// after, so that what the scale brings back into range does not leave it on the
-// way.
+// meet one block are scaled by a power of two that brings their largest finite
+// value to [2^14, 2^15): fp16 then holds every element exactly that is at least
+// 2^-31 of the largest. The power is taken back on each group's sums before the
+// group's scale. A CTA that meets an element that fp16 does not hold (or a block
+// with a value of 2^96 or more, whose sums could leave fp32's range before the
+// scale brings them back) says so while it stages, and takes x as it is instead:
+// bf16 through the bf16 instruction, with codes that bf16 holds just as exactly.
+// Then nothing is lost over bf16's whole range. The conversion of the codes costs
+// more there, so that this is the way of the few rows that need it (131072 x 4096,
+// one token: 78 us against 44).
 #include <cooperative_groups.h>
 #include <cmath>
 #include <type_traits>
@@ -52,6 +54,11 @@ constexpr int kMvMaxSmem = 227 * 1024 - 18 * 1024;  // for x and the blocks in f
 constexpr int kMvMaxCluster = 8;
 template <typename X>
 constexpr bool kScaledX = std::is_same<X, __nv_bfloat16>::value;
+constexpr int kMvHuge = 96;  // exponent from which bf16 activations are taken as they are
+// Codes that meet bf16 activations are held times this power, so that the sums
+// of a group's products stay below 2^128: 32 of 6 2^128, or 128 of 255 2^128.
+template <int FMT>
+constexpr float kWideCode = FMT == MOE_Q_FP4 ? 1.f / 256 : 1.f / 65536;
 constexpr int kCodeBytes = kMvRows * kMvStep / 2;
 
 // Block of 16 rows x 128 k: 1024 bytes of codes, then the scales.
@@ -81,12 +88,18 @@ struct MvArgs {
   bool x_vec;  // rows of x allow 16-byte loads
 };
 
+// X: the type of both operands.
+template <typename X>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  if constexpr (std::is_same<X, __nv_bfloat16>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The eight e2m1 codes of a word as fp16 pairs, in order.
@@ -141,6 +154,14 @@ __device__ __forceinline__ void int4_pairs(uint32_t word, uint32_t zero, uint32_
   h[3] = half2_fma(code_bits(up, 0x00F000F0u), sixteenth, zero16);
 }
 
+// fp16 pairs of codes as bf16 pairs times kWideCode, exactly.
+template <int FMT>
+__device__ __forceinline__ void wide_pairs(uint32_t (&h)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = pack2(mul2(unpack2(h[i], __half()), make_float2(kWideCode<FMT>, kWideCode<FMT>)), __nv_bfloat16());
+}
+
 // What a lane holds of one block.
 template <int SW>
 struct Block {
@@ -169,9 +190,9 @@ __device__ __forceinline__ void read_block(Block<SW>& b, const uint8_t* slot, in
 }
 
 // acc += block x tokens. GROUPS: scale groups per block (4, 2 or 1). xs: this
-// lane's part of its token's row at the block's k, x_scale: what of the tokens'
-// powers comes before the scale for this block.
-template <int FMT, int GROUPS, int NT, typename S, typename X, int SW>
+// lane's part of its token's row at the block's k, x_scale: the tokens' powers
+// for this block. WIDE: x is bf16 as it is, without powers.
+template <int FMT, int GROUPS, int NT, bool WIDE, typename S, typename X, int SW>
 __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<SW>& b,
                                                const uint8_t* const (&xs)[NT], const float* x_scale, int lane) {
   const int q = lane & 3;
@@ -180,13 +201,12 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
     ue8m0_scales(b.scale[0], scale[0]);
     ue8m0_scales(b.scale[1], scale[1]);
   }
-  float2 before[NT], after[NT];
-  if constexpr (kScaledX<X>) {
+  constexpr bool POWERS = kScaledX<X> && !WIDE;
+  using Operand = std::conditional_t<WIDE, __nv_bfloat16, __half>;
+  float2 back[NT];
+  if constexpr (POWERS) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      before[n] = *reinterpret_cast<const float2*>(x_scale + n * 8 + 2 * q);
-      after[n] = make_float2(fmaxf(before[n].x, 1.f), fmaxf(before[n].y, 1.f));
-    }
+    for (int n = 0; n < NT; ++n) back[n] = *reinterpret_cast<const float2*>(x_scale + n * 8 + 2 * q);
   }
   float c[NT][4];
 #pragma unroll
@@ -215,21 +235,29 @@ __device__ __forceinline__ void multiply_block(float (&acc)[NT][4], const Block<
       s0 = to_f32(*reinterpret_cast<const S*>(&h0));
       s1 = to_f32(*reinterpret_cast<const S*>(&h1));
     }
+    if constexpr (WIDE) {
+      wide_pairs<FMT>(a0);
+      wide_pairs<FMT>(a1);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (first) mma_16816(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y, 0.f, 0.f, 0.f, 0.f);
-      else mma_16816(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y, c[n][0], c[n][1], c[n][2], c[n][3]);
-      mma_16816(c[n], a0[2], a1[2], a0[3], a1[3], xv[n].z, xv[n].w, c[n][0], c[n][1], c[n][2], c[n][3]);
+      if (first) mma_16816<Operand>(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y, 0.f, 0.f, 0.f, 0.f);
+      else mma_16816<Operand>(c[n], a0[0], a1[0], a0[1], a1[1], xv[n].x, xv[n].y, c[n][0], c[n][1], c[n][2], c[n][3]);
+      mma_16816<Operand>(c[n], a0[2], a1[2], a0[3], a1[3], xv[n].z, xv[n].w, c[n][0], c[n][1], c[n][2], c[n][3]);
       if (last) {
         float2 lo = make_float2(c[n][0], c[n][1]), hi = make_float2(c[n][2], c[n][3]);
-        const float2 sum_lo = make_float2(acc[n][0], acc[n][1]), sum_hi = make_float2(acc[n][2], acc[n][3]);
-        if constexpr (kScaledX<X>) {
-          lo = fma2(mul2(mul2(lo, before[n]), make_float2(s0, s0)), after[n], sum_lo);
-          hi = fma2(mul2(mul2(hi, before[n]), make_float2(s1, s1)), after[n], sum_hi);
-        } else {
-          lo = fma2(lo, make_float2(s0, s0), sum_lo);
-          hi = fma2(hi, make_float2(s1, s1), sum_hi);
+        float2 scale_lo = make_float2(s0, s0), scale_hi = make_float2(s1, s1);
+        if constexpr (POWERS) {
+          lo = mul2(lo, back[n]);
+          hi = mul2(hi, back[n]);
         }
+        if constexpr (WIDE) {  // the codes' power after the scale, see kWideCode
+          lo = mul2(lo, scale_lo);
+          hi = mul2(hi, scale_hi);
+          scale_lo = scale_hi = make_float2(1.f / kWideCode<FMT>, 1.f / kWideCode<FMT>);
+        }
+        lo = fma2(lo, scale_lo, make_float2(acc[n][0], acc[n][1]));
+        hi = fma2(hi, scale_hi, make_float2(acc[n][2], acc[n][3]));
         acc[n][0] = lo.x;
         acc[n][1] = lo.y;
         acc[n][2] = hi.x;
@@ -268,17 +296,24 @@ __device__ __forceinline__ void store_tile(const MvArgs& a, int tile, const floa
   }
 }
 
-// Tiles are dealt round by round to groups of warps_k warps; the warps of a
-// group (and the CTAs of a cluster, one tile each then) share the tile's K
-// range in order and their sums are added in that order. DEPTH: blocks that a
-// warp has in flight or in work.
 template <int FMT, int GROUPS, int NT, int DEPTH, typename S, typename X>
-__global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
+__device__ __noinline__ void matvec_cta_wide(const MvArgs a, uint8_t* s_dyn, float (*s_red)[NT][4][32],
+                                             uint8_t* s_zero);
+
+// What a CTA does. Tiles are dealt round by round to groups of warps_k warps; the
+// warps of a group (and the CTAs of a cluster, one tile each then) share the
+// tile's K range in order and their sums are added in that order. DEPTH: blocks
+// that a warp has in flight or in work. WIDE: bf16 x as it is, which is where a
+// CTA goes whose x does not fit into fp16. That way is a function of its own, and
+// the CTA's answer goes through shared memory (behind s_zero): 131072 x 4096, one
+// token, takes 43.9 us so, and 46.2 with the barrier's own vote or with the
+// arguments passed by reference.
+template <int FMT, int GROUPS, int NT, int DEPTH, bool WIDE, typename S, typename X>
+__device__ __forceinline__ void matvec_cta(const MvArgs a, uint8_t* s_dyn, float (*s_red)[NT][4][32],
+                                           uint8_t* s_zero) {
   constexpr int SW = FMT == MOE_Q_FP4 ? 2 : 2 * GROUPS;
   constexpr int BYTES = block_bytes(FMT, kMvStep / GROUPS);
-  extern __shared__ __align__(16) uint8_t s_dyn[];
-  __shared__ float s_red[kMvWarps][NT][4][32];
-  __shared__ __align__(16) uint8_t s_zero[kMvStep * 2];
+  constexpr bool SCALED = kScaledX<X> && !WIDE;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same for the warp's lanes, as the compiler now knows
   const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
@@ -314,8 +349,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   // The weights are on their way before the kernel in front has finished: they
   // were laid out before it (the layout kernel lets nothing start before its
   // end). x and y are touched after it.
-  pdl_wait();
-  pdl_launch_dependents();
+  if (!WIDE) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
 
   // x: this CTA's K range as fp16, rows 64 bytes apart modulo 128 (the four
   // 16-byte reads of two tokens fill the banks), then the powers [step][token]
@@ -323,6 +360,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   float* s_power = reinterpret_cast<float*>(s_x + static_cast<size_t>(a.T) * x_stride);
   const X* x = static_cast<const X*>(a.x);
   constexpr int kAhead = 8;  // loads in flight
+  bool inexact = false;  // some element does not come out as scaled fp16
   for (int unit0 = tid >> 4; unit0 < a.T * cta_steps; unit0 += kAhead * (kMvThreads / 16)) {
     Pack<X, 8> p[kAhead];
 #pragma unroll
@@ -343,7 +381,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
       if (unit >= a.T * cta_steps) continue;
       const int t = unit / cta_steps, step = unit - t * cta_steps;
       uint4 out;
-      if constexpr (kScaledX<X>) {
+      if constexpr (SCALED) {
         float f[8], m = 0.f;
         unpack(p[j], f);
 #pragma unroll
@@ -351,19 +389,20 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
         const unsigned half = 0xFFFFu << (lane & 16);  // the units of a warp end apart
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
-        // 2^(14 - e), e the exponent of m or the even one above it (at least
-        // -112), and 2^(e - 14) to take it back, or its root if that is above 1:
-        // all are normal
-        const int e = max(15, static_cast<int>(__float_as_uint(m) >> 23) | 1), back = e - 141;
+        // 2^(14 - e) and back, e the exponent of m (at least -112: both are normal)
+        const int e = max(15, static_cast<int>(__float_as_uint(m) >> 23));
         const float scale = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+        const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+        inexact |= e >= 127 + kMvHuge;
         uint32_t* w = &out.x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 h = __floats2half2_rn(f[2 * i] * scale, f[2 * i + 1] * scale);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          const float2 v = make_float2(f[2 * i], f[2 * i + 1]);
+          w[i] = pack2(mul2(v, make_float2(scale, scale)), __half());
+          const float2 held = mul2(unpack2(w[i], __half()), make_float2(back, back));
+          inexact |= held.x != v.x || held.y != v.y;  // (a NaN says so too)
         }
-        if ((lane & 15) == 0)
-          s_power[step * kMvTokens + t] = __uint_as_float(static_cast<uint32_t>(127 + (back > 0 ? back / 2 : back)) << 23);
+        if ((lane & 15) == 0) s_power[step * kMvTokens + t] = back;
       } else {
         out = *reinterpret_cast<const uint4*>(&p[j]);
       }
@@ -372,7 +411,19 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
   }
   // what the lanes of absent tokens read, at every step
   if (tid < kMvStep * 2 / 16) reinterpret_cast<uint4*>(s_zero)[tid] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
+  if constexpr (SCALED) {
+    int* any = reinterpret_cast<int*>(s_zero + kMvStep * 2);
+    if (tid == 0) *any = 0;
+    __syncthreads();
+    if (inexact) *any = 1;
+    __syncthreads();
+    if (*any) {
+      cp_async_wait<0>();
+      return matvec_cta_wide<FMT, GROUPS, NT, DEPTH, S, X>(a, s_dyn, s_red, s_zero);
+    }
+  } else {
+    __syncthreads();
+  }
 
   const uint8_t* xs[NT];  // this lane's token (in each N tile) at the warp's first block
   int xs_step[NT];
@@ -392,7 +443,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
     __syncwarp();  // every lane's share has arrived
     Block<SW> b;
     read_block(b, ring + at_slot, lane);
-    multiply_block<FMT, GROUPS, NT, S, X>(acc, b, x_at, p_at, lane);
+    multiply_block<FMT, GROUPS, NT, WIDE, S, X>(acc, b, x_at, p_at, lane);
     at_slot = at_slot + BYTES == DEPTH * BYTES ? 0 : at_slot + BYTES;
   };
   auto walk = [&]() {  // a tile's blocks of this warp
@@ -454,6 +505,21 @@ __global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
   }
+}
+
+template <int FMT, int GROUPS, int NT, int DEPTH, typename S, typename X>
+__device__ __noinline__ void matvec_cta_wide(const MvArgs a, uint8_t* s_dyn, float (*s_red)[NT][4][32],
+                                             uint8_t* s_zero) {
+  matvec_cta<FMT, GROUPS, NT, DEPTH, true, S, X>(a, s_dyn, s_red, s_zero);
+}
+
+template <int FMT, int GROUPS, int NT, int DEPTH, typename S, typename X>
+__global__ void __launch_bounds__(kMvThreads, 1) matvec_kernel(MvArgs a) {
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  __shared__ float s_red[kMvWarps][NT][4][32];
+  // (the ring behind it has to start on a line: 16 bytes off, 131072 x 4096 takes 48.7 us)
+  __shared__ __align__(128) uint8_t s_zero[kMvStep * 2 + 128];
+  matvec_cta<FMT, GROUPS, NT, DEPTH, false, S, X>(a, s_dyn, s_red, s_zero);
 }
 
 // ------------------------------------------------------------------ layout
