@@ -194,9 +194,11 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS > 0 ? THREADS : 512, WARP
       if (!a.norm) inv = 1.f;
       else back = inv * inv * (inv * (h_G * inv_h));
       if (a.gate_kind == MOE_GATE_TOKEN) {
-        gt = gate_value(a.gate_act, to_f32(*token_gate));
+        const float logit = to_f32(*token_gate);
+        gt = gate_value(a.gate_act, logit);
         token_gate += step * a.ld_gate;
-        if (rows.j == 0) *dg_out = from_f32<T>(gate_slope(a.gate_act, gt) * (a.alpha * (inv * h_G)));
+        if (rows.j == 0)
+          *dg_out = from_f32<T>(gate_with_slope(a.gate_act, logit).slope.v[0] * (a.alpha * (inv * h_G)));
       }
     }
     const float scale = a.alpha * gt;
@@ -215,12 +217,9 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS > 0 ? THREADS : 512, WARP
       if constexpr (AFTER) {
         const Values<V> h = row_values(rows, kH, i), w = get_factor(kSumBlock, i, c);
         if constexpr (ELEMENT) {  // its gradient takes the G without it
-          const Values<V> g = gate_values(a.gate_act, row_values(rows, kGate, i));
-          Values<V> dg = G * (h * (a.alpha * inv)) * w;
-#pragma unroll
-          for (int e = 0; e < V; ++e) dg.v[e] *= gate_slope(a.gate_act, g.v[e]);
-          store_values(rows, dg_out, i, dg);
-          G = G * g;
+          const Gate<V> g = gate_with_slope(a.gate_act, row_values(rows, kGate, i));
+          store_values(rows, dg_out, i, G * (h * (a.alpha * inv)) * w * g.slope);
+          G = G * g.value;
         }
         sums[kSumBlock][i] = fma(G * (gt * inv), h, sums[kSumBlock][i]);
         store_values(rows, dh_out, i, fma(h, -scale * back, w * (G * (scale * inv))));
@@ -322,8 +321,9 @@ __global__ void __launch_bounds__(1024) norm_backward_general_kernel(NormBackwar
     if (!after) continue;
     float gt = 1.f, gt_slope = 0.f;
     if (a.gate_kind == MOE_GATE_TOKEN) {
-      gt = gate_value(a.gate_act, to_f32(gate[0]));
-      gt_slope = gate_slope(a.gate_act, gt);
+      const Gate<1> g = gate_with_slope(a.gate_act, to_f32(gate[0]));
+      gt = g.value.v[0];
+      gt_slope = g.slope.v[0];
     }
     float inv = 1.f, back = 0.f;
     if (a.norm || a.gate_kind == MOE_GATE_TOKEN) {
@@ -348,10 +348,10 @@ __global__ void __launch_bounds__(1024) norm_backward_general_kernel(NormBackwar
       const float hf = to_f32(h[c]), w = weight_at(a.norm ? a.weight : nullptr, c), G = G_at(c);
       float g = 1.f;
       if (column_gate) {
-        g = gate_value(a.gate_act, to_f32(gate[c]));
+        const Gate<1> gs = gate_with_slope(a.gate_act, to_f32(gate[c]));
+        g = gs.value.v[0];
         if (a.gate_kind == MOE_GATE_ELEMENT)
-          static_cast<T*>(b.d_gate)[t * a.H + c] =
-              from_f32<T>(gate_slope(a.gate_act, g) * (a.alpha * G * (hf * inv * w)));
+          static_cast<T*>(b.d_gate)[t * a.H + c] = from_f32<T>(gs.slope.v[0] * (a.alpha * G * (hf * inv * w)));
       }
       const float gG = scale * (g * G);
       if (wants(b, kSumBlock))
@@ -403,8 +403,9 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(NormBackwardArgs b, in
   float gate = 1.f;
   if (a.gate_kind == MOE_GATE_CHANNEL) {
     const float w = load_weight<T, 1>(a.norm ? a.weight : nullptr, a.weight_f32, a.w_offset, c).v[0];
-    gate = gate_value(a.gate_act, to_f32(static_cast<const T*>(a.gate)[c]));
-    static_cast<T*>(b.d_gate)[c] = from_f32<T>(gate_slope(a.gate_act, gate) * w * v);
+    const Gate<1> g = gate_with_slope(a.gate_act, to_f32(static_cast<const T*>(a.gate)[c]));
+    gate = g.value.v[0];
+    static_cast<T*>(b.d_gate)[c] = from_f32<T>(g.slope.v[0] * w * v);
   }
   if (b.d_weight != nullptr) store_weight(b.d_weight, gate * v);
 }
