@@ -10,8 +10,9 @@ As in `binding`, every step runs in the CUDA library on torch's current
 stream, and a missing library raises. Arguments are checked and outputs
 allocated in csrc/block/calls.cpp: these calls are short at decode, and the
 checks in Python would take longer than the kernels. permute_tokens,
-unpermute_tokens, norm_before and norm_after take part in autograd; the
-*_backward functions are their gradients as plain calls. Rows may be strided
+unpermute_tokens, norm_before and norm_after take part in autograd (backward
+only: forward-mode tangents and tracing are refused); the *_backward functions
+are their gradients as plain calls. Rows may be strided
 (the elements of a row contiguous); anything else is made contiguous first.
 """
 import ctypes

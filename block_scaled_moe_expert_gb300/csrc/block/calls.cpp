@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -73,9 +74,13 @@ void check(int status, const char* what) {
 
 // ---------------------------------------------------------------- operands
 
-void same_device(const Tensor& t, int dev) {
+// What every operand is asked. The kernels run past torch's dispatcher: neither a
+// tangent nor a trace would learn of them.
+void operand(const Tensor& t, int dev) {
   TORCH_CHECK(t.is_cuda() && t.get_device() == dev,
               "all tensors must live on the current CUDA device (one device per call)");
+  TORCH_CHECK(!t._fw_grad(/*level=*/0).defined(), "forward-mode differentiation is not implemented for this operator");
+  TORCH_CHECK(!torch::jit::tracer::isTracing(), "this operator cannot be traced: its kernels are not torch operators");
 }
 
 int dtype_code(at::ScalarType t) {
@@ -108,7 +113,7 @@ First first(const Tensor& t, const char* what) {
   const int code = dtype_code(t.scalar_type());
   TORCH_CHECK_VALUE(code >= 0, what, " must be bfloat16, float16 or float32, got ", t.scalar_type());
   const int dev = t.is_cuda() ? c10::cuda::current_device() : -1;
-  same_device(t, dev);
+  operand(t, dev);
   First f;
   static_cast<Rows&>(f) = strided(t);
   TORCH_CHECK_VALUE(f.n <= INT32_MAX && f.H <= INT32_MAX, what, " is too large: ", t.sizes());
@@ -123,7 +128,7 @@ Rows like(const Tensor& t, const First& f, int64_t n, const char* what) {
                     t.scalar_type());
   TORCH_CHECK_VALUE(t.dim() == 2 && t.size(0) == n && t.size(1) == f.H, what, " must have the shape [", n, ", ", f.H,
                     "], got ", t.sizes());
-  same_device(t, f.dev);
+  operand(t, f.dev);
   return strided(t);
 }
 Rows like(const Maybe& t, const First& f, int64_t n, const char* what) { return t ? like(*t, f, n, what) : Rows(); }
@@ -133,7 +138,7 @@ Tensor output(const Maybe& out, const First& f, int64_t n, int64_t H) {
   TORCH_CHECK_VALUE(out->scalar_type() == f.type && out->dim() == 2 && out->size(0) == n && out->size(1) == H &&
                         out->is_contiguous(),
                     "out must be a contiguous ", f.type, " tensor of shape [", n, ", ", H, "]");
-  same_device(*out, f.dev);
+  operand(*out, f.dev);
   return *out;
 }
 
@@ -167,7 +172,7 @@ Plan sort_tokens(const Tensor& topk_idx, int E, int align) {
   TORCH_CHECK_VALUE(topk_idx.scalar_type() == at::kInt && topk_idx.dim() == 2,
                     "topk_idx must be an int32 tensor [T, K]");
   const int dev = topk_idx.is_cuda() ? c10::cuda::current_device() : -1;
-  same_device(topk_idx, dev);
+  operand(topk_idx, dev);
   const Tensor idx = topk_idx.contiguous();
   TORCH_CHECK_VALUE(idx.size(0) <= INT32_MAX && idx.size(1) <= INT32_MAX, "topk_idx is too large: ", idx.sizes());
   Plan p;
@@ -186,7 +191,7 @@ Plan sort_tokens(const Tensor& topk_idx, int E, int align) {
 First plan_rows(const Tensor& t, const Plan& p, int n, const char* what) {
   First f = first(t, what);
   TORCH_CHECK_VALUE(f.n == n, what, " has ", f.n, " rows, the plan ", n);
-  same_device(p.buffer, f.dev);
+  operand(p.buffer, f.dev);
   return f;
 }
 
@@ -194,7 +199,7 @@ Tensor plan_weights(const Maybe& w, const Plan& p, int dev) {
   if (!w) return Tensor();
   TORCH_CHECK_VALUE(w->scalar_type() == at::kFloat && w->dim() == 2 && w->size(0) == p.T && w->size(1) == p.K,
                     "topk_w must be a float32 tensor [", p.T, ", ", p.K, "]");
-  same_device(*w, dev);
+  operand(*w, dev);
   return w->contiguous();
 }
 
@@ -247,7 +252,7 @@ Tensor norm_weight(const Maybe& w, const First& f, const char* what) {
   TORCH_CHECK_VALUE(w->dim() == 1 && w->size(0) == f.H, what, " must have the shape (", f.H, ",), got ", w->sizes());
   TORCH_CHECK_VALUE(w->scalar_type() == f.type || w->scalar_type() == at::kFloat, what, " must be ", f.type,
                     " or float32, got ", w->scalar_type());
-  same_device(*w, f.dev);
+  operand(*w, f.dev);
   return w->contiguous();
 }
 
@@ -272,7 +277,7 @@ Gate gate_arg(const Maybe& gate, const std::string& act, const First& f) {
   TORCH_CHECK_VALUE(g.act >= 0, "gate_act must be 'none', 'sigmoid' or 'tanh', got '", act, "'");
   if (!gate) return g;
   TORCH_CHECK_VALUE(gate->scalar_type() == f.type, "gate must be ", f.type, " like x, got ", gate->scalar_type());
-  same_device(*gate, f.dev);
+  operand(*gate, f.dev);
   if (gate->dim() == 1 && gate->size(0) == f.H) {
     g.kind = MOE_GATE_CHANNEL;
     g.t = gate->contiguous();
@@ -397,9 +402,9 @@ MatvecWeights prepare_matvec(int qfmt, int N, int K, int group, bool swiglu, con
   TORCH_CHECK_VALUE(!zero || (qfmt == MOE_Q_INT4 && zero->scalar_type() == at::kByte && shaped(*zero, groups)),
                     "w_zero must be uint8 [", N, ", ", groups, "], for int4 weights");
   const int dev = w.is_cuda() ? c10::cuda::current_device() : -1;
-  same_device(w, dev);
-  same_device(scale, dev);
-  if (zero) same_device(*zero, dev);
+  operand(w, dev);
+  operand(scale, dev);
+  if (zero) operand(*zero, dev);
   const Tensor wc = w.contiguous(), sc = scale.contiguous(), zc = zero ? zero->contiguous() : Tensor();
   MatvecWeights m{qfmt, N, K, group, qfmt == MOE_Q_FP4 ? 0 : dtype_code(st), swiglu,
                   at::empty({static_cast<int64_t>(bytes)}, w.options())};
@@ -414,7 +419,7 @@ Tensor matvec(const Tensor& x, const MatvecWeights& m, std::optional<double> lim
   TORCH_CHECK_VALUE(f.code != MOE_FP32, "matvec takes bfloat16 or float16 x, got ", f.type);
   TORCH_CHECK_VALUE(f.H == m.K, "x has ", f.H, " columns, the prepared weights ", m.K);
   TORCH_CHECK_VALUE(!limit || m.swiglu, "swiglu_limit is for weights prepared with swiglu=True");
-  same_device(m.prepared, f.dev);
+  operand(m.prepared, f.dev);
   const Tensor y = output(out, f, f.n, m.swiglu ? m.N / 2 : m.N);
   check(api.moe_matvec(m.qfmt, m.N, m.K, m.group, m.swiglu, limit ? static_cast<float>(*limit) : -1.f, m.scale_dtype,
                        m.prepared.const_data_ptr(), f.code, f.ptr(), f.ld, static_cast<int>(f.n), y.data_ptr(),
