@@ -259,7 +259,8 @@ def prepare_matvec(weights, swiglu=False):
 
 def matvec(x, prepared, swiglu_limit=None, out=None):
     """x [T, K] bf16 or fp16 times the prepared weights, [T, N] ([T, N/2] with
-    SwiGLU) of x's type, for few tokens. Not differentiable."""
+    SwiGLU) of x's type, for few tokens. It has no gradient: an x that requires
+    one is refused while gradients are recorded."""
     return _calls.matvec(x, prepared._weights, swiglu_limit, out)
 
 

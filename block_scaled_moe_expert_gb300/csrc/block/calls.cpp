@@ -7,6 +7,7 @@
 // library that `binding` loads, by address.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -418,6 +419,8 @@ Tensor matvec(const Tensor& x, const MatvecWeights& m, std::optional<double> lim
   const First f = first(x, "x");
   TORCH_CHECK_VALUE(f.code != MOE_FP32, "matvec takes bfloat16 or float16 x, got ", f.type);
   TORCH_CHECK_VALUE(f.H == m.K, "x has ", f.H, " columns, the prepared weights ", m.K);
+  TORCH_CHECK_VALUE(!x.requires_grad() || !c10::GradMode::is_enabled(),
+                    "matvec has no gradient: call it without gradients (torch.no_grad) or on x.detach()");
   TORCH_CHECK_VALUE(!limit || m.swiglu, "swiglu_limit is for weights prepared with swiglu=True");
   operand(m.prepared, f.dev);
   const Tensor y = output(out, f, f.n, m.swiglu ? m.N / 2 : m.N);

@@ -53,3 +53,13 @@ def test_tracing_is_refused():
         with pytest.raises(RuntimeError):
             torch.jit.trace(call, (arg,), check_trace=False)
 
+
+def test_matvec_of_tracked_activations_is_refused():
+    x, _, _, _, _, prepared = operands()
+    want = M.matvec(x, prepared)
+    x.requires_grad_()
+    with pytest.raises(ValueError):
+        M.matvec(x, prepared)
+    with torch.no_grad():
+        assert torch.equal(M.matvec(x, prepared), want)
+    assert torch.equal(M.matvec(x.detach(), prepared), want)
