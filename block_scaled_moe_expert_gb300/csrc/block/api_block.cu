@@ -62,9 +62,10 @@ moe_status rows_call(int dtype, const void* in, int64_t ld_in, const void* other
   return check_ptrs({{in, es}, {other, es}, {topk_w, 4}, {dots, 4}, {plan, 256}, {out, es}}, &d);
 }
 
-bool gate_ok(int kind, int act, const void* gate) {
+// A gate with one value for each token has none for no tokens.
+bool gate_ok(int kind, int act, const void* gate, int T) {
   if (kind < MOE_GATE_NONE || kind > MOE_GATE_ELEMENT || act < MOE_GATE_LINEAR || act > MOE_GATE_TANH) return false;
-  return (kind == MOE_GATE_NONE) == (gate == nullptr);
+  return (T == 0 && kind != MOE_GATE_CHANNEL) || (kind == MOE_GATE_NONE) == (gate == nullptr);
 }
 
 bool norm_shape_ok(int T, int H) { return T >= 0 && H >= 1 && H <= kMaxNormWidth; }
@@ -209,7 +210,7 @@ moe_status moe_norm_after(int dtype, const void* x, int64_t ld_x, const void* h,
   if (!dtype_ok(dtype) || ld_x < 0 || ld_h < 0 || ld_gate < 0) return MOE_ERR_INVALID_ARG;
   if (!norm_shape_ok(T, H)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
-  if (!gate_ok(gate_kind, gate_act, gate)) return MOE_ERR_INVALID_ARG;
+  if (!gate_ok(gate_kind, gate_act, gate, T)) return MOE_ERR_INVALID_ARG;
   if (x == nullptr || h == nullptr || r == nullptr) return MOE_ERR_INVALID_ARG;
   if ((!norm && weight != nullptr) || (y == nullptr && next_weight != nullptr)) return MOE_ERR_INVALID_ARG;
   DevInfo d;
@@ -232,7 +233,7 @@ moe_status moe_norm_after_backward(int dtype, const void* dr, int64_t ld_dr, con
   if (!dtype_ok(dtype) || ld_dr < 0 || ld_dy < 0 || ld_h < 0 || ld_r < 0 || ld_gate < 0) return MOE_ERR_INVALID_ARG;
   if (!norm_shape_ok(T, H)) return MOE_ERR_UNSUPPORTED_SHAPE;
   const bool any = T > 0;
-  if (any && !gate_ok(gate_kind, gate_act, gate)) return MOE_ERR_INVALID_ARG;
+  if (!gate_ok(gate_kind, gate_act, gate, T)) return MOE_ERR_INVALID_ARG;
   if (gate_kind != MOE_GATE_NONE && d_gate == nullptr && (any || gate_kind == MOE_GATE_CHANNEL))
     return MOE_ERR_INVALID_ARG;
   if (any && (dr == nullptr || h == nullptr || dh == nullptr || (dy != nullptr && r == nullptr)))
@@ -249,7 +250,8 @@ moe_status moe_norm_after_backward(int dtype, const void* dr, int64_t ld_dr, con
   const bool column = gate_kind == MOE_GATE_CHANNEL;
   const moe_status s =
       check_ptrs({row(dr), row(dy), row(h), row(dy != nullptr ? r : nullptr), {weight, ws}, {next_weight, ws},
-                  row(gate), row(dx), row(dh), {d_weight, ws}, {any || column ? d_gate : nullptr, es},
+                  {any || column ? gate : nullptr, es}, row(dx), row(dh), {d_weight, ws},
+                  {any || column ? d_gate : nullptr, es},
                   {d_next_weight, ws}, {workspace, 256}}, &d);
   if (s != MOE_OK) return s;
   NormBackwardArgs b = {};

@@ -124,6 +124,27 @@ def test_norms_check_arguments_before_the_device(L):
                                       size_t(ws), None) == INVALID
 
 
+def test_gradient_without_tokens_checks_the_channel_gate(L):
+    """Its d_gate is written for no tokens too, and the kernel reads the gate."""
+    a, odd, f = vp(0x100000), vp(0x100001), c_float(1e-6)
+    L.moe_norm_backward_workspace_bytes.restype = size_t
+    ws = L.moe_norm_backward_workspace_bytes(64)
+
+    def back(kind, gate, act=0, dgate=a, T=0):
+        return L.moe_norm_after_backward(0, None, i64(64), None, i64(64), None, i64(64), None, i64(64), 1, None, None, 0, f,
+                                         kind, act, gate, i64(64), f, f, f, f, T, 64, None, None, None, dgate, None, a,
+                                         size_t(ws), None)
+
+    assert back(1, None) == INVALID and back(1, odd) == ALIGNMENT
+    assert back(1, a, dgate=None) == INVALID and back(1, a, dgate=odd) == ALIGNMENT
+    for act in (-1, 3):
+        assert back(1, a, act=act) == INVALID and back(2, None, act=act) == INVALID
+    for kind in (-1, 4):
+        assert back(kind, None) == INVALID and back(kind, a) == INVALID
+    # gates of no elements have nothing to check
+    assert back(2, None, dgate=None) == 0 and back(3, None, dgate=None) == 0 and back(0, None, dgate=None) == 0
+
+
 def test_matvec_sizes_and_refusals(L):
     L.moe_matvec_prepared_bytes.restype = size_t
     for fmt, N, K, group, swiglu in [(0, 4096, 7168, 32, 1), (0, 17, 160, 32, 0), (1, 1000, 2880, 128, 0),
