@@ -12,6 +12,16 @@ constexpr int kMaxRowAlign = 256;
 constexpr int kMaxRowWidth = 65536;   // permute / unpermute
 constexpr int kMaxNormWidth = 16384;  // norms
 
+// Dynamic shared memory that a launch of `kernel` may ask for. The limit belongs to
+// the kernel, not to the launch: every call sets the same one, so that another
+// host thread's call cannot lower it between the two.
+constexpr int kMaxDynSmem = 226 * 1024;  // beside at most 1 KB of static shared memory
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t smem, int most = kMaxDynSmem) {
+  if (smem > static_cast<size_t>(most)) return cudaErrorInvalidValue;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // The sort plan as the kernels see it.
 struct SortPlan {
   uint32_t* status;

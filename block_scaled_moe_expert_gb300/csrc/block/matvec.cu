@@ -592,7 +592,7 @@ template <int FMT, int GROUPS, int NT, int DEPTH, typename S, typename X>
 cudaError_t run(const MvArgs& a, int grid, cudaStream_t st) {
   auto* k = matvec_kernel<FMT, GROUPS, NT, DEPTH, S, X>;
   const size_t smem = kMvWarps * DEPTH * block_bytes(FMT, kMvStep / GROUPS) + x_smem(a);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = allow_smem(k, smem, kMvMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;

@@ -173,7 +173,7 @@ cudaError_t run(const NormArgs& a, int threads, int num_sms, cudaStream_t st) {
   int blocks = std::max(1, (CH * V <= 16 ? 1024 : 512) / threads);
   if (smem > 0) blocks = std::max(1, std::min<int>(blocks, kQueueSmem / smem));
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(k, smem);
     if (e != cudaSuccess) return e;
   }
   const int rows = ceil_div(a.T, WARP ? threads / 32 : 1);

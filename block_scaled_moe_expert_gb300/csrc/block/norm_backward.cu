@@ -426,7 +426,7 @@ cudaError_t run(const NormBackwardArgs& b, int threads, int num_sms, cudaStream_
   int blocks = std::max(1, (THREADS == 256 ? CH <= 8 ? 1024 : 768 : 512) / threads);
   if (smem > 0) blocks = std::max(1, std::min<int>(blocks, kQueueSmem / smem));
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(k, smem);
     if (e != cudaSuccess) return e;
   }
   const int rows = ceil_div(a.T, WARP ? threads / 32 : 1);
@@ -440,8 +440,7 @@ cudaError_t run_general(const NormBackwardArgs& b, int num_sms, cudaStream_t st,
   const bool block = b.d_weight != nullptr || b.f.gate_kind == MOE_GATE_CHANNEL;
   const size_t smem = sizeof(float) * (block + (b.d_next_weight != nullptr)) * b.f.H;
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_backward_general_kernel<T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(norm_backward_general_kernel<T>, smem);
     if (e != cudaSuccess) return e;
   }
   *parts = std::min(std::min(b.f.T, num_sms), kNormParts);

@@ -212,8 +212,7 @@ constexpr size_t kSortMaxSmem = sizeof(int) * (kSortWarps + 3) * (kMaxExperts + 
 bool wide_clusters_fit() {
   static const bool fit = [] {
     if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSortMaxSmem)) != cudaSuccess) {
+        allow_smem(sort_kernel, kSortMaxSmem, kSortMaxSmem) != cudaSuccess) {
       cudaGetLastError();
       return false;
     }
@@ -249,8 +248,7 @@ cudaError_t launch_sort(const int32_t* topk_idx, const SortPlan& p, cudaStream_t
   const int threads = std::max(count_warps, ceil_div(p.E + 1, 32)) * 32;
   const size_t smem = sizeof(int) * (count_warps + 3) * (p.E + 1);
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(sort_kernel, smem, kSortMaxSmem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
