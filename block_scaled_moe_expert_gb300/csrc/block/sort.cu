@@ -18,6 +18,8 @@
 // 12.7 us (8 CTAs: 16.5), 131,072 over 512 20 us (8 CTAs: 30).
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "block_internal.cuh"
 #include "../ptx.cuh"
 
@@ -208,33 +210,38 @@ namespace {
 
 constexpr size_t kSortMaxSmem = sizeof(int) * (kSortWarps + 3) * (kMaxExperts + 1);
 
-// Clusters of 16 CTAs need a GPC with that many SMs: asked once.
+// Whether the current device runs clusters of 16 CTAs (they need a GPC with that
+// many SMs): asked once a device. That the kernel may have them is a limit of the
+// kernel there and is set in every call, as the one on shared memory is.
 bool wide_clusters_fit() {
-  static const bool fit = [] {
-    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        allow_smem(sort_kernel, kSortMaxSmem, kSortMaxSmem) != cudaSuccess) {
-      cudaGetLastError();
-      return false;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = 16;
-    cfg.blockDim = kSortThreads;
-    cfg.dynamicSmemBytes = kSortMaxSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 16;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      return false;
-    }
-    return clusters > 0;
-  }();
-  return fit;
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // 0: not asked yet, 1: yes, -1: no
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices ||
+      cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      allow_smem(sort_kernel, kSortMaxSmem, kSortMaxSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (const int answer = known[dev].load(std::memory_order_relaxed)) return answer > 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = 16;
+  cfg.blockDim = kSortThreads;
+  cfg.dynamicSmemBytes = kSortMaxSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 16;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, sort_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  known[dev].store(clusters > 0 ? 1 : -1, std::memory_order_relaxed);
+  return clusters > 0;
 }
 
 }  // namespace

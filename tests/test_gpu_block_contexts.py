@@ -1,6 +1,8 @@
-"""GPU: the C ABI from several host threads of one process: what a
+"""GPU: the C ABI from several contexts and host threads of one process: what a
 call sets up for its own launch does not fail another's."""
 import ctypes
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -11,6 +13,50 @@ from block_scaled_moe_expert_gb300 import binding as B
 pytestmark = pytest.mark.gpu
 
 vp, c_int, i64, size_t, c_float = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+
+TWO_CONTEXTS = """
+import ctypes, sys
+cu, L = ctypes.CDLL("libcuda.so.1"), ctypes.CDLL(sys.argv[1])
+vp = ctypes.c_void_p
+def ok(r):
+    assert r == 0, r
+class Layout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("total", "status", "counts", "offsets", "inv", "row_slot")] + [("rows", ctypes.c_int32)]
+T, E, K = 8192, 16, 4
+lay = Layout()
+ok(L.moe_query_sort_layout(T, E, K, 1, ctypes.byref(lay)))
+ok(cu.cuInit(0))
+host = (ctypes.c_int32 * (T * K))(*[i % E for i in range(T * K)])
+for turn in range(2):
+    ctx, idx, plan = vp(), vp(), vp()
+    ok(cu.cuCtxCreate_v2(ctypes.byref(ctx), 0, 0))
+    ok(cu.cuMemAlloc_v2(ctypes.byref(idx), ctypes.c_size_t(4 * T * K)))
+    ok(cu.cuMemAlloc_v2(ctypes.byref(plan), ctypes.c_size_t(lay.total)))
+    ok(cu.cuMemcpyHtoD_v2(idx, host, ctypes.c_size_t(4 * T * K)))
+    st = L.moe_sort_tokens(idx, T, E, K, 1, plan, ctypes.c_size_t(lay.total), None)
+    ok(cu.cuCtxSynchronize())
+    print("context", turn, "status", st)
+    assert st == 0
+    counts = (ctypes.c_int32 * E)()
+    ok(cu.cuMemcpyDtoH_v2(counts, vp(plan.value + lay.counts), ctypes.c_size_t(4 * E)))
+    assert list(counts) == [T * K // E] * E
+"""
+
+
+def test_large_sorts_in_a_second_context():
+    """Launch limits belong to a context: each one has its own."""
+    r = subprocess.run([sys.executable, "-c", TWO_CONTEXTS, B.LIB_PATH], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="one device")
+def test_large_sorts_on_a_second_device():
+    import block_scaled_moe_expert_gb300 as M
+    for dev in range(2):
+        with torch.cuda.device(dev):
+            idx = (torch.arange(20000 * 7, dtype=torch.int32, device="cuda") % 60).reshape(20000, 7)
+            assert M.sort_tokens(idx, 60).counts.tolist() == [-(-(140000 - e) // 60) for e in range(60)]
+
 
 def in_two_threads(call):
     """call(side, stream) from two host threads at once, each on its own
