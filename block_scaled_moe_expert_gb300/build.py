@@ -1,10 +1,11 @@
 """Compile the CUDA library (csrc/*.cu, csrc/block/*.cu) for sm_103a into libbsmoe.so, in tree.
 
 Each translation unit is compiled in parallel with nvcc; the objects are
-linked into one shared library next to this file. Beside them the host compiler
-builds csrc/block/calls.cpp, Python's way into include/moe_block.h, against the
-installed torch. Rebuilds only what changed (object newer than its source and
-every header).
+linked into one shared library next to this file; that takes the CUDA toolkit
+alone. A step of its own, left out where torch is not installed, builds
+csrc/block/calls.cpp (_calls.so), Python's way into include/moe_block.h, with the
+host compiler against the installed torch. Rebuilds only what changed (object
+newer than its source and every header).
 """
 import concurrent.futures as cf
 import glob
@@ -62,56 +63,70 @@ def _calls_command(src):
             "-o", CALLS, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
-def _calls_job(newest_header):
-    """The command that builds _calls.so, or None where it is up to date (it
-    belongs to one torch, whose version stands beside it)."""
-    import torch
-    src = os.path.join(SRC, "block", "calls.cpp")
-    stamp = os.path.join(BUILD, "calls.torch")
-    seen = open(stamp).read() if os.path.exists(stamp) else ""
-    if seen == torch.__version__ and not _stale(CALLS, src, newest_header):
+def _run(cmd, what):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("%s failed: %s\n%s" % (what, " ".join(cmd), res.stdout + res.stderr))
+    return res.stdout + res.stderr
+
+
+def build_library(ptxas_verbose=False):
+    """Build libbsmoe.so; returns the compilers' messages. Raises RuntimeError on
+    failure."""
+    nvcc = _nvcc()
+    os.makedirs(BUILD, exist_ok=True)
+    newest_header = max([os.path.getmtime(h) for h in _headers()] + [0])
+    extra = ["-Xptxas", "-v"] if ptxas_verbose else []
+    jobs, objs = [], []
+    for src in _sources():
+        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
+        objs.append(obj)
+        if ptxas_verbose or _stale(obj, src, newest_header):
+            jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj])
+    logs = []
+    if jobs:
+        with cf.ThreadPoolExecutor(max_workers=min(12, len(jobs))) as ex:
+            logs = list(ex.map(lambda c: _run(c, "nvcc"), jobs))
+    if any(not os.path.exists(LIB) or os.path.getmtime(LIB) < os.path.getmtime(o) for o in objs):
+        _run([nvcc, *ARCH, "-shared", "-o", LIB, *objs], "link")
+    return logs
+
+
+def build_calls():
+    """Build _calls.so for the installed torch (the stamp beside it says which);
+    returns its path, or None without torch. Raises RuntimeError on failure."""
+    try:
+        import torch
+    except ImportError:
         return None
-    with open(stamp, "w") as f:
-        f.write(torch.__version__)
-    return _calls_command(src)
+    os.makedirs(BUILD, exist_ok=True)
+    src, stamp = os.path.join(SRC, "block", "calls.cpp"), os.path.join(BUILD, "calls.torch")
+    seen = open(stamp).read() if os.path.exists(stamp) else ""
+    newest_header = max(os.path.getmtime(h) for h in glob.glob(os.path.join(INCLUDE, "*.h")))
+    if seen != torch.__version__ or _stale(CALLS, src, newest_header):
+        for old in (stamp, CALLS):
+            if os.path.exists(old):
+                os.remove(old)
+        _run(_calls_command(src), "g++")
+        with open(stamp, "w") as f:
+            f.write(torch.__version__)
+    return CALLS
 
 
 def build(verbose=False, ptxas_verbose=False):
-    """Build libbsmoe.so and _calls.so; returns the library's path. Raises
-    RuntimeError on failure."""
-    nvcc = _nvcc()
-    os.makedirs(BUILD, exist_ok=True)
-    sources = _sources()
-    newest_header = max([os.path.getmtime(h) for h in _headers()] + [0])
-    extra = ["-Xptxas", "-v"] if ptxas_verbose else []
-    jobs = []
-    for src in sources:
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        if ptxas_verbose or _stale(obj, src, newest_header):
-            jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj])
-    calls = _calls_job(newest_header)
-    commands = jobs + ([calls] if calls else [])
-    logs = []
-    if commands:
-        with cf.ThreadPoolExecutor(max_workers=min(12, len(commands))) as ex:
-            for cmd, res in zip(commands, ex.map(lambda c: subprocess.run(c, capture_output=True, text=True),
-                                                 commands)):
-                logs.append(res.stdout + res.stderr)
-                if res.returncode != 0:
-                    if cmd is calls and os.path.exists(CALLS):
-                        os.remove(CALLS)
-                    raise RuntimeError("%s failed: %s\n%s" % (os.path.basename(cmd[0]), " ".join(cmd),
-                                                             res.stdout + res.stderr))
-    objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in sources]
-    if jobs or not os.path.exists(LIB):
-        cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError("link failed: %s\n%s" % (" ".join(cmd), res.stdout + res.stderr))
+    """Build libbsmoe.so and, with torch, _calls.so; returns the library's path.
+    Raises RuntimeError on failure; the library is there all the same where only
+    the calls failed."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(build_calls)
+        logs = build_library(ptxas_verbose)
+        made = calls.result()
     if verbose:
         for l in logs:
             if l.strip():
                 print(l)
+        if made is None:
+            print("torch is not installed: built without Python's calls (_calls.so)")
     return LIB
 
 
