@@ -18,7 +18,7 @@
 //   sum h w g G = sum h w g dr + inv_r sum h w g (w' dy) - back sum h w g r.
 //
 // Measured: norm_after's gradient with token gate and next norm, 8192 rows of
-// 4096 bf16 columns, 85 us with the column sums, 4.8 TB/s (a plain copy: 6.8).
+// 4096 bf16 columns, 85 us with the column sums, 4.7 TB/s (a plain copy: 6.8).
 // What is left is the latency of its two passes with 16 warps an SM: the column
 // sums and the row leave no registers for more. Three stages of rows instead of
 // two: one block an SM fits, 133 us. Half as many columns a thread: 121 us.

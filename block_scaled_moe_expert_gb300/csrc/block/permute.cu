@@ -248,8 +248,11 @@ __global__ void __launch_bounds__(kPermThreads, kPermBlocks) gather_kernel(Gathe
 // Warps per token: one where the tokens alone give every SM a few rounds of
 // warps, more (up to a block) for fewer tokens, as far as the row has work for
 // them. The dots' join over a token's warps costs more than a shorter tail
-// gives, so with dots one round is enough (4096 tokens of 4096 bf16 columns,
-// K = 2: 29.6 us against 34.1; 8192 of 7168, K = 8, no dots: 173 against 165).
+// gives, so with dots one round is enough. Measured, one round against four:
+// 4096 tokens of 4096 bf16 columns, K = 2, gradient of unpermute 26.5 us against
+// 32.1, of permute 24.9 against 28.6; without dots 8192 of 7168, K = 8, permute
+// 190 against 170. (It is not so for all: 4096 of 4096, K = 2, without dots 15.1
+// against 17.9, and 8192 of 7168, K = 8, gradient of unpermute 330 against 309.)
 int warps_per_token(int T, int H, int V, bool dots) {
   const int64_t enough = 152 * (dots ? 32 : 128);
   int wpt = 1;

@@ -11,7 +11,8 @@
  *
  * The conventions of moe_experts.h hold: device pointers of the calling
  * thread's current device, an asynchronous call on `stream`, nothing
- * allocated, a non-MOE_OK status means that nothing was enqueued, element
+ * allocated, a non-MOE_OK status means that nothing was enqueued, calls from
+ * several host threads and for several devices do not disturb each other, element
  * types named by a moe_dtype argument and otherwise not checked. Row strides
  * (ld_*) count elements, from 0 (the same row for every token, inputs only)
  * up; the elements of a row are contiguous. Any alignment of at least the
@@ -164,7 +165,8 @@ moe_status moe_norm_after_backward(int dtype, const void* dr, int64_t ld_dr, con
                                    size_t workspace_bytes, void* stream);
 
 /* ------------------------------------- products with 4-bit weights -------
- * y[t, n] = sum over k of x[t, k] * W[n, k], sums in fp32, one rounding.
+ * y[t, n] = sum over k of x[t, k] * W[n, k], sums in fp32, one rounding. Every
+ * finite x counts in full, whatever else its row holds.
  *   MOE_Q_FP4:  the weights of MOE_W_FP4: codes u8 [N, K / 2] (e2m1, low
  *               nibble = even k), scale u8 [N, K / 32] (UE8M0; 255 = NaN);
  *   MOE_Q_INT4: codes u8 [N, K / 2] (0..15, low nibble = even k),
