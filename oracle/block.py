@@ -89,13 +89,13 @@ def gate_value(gate, act):
     return torch.sigmoid(g) if act == "sigmoid" else torch.tanh(g) if act == "tanh" else g
 
 
-def gate_slope(gate, act, mag=False):
-    g = gate_value(gate, act)
-    if act == "sigmoid":
-        return g * (1 + g) if mag else g * (1 - g)
-    if act == "tanh":
-        return 1 + g * g if mag else 1 - g * g
-    return torch.ones_like(g)
+def gate_slope(gate, act):
+    """d act / d gate, from the gate's distance from 0: 1 - g has no bits left
+    where g has come near 1. Never negative: its own magnitude."""
+    e = torch.exp(-gate.double().abs() * (2 if act == "tanh" else 1))
+    if act == "none":
+        return torch.ones_like(e)
+    return e / (1 + e) ** 2 * (4 if act == "tanh" else 1)
 
 
 def norm_after(x, h, w, gate, act, alpha, beta, eps, offset, has_norm, mag=False):
@@ -133,7 +133,7 @@ def norm_after_backward(dr, h, w, gate, act, alpha, beta, eps, offset, has_norm,
         g = g if gate is None else g.abs()
     dgate = None
     if gate is not None:
-        full = alpha * G * z * gate_slope(gate, act, mag)
+        full = alpha * G * z * gate_slope(gate, act)
         dgate = full.sum(0) if gate.dim() == 1 else full.sum(1, keepdim=True) if gate.shape[1] == 1 else full
     dz, dw = alpha * g * G, None
     dh = dz * torch.ones_like(h, dtype=torch.float64)

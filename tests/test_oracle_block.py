@@ -1,5 +1,7 @@
 """CPU: the 64-bit oracle of the operators around the experts forward, against
 closed forms, autograd and differences."""
+import math
+
 import pytest
 import torch
 
@@ -72,6 +74,21 @@ def test_gradients_of_the_norms(kind, act, has_norm):
             down = loss()[0]
             t += step * d
             assert abs((up - down) / (2 * step) - (g * d).sum()) < 1e-6 * (1 + (g * d).abs().sum())
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "tanh"])
+def test_slopes_of_saturated_gates(act):
+    """Even in the gate, log-linear in its distance from 0 far out, and their own magnitude."""
+    v = torch.linspace(0, 60, 241, dtype=torch.float64)
+    s = O.gate_slope(v, act)
+    assert torch.allclose(s, O.gate_slope(-v, act), rtol=1e-14, atol=0) and (s > 0).all()
+    rate = 1 if act == "sigmoid" else 2
+    far = v > 20
+    assert torch.allclose(s[far].log() + rate * v[far], torch.full_like(v[far], 0.0 if rate == 1 else math.log(4)),
+                          atol=1e-8)
+    near = v < 3
+    g = O.gate_value(v[near], act)
+    assert torch.allclose(s[near], g * (1 - g) if act == "sigmoid" else 1 - g * g, rtol=1e-12, atol=0)
 
 
 def test_norm_of_a_constant_row_and_magnitudes():
