@@ -76,6 +76,17 @@ def test_small_activations_beside_a_large_one_that_meets_zeros(fmt, group, gap):
         check(x, weights, M.matvec(x, M.prepare_matvec(weights)))
 
 
+def test_large_activations_in_a_part_of_one_row():
+    """CTAs that share a tile's K range, and passes of tokens, need not agree."""
+    for T, N, K, where in ((3, 16, 8192, 0), (3, 16, 8192, 8191), (1, 40, 16384, 5000), (20, 33, 4096, 700)):
+        g = C.gen(T + K + where)
+        weights = weights_of(g, "fp4", N, K, 32, -4)
+        x = C.randn(g, T, K, dtype=torch.bfloat16)
+        x[T // 2, where] = 2.0 ** 60
+        weights["w"][:, where // 2] = 0
+        check(x, weights, M.matvec(x, M.prepare_matvec(weights)))
+
+
 def test_the_whole_range_of_bf16_in_one_row():
     """Zero weights for all but one magnitude at a time, from the smallest
     subnormal to the largest exponent: that magnitude alone is the result."""
