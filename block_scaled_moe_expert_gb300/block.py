@@ -1,16 +1,20 @@
-"""Operators around the experts forward (include/moe_block.h).
+"""Operators around the experts forward (include/moe_block.h, include/moe_route_fp4.h).
 
 * sort_tokens / permute_tokens / unpermute_tokens: tokens sorted by expert and
   back with the routing weights applied, and their gradients;
 * norm_before / norm_after: the norms around a block fused with its gate, the
   residual scale and the next block's norm, and their gradients;
-* prepare_matvec / matvec: products of a few tokens with 4-bit weights.
+* prepare_matvec / matvec: products of a few tokens with 4-bit weights;
+* route_tokens: the router's choice of experts with its weights, and its gradient;
+* quantize_fp4 / dequantize_fp4: the FP4 format of the weights and back;
+  prepare_matmul_fp4 / matmul_fp4: products of many tokens with FP4 weights and
+  activations quantized to FP4 on the way.
 
 As in `binding`, every step runs in the CUDA library on torch's current
 stream, and a missing library raises. Arguments are checked and outputs
 allocated in csrc/block/calls.cpp: these calls are short at decode, and the
 checks in Python would take longer than the kernels. permute_tokens,
-unpermute_tokens, norm_before and norm_after take part in autograd (backward
+unpermute_tokens, norm_before, norm_after and route_tokens take part in autograd (backward
 only: forward-mode tangents and tracing are refused); the *_backward functions
 are their gradients as plain calls. Rows may be strided
 (the elements of a row contiguous); anything else is made contiguous first.
@@ -264,6 +268,115 @@ def matvec(x, prepared, swiglu_limit=None, out=None):
     return _calls.matvec(x, prepared._weights, swiglu_limit, out)
 
 
+# -------------------------------------------------------------------- routing
+
+def route_tokens_backward(d_topk_w, logits, topk_idx, *, score="softmax", renormalize=True, scale=1.0,
+                          d_mean_scores=None):
+    """Gradient of route_tokens: d_logits [T, E] of the logits' type, for the
+    choice topk_idx. Slots with an id outside [0, E) count for nothing."""
+    return _calls.route_tokens_backward(d_topk_w, logits, topk_idx, score, renormalize, scale, d_mean_scores)
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, score, bias, num_groups, top_groups, group_score, renormalize, scale, mean_scores):
+        ctx.args = dict(score=score, renormalize=renormalize, scale=scale)
+        idx, w, mean = _calls.route_tokens(logits, k, score, bias, num_groups, top_groups, group_score, renormalize,
+                                           scale, mean_scores)
+        ctx.save_for_backward(logits, idx)
+        ctx.mark_non_differentiable(idx)
+        ctx.set_materialize_grads(False)
+        return (idx, w, mean) if mean_scores else (idx, w)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, d_w, d_mean=None):
+        logits, idx = ctx.saved_tensors
+        if d_w is None and d_mean is None:
+            return (None,) * 10
+        if d_w is None:
+            d_w = torch.zeros(idx.shape, dtype=torch.float32, device=idx.device)
+        return (route_tokens_backward(d_w, logits, idx, d_mean_scores=d_mean, **ctx.args),) + (None,) * 9
+
+
+def route_tokens(logits, k, *, score="softmax", bias=None, num_groups=1, top_groups=1, group_score="top2",
+                 renormalize=True, scale=1.0, mean_scores=False):
+    """The k experts of each token and their weights: (topk_idx int32 [T, k],
+    topk_w float32 [T, k]), best first, what experts_forward and sort_tokens take.
+    logits [T, E]; score: "softmax" over a token's experts, or "sigmoid" of each.
+    bias, float32 [E], is added to the scores for the choice only (a balance bias;
+    it has no gradient). With num_groups > 1 the choice is among the experts of the
+    top_groups groups of E / num_groups neighbours whose two best ("top2") or best
+    ("max") biased scores are largest. topk_w: the scores of the chosen, divided by
+    their sum with renormalize, times scale. Ties go to the lowest index; an expert
+    with a logit of -inf is never chosen, and slots left over get -1 and weight 0.
+    mean_scores=True returns also the mean over the tokens of the scores divided by
+    their sum, float32 [E]: with the plan's counts, the terms of a balance loss.
+    topk_w and the mean scores are differentiable with respect to the logits."""
+    args = (int(k), score, bias, int(num_groups), int(top_groups), group_score, bool(renormalize), float(scale),
+            bool(mean_scores))
+    if _tracked(logits):
+        return _Route.apply(logits, *args)
+    idx, w, mean = _calls.route_tokens(logits, *args)
+    return (idx, w, mean) if mean_scores else (idx, w)
+
+
+# --------------------------------------------------------------- the FP4 format
+
+def quantize_fp4(x):
+    """(codes uint8 [..., C/2], scale uint8 [..., C/32]) of x [..., C], C a multiple
+    of 32: the FP4 format that prepare_weights, prepare_matvec and
+    prepare_matmul_fp4 take. A block of 32 gets the scale 2^n, n the smallest with
+    amax <= 6 * 2^n, and its elements round to the nearest e2m1 value, ties to even.
+    A block with a NaN or an infinity reads as NaN. It has no gradient: an x that
+    requires one is refused while gradients are recorded."""
+    return _calls.quantize_fp4(x)
+
+
+def dequantize_fp4(codes, scale, dtype=torch.bfloat16):
+    """The values [..., C] that codes and scale of quantize_fp4 stand for, in dtype."""
+    return _calls.dequantize_fp4(codes, scale, dtype)
+
+
+class PreparedMatmulFp4:
+    """Kernel-layout FP4 weights made once by moe_matmul_fp4_prepare."""
+
+    def __init__(self, N, K, swiglu, weights):
+        self.N, self.K, self.swiglu = N, K, swiglu
+        self.out_features = N // 2 if swiglu else N
+        self._weights = weights
+
+    prepared = property(lambda self: self._weights.prepared)
+
+    def workspace_bytes(self, T):
+        """Bytes of workspace for calls of up to T tokens."""
+        return _calls.matmul_fp4_workspace_bytes(self._weights, T)
+
+
+def prepare_matmul_fp4(weights, swiglu=False):
+    """Lay out one matrix [N, K] of FP4 weights for matmul_fp4. weights:
+    dict(fmt="fp4", N, K, w, w_scale) as prepare_matvec takes them (codes u8
+    [N, K/2], UE8M0 u8 [N, K/32]: what quantize_fp4 returns for the matrix).
+    swiglu: rows [0, N/2) are gate, [N/2, N) up, and matmul_fp4 returns
+    silu(gate) * up."""
+    fmt, N, K = weights["fmt"], weights["N"], weights["K"]
+    if fmt != "fp4":
+        raise ValueError(f"fmt must be 'fp4', got {fmt!r}")
+    made = _calls.prepare_matmul_fp4(N, K, bool(swiglu), weights["w"], weights["w_scale"])
+    return PreparedMatmulFp4(N, K, bool(swiglu), made)
+
+
+def matmul_fp4(x, prepared, swiglu_limit=None, workspace=None, out=None):
+    """x [T, K] bf16 or fp16, quantized as quantize_fp4 does, times the prepared
+    weights: [T, N] ([T, N/2] with SwiGLU) of x's type, on the FP4 tensor cores.
+    matvec takes the same weights with the activations as they are, for few tokens.
+    workspace: uint8, at least prepared.workspace_bytes(T), 256-byte aligned
+    (allocated if None); device_status(workspace) reads its flags. It has no
+    gradient: an x that requires one is refused while gradients are recorded."""
+    return _calls.matmul_fp4(x, prepared._weights, swiglu_limit, workspace, out)
+
+
 __all__ = ["SortPlan", "sort_tokens", "permute_tokens", "permute_tokens_backward", "unpermute_tokens",
            "unpermute_tokens_backward", "norm_before", "norm_before_backward", "norm_after", "norm_after_backward",
-           "PreparedMatvec", "prepare_matvec", "matvec"]
+           "PreparedMatvec", "prepare_matvec", "matvec", "route_tokens", "route_tokens_backward", "quantize_fp4",
+           "dequantize_fp4", "PreparedMatmulFp4", "prepare_matmul_fp4", "matmul_fp4"]

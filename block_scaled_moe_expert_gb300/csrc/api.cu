@@ -14,6 +14,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "block/block_internal.cuh"
 #include "device_check.h"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
@@ -66,6 +67,14 @@ bool make_tmap(CUtensorMap* m, bool fp4, const void* base, uint64_t k_elems, uin
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+bool byte_tmap(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+  return make_tmap(m, false, base, row_bytes, rows, box_rows);
+}
+
+namespace {
 
 // Self-test of the bounded-wait paths: thread 0 waits, through the helper
 // the GEMM pipeline uses, on an mbarrier phase that nothing completes; thread

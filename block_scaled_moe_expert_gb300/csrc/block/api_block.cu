@@ -1,5 +1,5 @@
 // C entry points of the operators around the experts forward
-// (include/moe_block.h): argument checks and launches on the caller's stream.
+// (include/moe_block.h, include/moe_route_fp4.h): argument checks and launches on the caller's stream.
 // No allocation, no host synchronization. Checks come in the order of the
 // experts forward's: arguments and shapes, null pointers, alignment, sizes,
 // device, memory of every pointer.
@@ -67,6 +67,15 @@ bool gate_ok(int kind, int act, const void* gate, int T) {
   if (kind < MOE_GATE_NONE || kind > MOE_GATE_ELEMENT || act < MOE_GATE_LINEAR || act > MOE_GATE_TANH) return false;
   return (T == 0 && kind != MOE_GATE_CHANNEL) || (kind == MOE_GATE_NONE) == (gate == nullptr);
 }
+
+bool route_shape_ok(int T, int E, int K) {
+  return T >= 0 && E >= 1 && E <= kMaxExperts && K >= 1 && K <= kMaxTopK && K <= E &&
+         static_cast<int64_t>(T) * K <= (1 << 26);
+}
+bool score_ok(int score) { return score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID; }
+
+constexpr int kMaxFp4Width = 1 << 20, kMaxMatmulTokens = 1 << 20;
+bool fp4_shape_ok(int R, int C) { return R >= 0 && C >= 32 && C <= kMaxFp4Width && C % 32 == 0; }
 
 bool norm_shape_ok(int T, int H) { return T >= 0 && H >= 1 && H <= kMaxNormWidth; }
 
@@ -306,6 +315,130 @@ moe_status moe_matvec(int qfmt, int N, int K, int group, int swiglu, float swigl
   if (s != MOE_OK) return s;
   return launched(launch_matvec(shape, swiglu_limit, scale_dtype, prepared, dtype, x, ld_x, T, y, d.sms,
                                 static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_route_workspace_bytes(int E) {
+  return E >= 1 && E <= kMaxExperts ? sizeof(float) * kRouteParts * E : 0;
+}
+
+moe_status moe_route_tokens(int dtype, const void* logits, int64_t ld_logits, const float* bias, int T, int E, int K,
+                            int score, int num_groups, int top_groups, int group_score, int renormalize, float scale,
+                            int32_t* topk_idx, float* topk_w, float* mean_scores, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype) || ld_logits < 0 || !score_ok(score) ||
+      (group_score != MOE_GROUP_TOP2 && group_score != MOE_GROUP_MAX))
+    return MOE_ERR_INVALID_ARG;
+  if (!route_shape_ok(T, E, K) || num_groups < 1 || num_groups > 32 || E % num_groups || top_groups < 1 ||
+      top_groups > num_groups || K > top_groups * (E / num_groups))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  const bool any = T > 0, mean = mean_scores != nullptr;
+  if (!any && !mean) return MOE_OK;
+  if (any && (logits == nullptr || topk_idx == nullptr || topk_w == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (mean && workspace == nullptr) return MOE_ERR_INVALID_ARG;
+  if (mean && workspace_bytes < moe_route_workspace_bytes(E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  DevInfo d;
+  auto row = [&](const void* p, size_t align) { return Ptr{any ? p : nullptr, align}; };
+  const moe_status s = check_ptrs({row(logits, esize(dtype)), row(bias, 4), row(topk_idx, 4), row(topk_w, 4),
+                                   {mean_scores, 4}, {mean ? workspace : nullptr, 256}}, &d);
+  if (s != MOE_OK) return s;
+  const RouteArgs a = {logits, ld_logits, bias, T, E, K, num_groups, top_groups, group_score == MOE_GROUP_MAX,
+                       score == MOE_SCORE_SIGMOID, renormalize ? 1 : 0, scale, topk_idx, topk_w, mean_scores,
+                       static_cast<float*>(workspace)};
+  return launched(launch_route_tokens(dtype, a, d.sms, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_route_tokens_backward(int dtype, const float* d_topk_w, const float* d_mean_scores, const void* logits,
+                                     int64_t ld_logits, const int32_t* topk_idx, int T, int E, int K, int score,
+                                     int renormalize, float scale, void* d_logits, void* stream) {
+  if (!dtype_ok(dtype) || ld_logits < 0 || !score_ok(score)) return MOE_ERR_INVALID_ARG;
+  if (!route_shape_ok(T, E, K)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (d_topk_w == nullptr || logits == nullptr || topk_idx == nullptr || d_logits == nullptr) return MOE_ERR_INVALID_ARG;
+  DevInfo d;
+  const size_t es = esize(dtype);
+  const moe_status s = check_ptrs({{d_topk_w, 4}, {d_mean_scores, 4}, {logits, es}, {topk_idx, 4}, {d_logits, es}}, &d);
+  if (s != MOE_OK) return s;
+  RouteArgs a = {};
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.T = T;
+  a.E = E;
+  a.K = K;
+  a.G = 1;
+  a.sigmoid = score == MOE_SCORE_SIGMOID;
+  a.renorm = renormalize ? 1 : 0;
+  a.scale = scale;
+  a.idx = const_cast<int32_t*>(topk_idx);
+  return launched(launch_route_tokens_backward(dtype, a, d_topk_w, d_mean_scores, d_logits, d.sms,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_quantize_fp4(int dtype, const void* x, int64_t ld_x, int R, int C, void* codes, void* scale,
+                            void* stream) {
+  if (!dtype_ok(dtype) || ld_x < 0) return MOE_ERR_INVALID_ARG;
+  if (!fp4_shape_ok(R, C)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (R == 0) return MOE_OK;
+  if (x == nullptr || codes == nullptr || scale == nullptr) return MOE_ERR_INVALID_ARG;
+  DevInfo d;
+  const moe_status s = check_ptrs({{x, esize(dtype)}, {codes, 16}, {scale, 1}}, &d);
+  if (s != MOE_OK) return s;
+  return launched(launch_quantize_fp4(dtype, x, ld_x, R, C, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scale),
+                                      d.sms, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dequantize_fp4(int dtype, const void* codes, const void* scale, int R, int C, void* out, void* stream) {
+  if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  if (!fp4_shape_ok(R, C)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (R == 0) return MOE_OK;
+  if (codes == nullptr || scale == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+  DevInfo d;
+  const moe_status s = check_ptrs({{codes, 1}, {scale, 1}, {out, esize(dtype)}}, &d);
+  if (s != MOE_OK) return s;
+  return launched(launch_dequantize_fp4(dtype, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scale),
+                                        static_cast<int64_t>(R) * (C / 32), out, d.sms,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_matmul_fp4_prepared_bytes(int N, int K, int swiglu) {
+  return matmul_layout({N, K, swiglu ? 1 : 0}).total;
+}
+
+moe_status moe_matmul_fp4_prepare(int N, int K, int swiglu, const void* codes, const void* scale, void* prepared,
+                                  size_t prepared_bytes, void* stream) {
+  const MatmulShape shape = {N, K, swiglu ? 1 : 0};
+  const size_t need = matmul_layout(shape).total;
+  if (need == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (codes == nullptr || scale == nullptr || prepared == nullptr) return MOE_ERR_INVALID_ARG;
+  if (prepared_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  DevInfo d;
+  const moe_status s = check_ptrs({{codes, 1}, {scale, 1}, {prepared, 256}}, &d);
+  if (s != MOE_OK) return s;
+  return launched(launch_matmul_prepare(shape, codes, scale, prepared, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_matmul_fp4_workspace_bytes(int T_max, int K) {
+  if (T_max < 0 || T_max > kMaxMatmulTokens || matmul_layout({1, K, 0}).total == 0) return 0;
+  return matmul_workspace(T_max, K).total;
+}
+
+moe_status moe_matmul_fp4(int N, int K, int swiglu, float swiglu_limit, const void* prepared, int dtype, const void* x,
+                          int64_t ld_x, int T, void* workspace, size_t workspace_bytes, void* y, void* stream) {
+  const MatmulShape shape = {N, K, swiglu ? 1 : 0};
+  if (T < 0 || ld_x < 0 || (dtype != MOE_BF16 && dtype != MOE_FP16)) return MOE_ERR_INVALID_ARG;
+  if (matmul_layout(shape).total == 0 || T > kMaxMatmulTokens) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (prepared == nullptr || x == nullptr || y == nullptr || workspace == nullptr) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < matmul_workspace(T, K).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  DevInfo d;
+  const moe_status s = check_ptrs({{prepared, 256}, {x, 2}, {workspace, 256}, {y, 2}}, &d);
+  if (s != MOE_OK) return s;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const MatmulWorkspace w = matmul_workspace(T, K);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_quantize_act(dtype, x, ld_x, T, K, ws + w.codes, reinterpret_cast<uint32_t*>(ws + w.sf),
+                                            reinterpret_cast<uint32_t*>(ws), d.sms, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  return launched(launch_matmul_fp4(shape, swiglu_limit, prepared, dtype, T, y, ws, d.sms, st));
 }
 
 }  // extern "C"

@@ -3,7 +3,7 @@
 #pragma once
 #include "../device_check.h"
 #include "../moe_internal.cuh"
-#include "moe_block.h"
+#include "moe_route_fp4.h"
 #include "vec_io.cuh"
 
 namespace bsmoe {
@@ -91,5 +91,52 @@ cudaError_t launch_matvec_prepare(const MatvecShape& s, const void* codes, const
                                   const void* zero, void* prepared, cudaStream_t st);
 cudaError_t launch_matvec(const MatvecShape& s, float limit, int scale_dtype, const void* prepared, int dtype,
                           const void* x, int64_t ld_x, int T, void* y, int num_sms, cudaStream_t st);
+
+// Routing: the choice of experts and its gradient.
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;
+  const float* bias;  // null: none
+  int T, E, K, G, top_groups, group_max, sigmoid, renorm;
+  float scale;
+  int32_t* idx;
+  float *w, *mean;  // mean null: not asked for
+  float* partials;  // [kRouteParts][E] with mean
+};
+constexpr int kRouteParts = 608;  // the mean's column sums are taken over at most this many blocks
+cudaError_t launch_route_tokens(int dtype, const RouteArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_route_tokens_backward(int dtype, const RouteArgs& a, const float* dw, const float* dmean, void* dx,
+                                         int num_sms, cudaStream_t st);
+
+// The FP4 format: rows of C elements, C a multiple of 32; codes 8-byte aligned when written.
+cudaError_t launch_quantize_fp4(int dtype, const void* x, int64_t ld, int R, int C, uint8_t* codes, uint8_t* scale,
+                                int num_sms, cudaStream_t st);
+cudaError_t launch_dequantize_fp4(int dtype, const uint8_t* codes, const uint8_t* scale, int64_t blocks, void* out,
+                                  int num_sms, cudaStream_t st);
+
+// Tensor map of rows of `row_bytes` bytes (a multiple of 16), boxes of 128 bytes x
+// box_rows rows in the 128-byte swizzle; false if it cannot be made (api.cu).
+bool byte_tmap(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+
+// FP4 x FP4 products.
+struct MatmulShape {
+  int N, K, swiglu;
+};
+struct MatmulLayout {  // prepared weights: codes, then scale words
+  int KB, NT;          // 128-K blocks, 256-row tiles
+  size_t codes_bytes, total;  // total 0: unsupported
+};
+MatmulLayout matmul_layout(const MatmulShape& s);
+struct MatmulWorkspace {  // status word, then the quantized activations
+  size_t sf, codes, total;
+};
+MatmulWorkspace matmul_workspace(int T, int K);
+cudaError_t launch_matmul_prepare(const MatmulShape& s, const void* codes, const void* scale, void* prepared,
+                                  cudaStream_t st);
+// Activations [T][K] to codes [T][Kp / 2] and scale words; clears the status word.
+cudaError_t launch_quantize_act(int dtype, const void* x, int64_t ld, int T, int K, uint8_t* codes, uint32_t* sf,
+                                uint32_t* status, int num_sms, cudaStream_t st);
+cudaError_t launch_matmul_fp4(const MatmulShape& s, float limit, const void* prepared, int dtype, int T, void* y,
+                              uint8_t* workspace, int num_sms, cudaStream_t st);
 
 }  // namespace bsmoe

@@ -1,4 +1,5 @@
-// Python's way into the C entry points of include/moe_block.h.
+// Python's way into the C entry points of include/moe_block.h and
+// include/moe_route_fp4.h.
 //
 // The calls are short at decode (a kernel of a few microseconds), so their
 // arguments are checked and their outputs allocated here rather than in
@@ -17,7 +18,7 @@
 #include <optional>
 #include <tuple>
 
-#include "moe_block.h"
+#include "moe_route_fp4.h"
 
 namespace py = pybind11;
 using at::Tensor;
@@ -41,7 +42,16 @@ namespace {
   X(moe_norm_after_backward)                                                                                    \
   X(moe_matvec_prepared_bytes)                                                                                  \
   X(moe_matvec_prepare)                                                                                         \
-  X(moe_matvec)
+  X(moe_matvec)                                                                                                 \
+  X(moe_route_workspace_bytes)                                                                                  \
+  X(moe_route_tokens)                                                                                           \
+  X(moe_route_tokens_backward)                                                                                  \
+  X(moe_quantize_fp4)                                                                                           \
+  X(moe_dequantize_fp4)                                                                                         \
+  X(moe_matmul_fp4_prepared_bytes)                                                                              \
+  X(moe_matmul_fp4_prepare)                                                                                     \
+  X(moe_matmul_fp4_workspace_bytes)                                                                             \
+  X(moe_matmul_fp4)
 
 struct Api {
 #define X(name) decltype(&::name) name = nullptr;
@@ -431,6 +441,179 @@ Tensor matvec(const Tensor& x, const MatvecWeights& m, std::optional<double> lim
   return y;
 }
 
+// ----------------------------------------------------------------- routing
+
+int score_code(const std::string& score) {
+  const int c = score == "softmax" ? MOE_SCORE_SOFTMAX : score == "sigmoid" ? MOE_SCORE_SIGMOID : -1;
+  TORCH_CHECK_VALUE(c >= 0, "score must be 'softmax' or 'sigmoid', got '", score, "'");
+  return c;
+}
+
+Tensor f32_vector(const Maybe& t, const First& f, const char* what) {
+  if (!t) return Tensor();
+  TORCH_CHECK_VALUE(t->scalar_type() == at::kFloat && t->dim() == 1 && t->size(0) == f.H, what,
+                    " must be a float32 tensor of shape (", f.H, ",)");
+  operand(*t, f.dev);
+  return t->contiguous();
+}
+
+// (topk_idx, topk_w, mean_scores or None)
+py::tuple route_tokens(const Tensor& logits, int k, const std::string& score, const Maybe& bias, int num_groups,
+                       int top_groups, const std::string& group_score, bool renormalize, double scale, bool mean) {
+  const First f = first(logits, "logits");
+  const int by = score_code(score);
+  TORCH_CHECK_VALUE(group_score == "top2" || group_score == "max", "group_score must be 'top2' or 'max', got '",
+                    group_score, "'");
+  const Tensor b = f32_vector(bias, f, "bias");
+  // sizes are checked by the call below, before any use of these
+  const int64_t cols = k > 0 && k <= 32 ? k : 1;
+  const Tensor idx = at::empty({f.n, cols}, f.t.options().dtype(at::kInt));
+  const Tensor w = at::empty({f.n, cols}, f.t.options().dtype(at::kFloat));
+  Tensor m, ws;
+  size_t bytes = 0;
+  if (mean) {
+    m = at::empty({f.H}, w.options());
+    bytes = api.moe_route_workspace_bytes(static_cast<int>(f.H));
+    ws = at::empty({static_cast<int64_t>(bytes)}, f.t.options().dtype(at::kByte));
+  }
+  check(api.moe_route_tokens(f.code, f.ptr(), f.ld, static_cast<const float*>(ptr(b)), static_cast<int>(f.n),
+                             static_cast<int>(f.H), k, by, num_groups, top_groups,
+                             group_score == "top2" ? MOE_GROUP_TOP2 : MOE_GROUP_MAX, renormalize,
+                             static_cast<float>(scale), static_cast<int32_t*>(idx.data_ptr()),
+                             static_cast<float*>(w.data_ptr()), static_cast<float*>(out_ptr(m)), out_ptr(ws), bytes,
+                             stream(f.dev)),
+        "moe_route_tokens");
+  return py::make_tuple(idx, w, or_none(m));
+}
+
+Tensor route_tokens_backward(const Tensor& d_w, const Tensor& logits, const Tensor& topk_idx, const std::string& score,
+                             bool renormalize, double scale, const Maybe& d_mean) {
+  const First f = first(logits, "logits");
+  const int by = score_code(score);
+  TORCH_CHECK_VALUE(topk_idx.scalar_type() == at::kInt && topk_idx.dim() == 2 && topk_idx.size(0) == f.n,
+                    "topk_idx must be an int32 tensor [", f.n, ", K]");
+  TORCH_CHECK_VALUE(d_w.scalar_type() == at::kFloat && d_w.sizes() == topk_idx.sizes(),
+                    "d_topk_w must be a float32 tensor of topk_idx's shape");
+  TORCH_CHECK_VALUE(topk_idx.size(1) <= INT32_MAX, "topk_idx is too large: ", topk_idx.sizes());
+  operand(topk_idx, f.dev);
+  operand(d_w, f.dev);
+  const Tensor idx = topk_idx.contiguous(), dw = d_w.contiguous(), dm = f32_vector(d_mean, f, "d_mean_scores");
+  const Tensor dx = at::empty({f.n, f.H}, f.t.options());
+  check(api.moe_route_tokens_backward(f.code, static_cast<const float*>(ptr(dw)), static_cast<const float*>(ptr(dm)),
+                                      f.ptr(), f.ld, static_cast<const int32_t*>(ptr(idx)), static_cast<int>(f.n),
+                                      static_cast<int>(f.H), static_cast<int>(idx.size(1)), by, renormalize,
+                                      static_cast<float>(scale), dx.data_ptr(), stream(f.dev)),
+        "moe_route_tokens_backward");
+  return dx;
+}
+
+// ----------------------------------------------------------- the FP4 format
+
+void no_gradient(const Tensor& x, const char* what) {
+  TORCH_CHECK_VALUE(!x.requires_grad() || !c10::GradMode::is_enabled(), what,
+                    " has no gradient: call it without gradients (torch.no_grad) or on x.detach()");
+}
+
+// (codes, scale) of x [..., C]
+std::tuple<Tensor, Tensor> quantize_fp4(const Tensor& x) {
+  const at::IntArrayRef sizes = x.sizes();
+  TORCH_CHECK_VALUE(x.dim() >= 1, "x must have at least one dimension");
+  no_gradient(x, "quantize_fp4");
+  const int64_t C = sizes.back();
+  // rows: every dimension but the last
+  const First f = first(x.dim() == 2 ? x : x.contiguous().view({C == 0 ? 0 : x.numel() / C, C}), "x");
+  TORCH_CHECK_VALUE(C > 0 && C % 32 == 0, "the last dimension must be a multiple of 32, got ", C);
+  std::vector<int64_t> cs(sizes.begin(), sizes.end()), ss = cs;
+  cs.back() = C / 2;
+  ss.back() = C / 32;
+  const auto u8 = f.t.options().dtype(at::kByte);
+  const Tensor codes = at::empty(cs, u8), scale = at::empty(ss, u8);
+  check(api.moe_quantize_fp4(f.code, f.ptr(), f.ld, static_cast<int>(f.n), static_cast<int>(C), codes.data_ptr(),
+                             scale.data_ptr(), stream(f.dev)),
+        "moe_quantize_fp4");
+  return {codes, scale};
+}
+
+Tensor dequantize_fp4(const Tensor& codes, const Tensor& scale, at::ScalarType dtype) {
+  const int code = dtype_code(dtype);
+  TORCH_CHECK_VALUE(code >= 0, "dtype must be bfloat16, float16 or float32, got ", dtype);
+  TORCH_CHECK_VALUE(codes.scalar_type() == at::kByte && codes.dim() >= 1 && codes.size(-1) % 16 == 0 && codes.size(-1) > 0,
+                    "codes must be uint8 [..., C / 2], C a multiple of 32");
+  std::vector<int64_t> sizes = codes.sizes().vec();
+  const int64_t C = 2 * sizes.back();
+  sizes.back() = C / 32;
+  TORCH_CHECK_VALUE(scale.scalar_type() == at::kByte && scale.sizes() == at::IntArrayRef(sizes),
+                    "scale must be uint8 of shape ", at::IntArrayRef(sizes), ", got ", scale.sizes());
+  const int dev = codes.is_cuda() ? c10::cuda::current_device() : -1;
+  operand(codes, dev);
+  operand(scale, dev);
+  const Tensor c = codes.contiguous(), s = scale.contiguous();
+  sizes.back() = C;
+  const Tensor out = at::empty(sizes, c.options().dtype(dtype));
+  const int64_t rows = c.numel() / (C / 2);
+  TORCH_CHECK_VALUE(rows <= INT32_MAX && C <= INT32_MAX, "codes is too large: ", codes.sizes());
+  check(api.moe_dequantize_fp4(code, ptr(c), ptr(s), static_cast<int>(rows), static_cast<int>(C), out.data_ptr(),
+                               stream(dev)),
+        "moe_dequantize_fp4");
+  return out;
+}
+
+struct MatmulWeights {
+  int N, K;
+  bool swiglu;
+  Tensor prepared;
+};
+
+MatmulWeights prepare_matmul_fp4(int N, int K, bool swiglu, const Tensor& w, const Tensor& scale) {
+  const size_t bytes = api.moe_matmul_fp4_prepared_bytes(N, K, swiglu);
+  if (bytes == 0) check(MOE_ERR_UNSUPPORTED_SHAPE, "moe_matmul_fp4_prepared_bytes");
+  auto shaped = [&](const Tensor& t, int64_t cols) {
+    return t.scalar_type() == at::kByte && t.dim() == 2 && t.size(0) == N && t.size(1) == cols;
+  };
+  TORCH_CHECK_VALUE(shaped(w, K / 2), "w must be uint8 [", N, ", ", K / 2, "]");
+  TORCH_CHECK_VALUE(shaped(scale, K / 32), "w_scale must be uint8 [", N, ", ", K / 32, "]");
+  const int dev = w.is_cuda() ? c10::cuda::current_device() : -1;
+  operand(w, dev);
+  operand(scale, dev);
+  const Tensor wc = w.contiguous(), sc = scale.contiguous();
+  MatmulWeights m{N, K, swiglu, at::empty({static_cast<int64_t>(bytes)}, w.options())};
+  check(api.moe_matmul_fp4_prepare(N, K, swiglu, ptr(wc), ptr(sc), m.prepared.data_ptr(), bytes, stream(dev)),
+        "moe_matmul_fp4_prepare");
+  return m;
+}
+
+int64_t matmul_fp4_workspace_bytes(const MatmulWeights& m, int64_t T) {
+  const size_t bytes = T < 0 || T > INT32_MAX ? 0 : api.moe_matmul_fp4_workspace_bytes(static_cast<int>(T), m.K);
+  if (bytes == 0) check(MOE_ERR_UNSUPPORTED_SHAPE, "moe_matmul_fp4_workspace_bytes");
+  return static_cast<int64_t>(bytes);
+}
+
+Tensor matmul_fp4(const Tensor& x, const MatmulWeights& m, std::optional<double> limit, const Maybe& workspace,
+                  const Maybe& out) {
+  const First f = first(x, "x");
+  TORCH_CHECK_VALUE(f.code != MOE_FP32, "matmul_fp4 takes bfloat16 or float16 x, got ", f.type);
+  TORCH_CHECK_VALUE(f.H == m.K, "x has ", f.H, " columns, the prepared weights ", m.K);
+  no_gradient(x, "matmul_fp4");
+  TORCH_CHECK_VALUE(!limit || m.swiglu, "swiglu_limit is for weights prepared with swiglu=True");
+  operand(m.prepared, f.dev);
+  const int64_t need = matmul_fp4_workspace_bytes(m, f.n);
+  Tensor ws;
+  if (workspace) {
+    TORCH_CHECK_VALUE(workspace->scalar_type() == at::kByte && workspace->is_contiguous(),
+                      "workspace must be a contiguous uint8 tensor");
+    operand(*workspace, f.dev);
+    ws = *workspace;
+  } else {
+    ws = at::empty({need}, f.t.options().dtype(at::kByte));
+  }
+  const Tensor y = output(out, f, f.n, m.swiglu ? m.N / 2 : m.N);
+  check(api.moe_matmul_fp4(m.N, m.K, m.swiglu, limit ? static_cast<float>(*limit) : -1.f, m.prepared.const_data_ptr(),
+                           f.code, f.ptr(), f.ld, static_cast<int>(f.n), ws.data_ptr(),
+                           static_cast<size_t>(ws.numel()), y.data_ptr(), stream(f.dev)),
+        "moe_matmul_fp4");
+  return y;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
@@ -460,4 +643,12 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   py::class_<MatvecWeights>(m, "MatvecWeights").def_readonly("prepared", &MatvecWeights::prepared);
   m.def("prepare_matvec", wrap_pybind_function(prepare_matvec));
   m.def("matvec", wrap_pybind_function(matvec));
+  m.def("route_tokens", wrap_pybind_function(route_tokens));
+  m.def("route_tokens_backward", wrap_pybind_function(route_tokens_backward));
+  m.def("quantize_fp4", wrap_pybind_function(quantize_fp4));
+  m.def("dequantize_fp4", wrap_pybind_function(dequantize_fp4));
+  py::class_<MatmulWeights>(m, "MatmulWeights").def_readonly("prepared", &MatmulWeights::prepared);
+  m.def("prepare_matmul_fp4", wrap_pybind_function(prepare_matmul_fp4));
+  m.def("matmul_fp4_workspace_bytes", wrap_pybind_function(matmul_fp4_workspace_bytes));
+  m.def("matmul_fp4", wrap_pybind_function(matmul_fp4));
 }

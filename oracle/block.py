@@ -171,3 +171,107 @@ def swiglu(y, limit=None):
     if limit is not None:
         gate, up = gate.clamp(max=limit), up.clamp(-limit, limit)
     return gate * torch.sigmoid(gate) * up
+
+
+# -------------------------------------------------------------------- routing
+
+def scores(logits, score):
+    """(scores, scores over their sum): 0 for a logit of -inf and for a token of nothing else."""
+    x = logits.double()
+    most = x.max(dim=1, keepdim=True)[0]
+    e = torch.where(x == -math.inf, torch.zeros_like(x), torch.exp(x - most))
+    total = e.sum(1, keepdim=True)
+    soft = torch.where(total == 0, torch.zeros_like(e), e / total)
+    if score == "softmax":
+        return soft, soft
+    # the sum in units of e^most where every score is smaller than 64 bits hold
+    s = 1 / (1 + torch.exp(-x))
+    total = s.sum(1, keepdim=True)
+    return s, torch.where(total < 1e-280, soft, s / total)
+
+
+def choose(logits, K, score, bias=None, groups=1, top_groups=1, group_score="top2"):
+    """int64 [T, K], expert by expert: -1 where no available expert is left."""
+    x = logits.double()
+    T, E = x.shape
+    q = scores(logits, score)[0]
+    q = q if bias is None else q + bias.double()
+    key = x + 0.0 if bias is None else q
+    ok = (x > -math.inf) & (q > -math.inf)
+    q, key = (torch.where(ok, v, torch.full_like(v, -math.inf)) for v in (q, key))
+    if groups > 1:
+        two = q.view(T, groups, -1).sort(dim=2, descending=True)[0][:, :, :2]
+        value = two[:, :, 0]
+        if group_score == "top2" and two.shape[2] == 2:
+            value = torch.where(two[:, :, 1] > -math.inf, two.sum(2), value)
+        best = value.sort(dim=1, descending=True, stable=True)[1][:, :top_groups]
+        keep = torch.zeros(T, groups, dtype=torch.bool, device=x.device).scatter_(1, best, True)
+        key = torch.where(keep.repeat_interleave(E // groups, dim=1), key, torch.full_like(key, -math.inf))
+    top, idx = key.sort(dim=1, descending=True, stable=True)
+    return torch.where(top[:, :K] > -math.inf, idx[:, :K], -1)
+
+
+def route_weights(logits, idx, score, renorm, scale):
+    """float64 [T, K] of the chosen experts, 0 at -1."""
+    have = idx >= 0
+    x = torch.where(have, logits.double().gather(1, idx.clamp(min=0)), -math.inf)
+    s = torch.where(have, scores(logits, score)[0].gather(1, idx.clamp(min=0)), 0.0)
+    if renorm:
+        if score == "softmax":
+            s = scores(x, "softmax")[0]
+        else:
+            s = scores(x, "sigmoid")[1]
+        s = torch.where(have, s, 0.0)
+    s = s * scale
+    return torch.where(logits.isnan().any(1, keepdim=True), float("nan"), s)
+
+
+def route_backward(d_w, logits, idx, score, renorm, scale, d_mean=None, mag=False):
+    """float64 [T, E]. Through one-hot rows: the same expert twice adds up."""
+    T, E = logits.shape
+    have = (idx >= 0) & (idx < E)
+    hot = torch.nn.functional.one_hot(torch.where(have, idx, 0).long(), E).double() * have[:, :, None]
+    v = scale * d_w.double() * have
+    s, p = scores(logits, score)
+    x = torch.where(have, logits.double().gather(1, torch.where(have, idx, 0).long()), -math.inf)
+    wn = torch.where(have, scores(x, score)[1], 0.0)
+    slope = 1.0 if score == "softmax" else 1 / (1 + torch.exp(logits.double()))  # 1 - s
+    if mag:
+        v, minus = v.abs(), -1.0
+    else:
+        minus = 1.0
+    if renorm:
+        inner = (v * wn).sum(1, keepdim=True)
+        dx = torch.einsum("tk,tke->te", wn * (v - minus * inner), hot) * slope
+    else:
+        ds = torch.einsum("tk,tke->te", v, hot)
+        dx = s * ds * slope if score == "sigmoid" else s * (ds - minus * (ds * s).sum(1, keepdim=True))
+    if d_mean is not None:
+        h = d_mean.double() / T
+        h = h.abs() if mag else h
+        dx = dx + p * (h - minus * (h * p).sum(1, keepdim=True)) * slope
+    return dx
+
+
+# --------------------------------------------------------------- the FP4 format
+
+def quantize_fp4(x):
+    """(code int64 [R, C], exponent int64 [R, C / 32]) from the definition; blocks without NaN or infinity."""
+    R, C = x.shape
+    b = x.double().view(R, C // 32, 32)
+    amax = b.abs().amax(2, keepdim=True)
+    n = torch.full_like(amax, -127)
+    for k in range(-126, 128):
+        n = torch.where(amax > 6 * 2.0 ** (k - 1), float(k), n)
+    n = torch.where(amax == 0, 0.0, n)
+    a = b.abs() * torch.exp2(-n)
+    code = torch.zeros_like(a)
+    for i in range(1, 8):
+        border = (E2M1[i - 1] + E2M1[i]) / 2
+        code += (a >= border if i % 2 == 0 else a > border).double()
+    return (code.long() + 8 * torch.signbit(b).long()).view(R, C), n.long().squeeze(2)
+
+
+def fp4_values(code, exponent):
+    table = torch.tensor(E2M1, dtype=torch.float64, device=code.device)
+    return table[code] * torch.exp2(exponent.double()).repeat_interleave(32, dim=1)
