@@ -29,7 +29,8 @@ struct Shape {
   int T, E, K, dtype, G, top_groups, group_max, sigmoid, renorm;
   int64_t ld;
   float scale;
-  bool vec;  // a lane's logits are whole 16-byte (or, below that, whole power-of-two) loads
+  bool vec;       // a lane's logits are whole 16-byte (or, below that, whole power-of-two) loads
+  bool vec_bias;  // and its biases
 };
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -100,7 +101,6 @@ __device__ __forceinline__ void sigmoid_pair(float x, float* s, float* not_s) {
   *not_s = x >= 0.f ? z * d : d;
 }
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ double sigmoid_exact(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 // Scores up to a common factor, for ratios of them: below -60 sigmoid(x) is e^x in
 // fp32, so where the largest logit `most` is there, e^(x - most) keeps the ratios
@@ -113,238 +113,488 @@ __device__ __forceinline__ float ratio_score(bool sigmoid, float x, float most) 
   return s;
 }
 
-struct Chosen {
-  int idx;      // lane k: the k-th expert, -1 if none is left
-  float x;      // its logit
-  bool unsure;  // the token's: fp32 keys do not settle the choice
-};
-
 // What the lanes of a token know about all its logits.
 struct Row {
   float most;  // largest logit
-  float sum;   // sum of e^(x - most) (softmax where scores are needed)
+  float sum;   // sum of e^(x - most), where softmax scores are needed
 };
 
-// The K best of the token's experts. V: type of the keys. `slack`: largest
-// error of an fp32 key beside 2^-22 of the key itself.
-template <typename V, int P, int L>
-__device__ __forceinline__ Chosen choose(const Shape& s, const float (&x)[P], Span sp, const float* bias, Row row,
-                                         int sub, float slack) {
-  constexpr bool kExact = sizeof(V) == 8;
-  const V none = neg_inf();
-  V key[P];
-  const bool by_score = bias != nullptr || (s.G > 1 && !s.group_max);
-  V total = 1;
-  if (kExact && by_score && !s.sigmoid) {
-    V t = 0;
+// A monotone map of floats to whole numbers above 0, and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ int64_t ordered(double v) {
+  const int64_t u = __double_as_longlong(v);
+  return u ^ static_cast<int64_t>(static_cast<uint64_t>(u >> 63) >> 1);
+}
+constexpr int64_t kNone64 = INT64_MIN;  // below the image of every number
+
+template <int L>
+__device__ __forceinline__ uint32_t lane_max_u32(uint32_t v) {
+  if constexpr (L == 32) {
+    return __reduce_max_sync(kFull, v);
+  } else {
 #pragma unroll
-    for (int i = 0; i < P; ++i) t += x[i] > neg_inf() ? exp(static_cast<double>(x[i]) - static_cast<double>(row.most)) : 0.0;
-    total = lane_sum<L>(t);
-  } else if (by_score && !s.sigmoid) {
-    total = __fdividef(1.f, row.sum);
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
   }
-  // q: scores plus bias (what groups are ranked by); key: what experts are
+}
+// The lowest lane of the token for which `mine` holds.
+template <int L>
+__device__ __forceinline__ int first_lane(bool mine, int first) {
+  unsigned who = __ballot_sync(kFull, mine);
+  if (L < 32) who = (who >> first) & ((1u << (L & 31)) - 1u);
+  return first + __ffs(who) - 1;
+}
+
+// Descending sort of a lane's keys (Batcher's odd-even merge network).
+template <int P>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[P]) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    V q = x[i] + 0.f;  // -0 and 0 are one value
-    if (by_score) {
-      if constexpr (kExact) {
-        q = s.sigmoid ? sigmoid_exact(x[i]) : exp(static_cast<double>(x[i]) - static_cast<double>(row.most)) / total;
-        if (bias != nullptr && i < sp.n) q += static_cast<double>(__ldg(bias + sp.e0 + i));
-      } else {
-        q = s.sigmoid ? sigmoid_fast(x[i]) : __expf(x[i] - row.most) * static_cast<float>(total);
-        if (bias != nullptr && i < sp.n) q += __ldg(bias + sp.e0 + i);
+  for (int p = 1; p < P; p *= 2) {
+#pragma unroll
+    for (int q = p; q > 0; q /= 2) {
+#pragma unroll
+      for (int j = q % p; j + q < P; j += 2 * q) {
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          const int a = i + j, b = i + j + q;
+          if (b < P && a / (2 * p) == b / (2 * p)) {
+            const uint32_t hi = max(k[a], k[b]), lo = min(k[a], k[b]);
+            k[a] = hi;
+            k[b] = lo;
+          }
+        }
       }
     }
-    key[i] = i < sp.n && x[i] > neg_inf() && q > none ? q : none;
   }
-  bool unsure = false;
+}
+
+// fp32 scores plus bias of a lane's experts, NaN or -inf where one is not available.
+// Errors of an fp32 score: sigmoid: below 3e-7 (its slope times the exponential's
+// 2^-22 and its argument's |x| 2^-23, the sum's and the quotient's roundings);
+// softmax: those of the exponential and of the sum, in all below 1.2e-6 of the
+// largest score. `score_slack` is above both.
+__device__ __forceinline__ float score_slack(const Shape& s, Row row) {
+  return s.sigmoid ? 4e-7f : __fdividef(1.5e-6f, row.sum);
+}
+template <int P>
+__device__ __forceinline__ void add_bias(const float* bias, Span sp, bool vec, float (&q)[P]) {
+  float b[P];
+  load_as<P, float>(bias, sp.e0, sp.n, vec, b);
+#pragma unroll
+  for (int i = 0; i < P; ++i) q[i] += b[i];
+}
+
+// 64-bit scores of a few of a lane's experts (bits of `need`) into keys. All lanes call it.
+template <int P>
+__device__ __forceinline__ void exact_keys(const Shape& s, const float (&x)[P], Span sp, const float* bias, float most,
+                                           double total, unsigned need, int64_t (&key)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) key[i] = kNone64;
+  while (__any_sync(kFull, need != 0)) {
+    const int at = need != 0 ? __ffs(need) - 1 : 0;
+    float xv = x[0];
+#pragma unroll
+    for (int i = 1; i < P; ++i) xv = i == at ? x[i] : xv;
+    const double e = exp(s.sigmoid ? -static_cast<double>(xv) : static_cast<double>(xv) - static_cast<double>(most));
+    double q = s.sigmoid ? 1.0 / (1.0 + e) : e / total;
+    if (bias != nullptr && at < sp.n) q += static_cast<double>(__ldg(bias + sp.e0 + at));
+    const int64_t k = ordered(q);
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = need != 0 && i == at ? k : key[i];
+    need &= need - 1;
+  }
+}
+
+template <int L>
+__device__ __forceinline__ int64_t lane_max_i64(int64_t v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const int64_t w = __shfl_xor_sync(kFull, v, o);
+    v = v > w ? v : w;
+  }
+  return v;
+}
+
+// The choice with keys in 64 bits: the whole warp calls it where a token of it is
+// unsure. Only experts whose fp32 key is within its error of the border get one.
+// Returns the index of the sub-th choice.
+template <int P, int L>
+__device__ __noinline__ int choose_exact(Shape s, const void* logits, int64_t t, const float* bias, Row row, int sub) {
+  const int first = (threadIdx.x & 31) - sub;
+  const Span sp = span_of<P, L>(s, sub);
+  const bool by_score = bias != nullptr || (s.G > 1 && !s.group_max);
+  const float slack = score_slack(s, row);
+  float x[P], q[P];
+  load_logits<P>(s, logits, t, sp, x);
+  double total = 1;
+  if (by_score && !s.sigmoid) {
+    double sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < P; ++i) {
+      float xv = x[0];
+#pragma unroll
+      for (int j = 1; j < P; ++j) xv = j == i ? x[j] : xv;
+      sum += xv > neg_inf() ? exp(static_cast<double>(xv) - static_cast<double>(row.most)) : 0.0;
+    }
+    total = lane_sum<L>(sum);
+  }
+  const float inv = by_score && !s.sigmoid ? __fdividef(1.f, row.sum) : 1.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    q[i] = x[i] + 0.f;
+    if (by_score) q[i] = s.sigmoid ? sigmoid_fast(x[i]) : __expf(x[i] - row.most) * inv;
+  }
+  if (bias != nullptr) add_bias<P>(bias, sp, false, q);
+#pragma unroll
+  for (int i = 0; i < P; ++i) q[i] = i < sp.n && x[i] > neg_inf() && q[i] > neg_inf() ? q[i] : neg_inf();
+  int64_t key[P];
+  // the experts that may reach a border at `edge`
+  auto near = [&](float edge) {
+    const float from = fabsf(edge) < INFINITY ? edge - 4.f * slack - 0x1p-20f * fabsf(edge) : edge;
+    unsigned need = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) need |= static_cast<unsigned>(q[i] > neg_inf() && q[i] >= from) << i;
+    return need;
+  };
   if (s.G > 1) {
     const int lpg = 1 << (31 - __clz(32 / s.G));
-    V a = none, b = none;  // largest and second
+    float a = neg_inf(), b = neg_inf();
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      b = fmax(b, fmin(a, key[i]));
-      a = fmax(a, key[i]);
+      b = fmaxf(b, fminf(a, q[i]));
+      a = fmaxf(a, q[i]);
     }
     for (int o = lpg / 2; o > 0; o >>= 1) {
-      const V a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
-      b = fmax(fmin(a, a2), fmax(b, b2));
-      a = fmax(a, a2);
+      const float a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+      b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+      a = fmaxf(a, a2);
     }
-    const V value = s.group_max || b == none ? a : a + b;
+    if (by_score) {
+      exact_keys<P>(s, x, sp, bias, row.most, total, near(s.group_max ? a : b), key);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) key[i] = q[i] > neg_inf() ? ordered(static_cast<double>(q[i])) : kNone64;
+    }
+    int64_t c = kNone64, d = kNone64;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int64_t lo = key[i] < c ? key[i] : c;
+      d = d > lo ? d : lo;
+      c = c > key[i] ? c : key[i];
+    }
+    for (int o = lpg / 2; o > 0; o >>= 1) {
+      const int64_t c2 = __shfl_xor_sync(kFull, c, o), d2 = __shfl_xor_sync(kFull, d, o);
+      const int64_t lo = c < c2 ? c : c2, hi = d > d2 ? d : d2;
+      d = lo > hi ? lo : hi;
+      c = c > c2 ? c : c2;
+    }
+    auto value_of = [](int64_t o) { return __longlong_as_double(o ^ static_cast<int64_t>(static_cast<uint64_t>(o >> 63) >> 1)); };
+    const int64_t value = s.group_max || d == kNone64 ? c : ordered(value_of(c) + value_of(d));
     const int g = sub / lpg;
     int rank = 0;
     for (int j = 0; j < s.G; ++j) {
-      const V v = __shfl_sync(kFull, value, j * lpg);
+      const int64_t v = __shfl_sync(kFull, value, j * lpg);
       rank += v > value || (v == value && j < g);
     }
-    const bool in = rank < s.top_groups && g < s.G;
-    if (!kExact && by_score) {
-      const V worst = -lane_max<L>(in ? -value : none), best = lane_max<L>(in || g >= s.G ? none : value);
-      unsure = worst - best <= 4.f * slack + 0x1p-20f * (fabsf(worst) + fabsf(best));
-    }
-    if (bias == nullptr) {  // within the groups the order is that of the logits
 #pragma unroll
-      for (int i = 0; i < P; ++i) key[i] = key[i] > none ? static_cast<V>(x[i] + 0.f) : none;
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) key[i] = in ? key[i] : none;
+    for (int i = 0; i < P; ++i) q[i] = rank < s.top_groups && g < s.G ? q[i] : neg_inf();
   }
-  Chosen c = {-1, neg_inf(), unsure};
-  V mine = none, last = none;
-  int last_idx = -1;
-  float last_x = 0.f;
-  const bool check = !kExact && bias != nullptr;
-  const int rounds = s.K + (check && s.K < s.E ? 1 : 0);
-  for (int k = 0; k < rounds; ++k) {
-    V best = key[0];
+  // the K-th fp32 key, then 64-bit keys from there up
+  float edge = neg_inf();
+  {
+    uint32_t k[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) k[i] = q[i] > neg_inf() ? ordered(q[i] + 0.f) : 0u;
+    for (int r = 0; r < s.K; ++r) {
+      uint32_t best = k[0];
+      int at = 0;
+#pragma unroll
+      for (int i = 1; i < P; ++i) {
+        at = k[i] > best ? i : at;
+        best = max(best, k[i]);
+      }
+      const uint32_t top = lane_max_u32<L>(best);
+      const bool mine = first + sub == first_lane<L>(best == top, first);
+#pragma unroll
+      for (int i = 0; i < P; ++i) k[i] = mine && i == at ? 0u : k[i];
+      edge = top != 0 ? unordered(top) : neg_inf();
+    }
+  }
+  if (bias != nullptr) {
+    exact_keys<P>(s, x, sp, bias, row.most, total, near(edge), key);
+  } else {  // the order is that of the logits
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = q[i] > neg_inf() ? static_cast<int64_t>(ordered(x[i] + 0.f)) : kNone64;
+  }
+  int chosen = -1;
+  for (int r = 0; r < s.K; ++r) {
+    int64_t best = key[0];
     int at = 0;
-    float bx = x[0];
 #pragma unroll
     for (int i = 1; i < P; ++i) {
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-        bx = x[i];
-      }
+      at = key[i] > best ? i : at;
+      best = key[i] > best ? key[i] : best;
     }
-    const V top = lane_max<L>(best);
-    unsigned who = __ballot_sync(kFull, best == top);
-    const int lane = threadIdx.x & 31, first = lane - sub;
-    if (L < 32) who = (who >> first) & ((1u << (L & 31)) - 1u);
-    const int from = first + __ffs(who) - 1;
-    int idx = __shfl_sync(kFull, sp.e0 + at, from);
-    const float wx = __shfl_sync(kFull, bx, from);
-    if (!(top > none)) idx = -1;
-    if (lane == from) {
+    const int64_t top = lane_max_i64<L>(best);
+    const int from = first_lane<L>(best == top, first);
+    const int idx = __shfl_sync(kFull, sp.e0 + at, from);
+    if (r == sub) chosen = top != kNone64 ? idx : -1;
+    const bool mine = first + sub == from;
 #pragma unroll
-      for (int i = 0; i < P; ++i) key[i] = i == at ? none : key[i];
-    }
-    if (k == sub && k < s.K) {
-      c.idx = idx;
-      c.x = idx < 0 ? neg_inf() : wx;
-      mine = top;
-    }
-    if (check) {
-      const float gap = last - top;
-      if (k > 0 && idx >= 0 && gap <= 2.f * slack + 0x1p-21f * (fabsf(last) + fabsf(top)) &&
-          !(wx == last_x && __ldg(bias + idx) == __ldg(bias + last_idx)))
-        c.unsure = true;
-      last = top;
-      last_idx = idx;
-      last_x = wx;
-    }
+    for (int i = 0; i < P; ++i) key[i] = mine && i == at ? kNone64 : key[i];
   }
-  (void)mine;
-  return c;
+  return chosen;
 }
 
-template <int P, int L>
-__device__ __noinline__ int2 choose_exact(const Shape& s, const float (&x)[P], Span sp, const float* bias, Row row,
-                                          int sub) {
-  const Chosen c = choose<double, P, L>(s, x, sp, bias, row, sub, 0.f);
-  return make_int2(c.idx, __float_as_int(c.x));
+__device__ __forceinline__ float logit_at(const Shape& s, const void* logits, int64_t at) {
+  return s.dtype == MOE_BF16   ? to_f32(static_cast<const __nv_bfloat16*>(logits)[at])
+         : s.dtype == MOE_FP16 ? to_f32(static_cast<const __half*>(logits)[at])
+                               : static_cast<const float*>(logits)[at];
 }
 
-template <int P, int L>
+// Over the first `width` lanes of a token (a power of two), valid in these.
+__device__ __forceinline__ float head_max(float v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float head_sum(float v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// Keys of the fast choice: the fp32 key as a whole number, its low log2(P) bits
+// replaced by the expert's place in the lane (lower places larger). A lane sorts
+// its keys once; a round is then one maximum over the lanes' heads, and the lane that
+// has it moves up. What the cut bits and the scores' errors leave open
+// is found afterwards, between neighbours of the result.
+template <int P, int L, bool MEAN>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(Shape s, const void* __restrict__ logits,
                                                               const float* __restrict__ bias, int32_t* __restrict__ idx,
                                                               float* __restrict__ w, float* __restrict__ partials) {
   constexpr int kTokens = kRouteThreads / L;  // a block at a time
-  const int lane = threadIdx.x & 31, sub = lane % L;
+  constexpr float kCut = P * 0x1p-22f;        // of a key: the cut bits, and its own rounding
+  const int lane = threadIdx.x & 31, sub = lane % L, first = lane - sub;
   const Span sp = span_of<P, L>(s, sub);
-  const bool mean = partials != nullptr;
-  const bool scores = bias != nullptr || (s.G > 1 && !s.group_max);
-  float acc[P];
+  const bool by_score = bias != nullptr || (s.G > 1 && !s.group_max);
+  const bool softmax_sum = !s.sigmoid && (by_score || !s.renorm || MEAN);
+  // 16-bit logits keep all their bits in a key
+  const bool check = by_score || s.dtype == MOE_FP32;
+  const int rounds = s.K + (check && s.K < s.E ? 1 : 0);
+  const int width = s.K > 1 ? 2 << (31 - __clz(s.K - 1)) : 1;
+  const bool vec_bias = bias != nullptr && s.vec_bias;
+  float acc[MEAN ? P : 1];
+  if constexpr (MEAN) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) acc[i] = 0.f;
+    for (int i = 0; i < P; ++i) acc[i] = 0.f;
+  }
   pdl_wait();
   pdl_launch_dependents();
   // every lane walks the same number of tokens: the shuffles take whole warps
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < s.T; t0 += static_cast<int64_t>(gridDim.x) * kTokens) {
     const int64_t t = t0 + threadIdx.x / L;
     const bool valid = t < s.T;
-    float x[P];
-    load_logits<P>(s, logits, valid ? t : s.T - 1, sp, x);
-    Row row = {neg_inf(), 1.f};
+    const int64_t tr = valid ? t : s.T - 1;
+    float x[P], q[P];  // logits; scores (softmax: times their sum)
+    load_logits<P>(s, logits, tr, sp, x);
     bool nan = false;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      row.most = fmaxf(row.most, x[i]);
-      nan |= x[i] != x[i];
-    }
-    row.most = lane_max<L>(row.most);
+    for (int i = 0; i < P; ++i) nan |= x[i] != x[i];
     unsigned any_nan = __ballot_sync(kFull, nan);
-    if (L < 32) any_nan = (any_nan >> (lane - sub)) & ((1u << (L & 31)) - 1u);
-    if (!s.sigmoid && (scores || !s.renorm || mean)) {
+    if (L < 32) any_nan = (any_nan >> first) & ((1u << (L & 31)) - 1u);
+    Row row = {neg_inf(), 1.f};
+    if (softmax_sum) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) row.most = fmaxf(row.most, x[i]);
+      row.most = lane_max<L>(row.most);
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < P; ++i) sum += x[i] > neg_inf() ? __expf(x[i] - row.most) : 0.f;
+      for (int i = 0; i < P; ++i) {
+        q[i] = x[i] > neg_inf() ? __expf(x[i] - row.most) : 0.f;
+        sum += q[i];
+      }
       row.sum = lane_sum<L>(sum);
+    } else if (s.sigmoid && (by_score || MEAN)) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) q[i] = sigmoid_fast(x[i]);
     }
-    // Errors of an fp32 score: sigmoid: below 3e-7 (its slope times the
-    // exponential's 2^-22 and its argument's |x| 2^-23, the sum's and the
-    // quotient's roundings); softmax: those of the exponential and of the sum, in
-    // all below 1.2e-6 of the largest score.
-    const float slack = s.sigmoid ? 4e-7f : __fdividef(1.5e-6f, row.sum);
-    Chosen c = choose<float, P, L>(s, x, sp, bias, row, sub, slack);
-    if (__any_sync(kFull, c.unsure)) {
-      const int2 e = choose_exact<P, L>(s, x, sp, bias, row, sub);
-      c.idx = e.x;
-      c.x = __int_as_float(e.y);
+    uint32_t key[P];
+    {
+      float v[P];
+      const float inv = by_score && !s.sigmoid ? __fdividef(1.f, row.sum) : 1.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = by_score ? q[i] * inv : x[i];
+      if (bias != nullptr) add_bias<P>(bias, sp, vec_bias, v);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const bool ok = x[i] > neg_inf() && v[i] > neg_inf();  // -inf behind the lane's last
+        key[i] = ok ? (ordered(v[i] + 0.f) & ~static_cast<uint32_t>(P - 1)) | (P - 1 - i) : 0u;
+      }
     }
-    float weight;
-    const bool have = sub < s.K && c.idx >= 0;
-    if (s.renorm) {
-      const float most = lane_max<L>(have ? c.x : neg_inf());
-      const float score = have ? ratio_score(s.sigmoid, c.x, most) : 0.f;
-      const float sum = lane_sum<L>(score);
+    sort_keys<P>(key);
+    const float slack = by_score ? score_slack(s, row) : 0.f;
+    bool unsure = false;
+    if (s.G > 1) {
+      const int lpg = 1 << (31 - __clz(32 / s.G));
+      uint32_t a = key[0], b = key[P > 1 ? 1 : 0];
+      for (int o = lpg / 2; o > 0; o >>= 1) {
+        const uint32_t a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+        b = max(min(a, a2), max(b, b2));
+        a = max(a, a2);
+      }
+      const float va = a != 0 ? unordered(a & ~static_cast<uint32_t>(P - 1)) : neg_inf();
+      const float vb = s.group_max || b == 0 ? 0.f : unordered(b & ~static_cast<uint32_t>(P - 1));
+      const float value = va + vb;
+      const int g = sub / lpg;
+      int rank = 0;
+      for (int j = 0; j < s.G; ++j) {
+        const float v = __shfl_sync(kFull, value, j * lpg);
+        rank += v > value || (v == value && j < g);
+      }
+      const bool in = rank < s.top_groups && g < s.G;
+      if (check && s.top_groups < s.G) {
+        const float err = 2.f * slack + kCut * (fabsf(va) + fabsf(vb));
+        const float worst = -lane_max<L>(in ? err - value : neg_inf());
+        const float best = lane_max<L>(in || g >= s.G ? neg_inf() : value + err);
+        unsure = worst <= best;
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) key[i] = in ? key[i] : 0u;
+    }
+    // lane k keeps the k-th key and the lane that had it; `next`: the one behind the last lane's
+    uint32_t mine = 0, next = 0;
+    int from_k = lane, from_next = lane;
+    for (int k = 0; k < rounds; ++k) {
+      // between lanes the places do not count: equal keys go to the lowest lane
+      const uint32_t head = key[0] & ~static_cast<uint32_t>(P - 1);
+      const int from = first_lane<L>(head == lane_max_u32<L>(head), first);
+      const uint32_t top = __shfl_sync(kFull, key[0], from);
+      if (k == sub) {
+        mine = top;
+        from_k = from;
+      }
+      if (k == L) {
+        next = top;
+        from_next = from;
+      }
+      if (lane == from) {
+#pragma unroll
+        for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1];
+        key[P - 1] = 0u;
+      }
+    }
+    const int place = P - 1 - static_cast<int>(mine & (P - 1));
+    int e = __shfl_sync(kFull, sp.e0, from_k) + place;
+    if (mine == 0) e = -1;
+    float xe = e >= 0 ? logit_at(s, logits, tr * s.ld + e) : neg_inf();
+    if (check) {
+      float be = e >= 0 && bias != nullptr ? __ldg(bias + e) : 0.f;
+      // the neighbour behind: the next lane's, or the extra one
+      uint32_t after = __shfl_sync(kFull, mine, (lane + 1) & 31);
+      float xa = __shfl_sync(kFull, xe, (lane + 1) & 31), ba = __shfl_sync(kFull, be, (lane + 1) & 31);
+      const int ea = __shfl_sync(kFull, sp.e0, from_next) + P - 1 - static_cast<int>(next & (P - 1));
+      if (sub == L - 1) {
+        after = next;
+        if (next != 0) {
+          xa = logit_at(s, logits, tr * s.ld + ea);
+          ba = bias != nullptr ? __ldg(bias + ea) : 0.f;
+        }
+      }
+      if (sub < s.K && sub + 1 < rounds && mine != 0 && after != 0) {
+        const float a = unordered(mine & ~static_cast<uint32_t>(P - 1)), b = unordered(after & ~static_cast<uint32_t>(P - 1));
+        const float err = by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f;
+        unsure |= a - b <= err && !(xe == xa && be == ba);
+      }
+      if (__any_sync(kFull, unsure)) {
+        e = choose_exact<P, L>(s, logits, tr, bias, row, sub);
+        if (sub >= s.K) e = -1;
+        xe = e >= 0 ? logit_at(s, logits, tr * s.ld + e) : neg_inf();
+      }
+    }
+    const bool have = sub < s.K && e >= 0;
+    float weight = 0.f;
+    if (s.sigmoid) {
+      float score = 0.f, n;
+      if (have) sigmoid_pair(xe, &score, &n);
+      if (s.renorm) {
+        float sum = head_sum(score, width);
+        if (__any_sync(kFull, sub < width && sum < 1e-20f)) {  // below fp32's range the ratios are those of e^x
+          const float most = head_max(have ? xe : neg_inf(), width);
+          const float low = have ? ratio_score(true, xe, most) : 0.f;
+          const float low_sum = head_sum(low, width);
+          if (sum < 1e-20f) {
+            score = low;
+            sum = low_sum;
+          }
+        }
+        score = have ? score / sum : 0.f;
+      }
+      weight = score * s.scale;
+    } else if (s.renorm) {
+      const float most = head_max(have ? xe : neg_inf(), width);
+      const float score = have ? expf(xe - most) : 0.f;
+      const float sum = head_sum(score, width);
       weight = have ? score / sum * s.scale : 0.f;
-    } else if (s.sigmoid) {
-      float sc, n;
-      sigmoid_pair(c.x, &sc, &n);
-      weight = have ? sc * s.scale : 0.f;
     } else {
-      weight = have ? expf(c.x - row.most) / row.sum * s.scale : 0.f;
+      weight = have ? expf(xe - row.most) / row.sum * s.scale : 0.f;
     }
     if (any_nan) weight = __int_as_float(0x7fffffff);
     if (valid && sub < s.K) {
-      idx[t * s.K + sub] = c.idx;
+      idx[t * s.K + sub] = e;
       w[t * s.K + sub] = weight;
     }
-    if (mean) {
-      float p[P], sum = 0.f;
+    if constexpr (MEAN) {
+      float sum = row.sum;
+      if (s.sigmoid) {
+        sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        if (!s.sigmoid) p[i] = x[i] == neg_inf() ? 0.f : __expf(x[i] - row.most);
-        else if (row.most < -60.f) p[i] = x[i] == neg_inf() ? 0.f : __expf(x[i] - row.most);
-        else p[i] = sigmoid_fast(x[i]);
-        sum += p[i];
+        for (int i = 0; i < P; ++i) sum += q[i];
+        sum = lane_sum<L>(sum);
+        if (__any_sync(kFull, sum < 1e-20f)) {
+          float most = neg_inf(), low = 0.f;
+#pragma unroll
+          for (int i = 0; i < P; ++i) most = fmaxf(most, x[i]);
+          most = lane_max<L>(most);
+          const bool small = sum < 1e-20f;
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            if (small) q[i] = x[i] == neg_inf() ? 0.f : __expf(x[i] - most);
+            low += q[i];
+          }
+          low = lane_sum<L>(low);
+          if (small) sum = low;
+        }
       }
-      sum = lane_sum<L>(sum);
-      const float f = valid && sum != 0.f ? __fdividef(1.f, sum) : 0.f;
+      if (any_nan) sum = __int_as_float(0x7fffffff);
+      const float f = sum != 0.f ? __fdividef(1.f, sum) : 0.f;
 #pragma unroll
-      for (int i = 0; i < P; ++i) acc[i] += valid ? p[i] * f : 0.f;
+      for (int i = 0; i < P; ++i) acc[i] += valid ? q[i] * f : 0.f;
     }
   }
-  if (!mean) return;
-  // lanes that hold the same experts, then the block's warps, in a fixed order
+  if constexpr (MEAN) {
+    // lanes that hold the same experts, then the block's warps, in a fixed order
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
+    for (int i = 0; i < P; ++i) {
 #pragma unroll
-    for (int o = 16; o >= L; o >>= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
-  }
-  __shared__ float cols[kRouteThreads / 32][kMaxExperts];
-  if (lane < L) {
-    for (int i = 0; i < P; ++i)
-      if (i < sp.n) cols[threadIdx.x / 32][sp.e0 + i] = acc[i];
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < s.E; e += kRouteThreads) {
-    float v = 0.f;
-    for (int k = 0; k < kRouteThreads / 32; ++k) v += cols[k][e];
-    partials[static_cast<size_t>(blockIdx.x) * s.E + e] = v;
+      for (int o = 16; o >= L; o >>= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
+    }
+    __shared__ float cols[kRouteThreads / 32][kMaxExperts];
+    if (lane < L) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (i < sp.n) cols[threadIdx.x / 32][sp.e0 + i] = acc[i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < s.E; e += kRouteThreads) {
+      float v = 0.f;
+      for (int k = 0; k < kRouteThreads / 32; ++k) v += cols[k][e];
+      partials[static_cast<size_t>(blockIdx.x) * s.E + e] = v;
+    }
   }
 }
 
@@ -413,10 +663,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(Shape s, 
       if (e < 0 || e >= s.E) e = -1;
       if (e >= 0) {
         v = dw[tr * s.K + sub] * s.scale;
-        const int64_t at = tr * s.ld + e;
-        xk = s.dtype == MOE_BF16   ? to_f32(static_cast<const __nv_bfloat16*>(logits)[at])
-             : s.dtype == MOE_FP16 ? to_f32(static_cast<const __half*>(logits)[at])
-                                   : static_cast<const float*>(logits)[at];
+        xk = logit_at(s, logits, tr * s.ld + e);
       }
     }
     float most = neg_inf(), sum = 0.f;
@@ -456,44 +703,52 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(Shape s, 
       add = e >= 0 ? v * sc : 0.f;
       all = lane_sum<L>(add);
     }
+    // the experts that are not chosen: their part of the mean's gradient and of `all`
+    float inner = 0.f;
     if (dense) {
-      float h[P], inner = 0.f;
+      float h[P];
       if (dmean != nullptr) {
+        load_as<P, float>(dmean, sp.e0, sp.n, s.vec_bias, h);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          h[i] = i < sp.n ? __ldg(dmean + sp.e0 + i) * inv_T : 0.f;
-          inner += d[i] * inv * h[i];
-        }
-        inner = lane_sum<L>(inner);
+        for (int i = 0; i < P; ++i) inner += i < sp.n ? d[i] * h[i] : 0.f;
+        inner = lane_sum<L>(inner) * inv;
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        float g = -all;
-        if (dmean != nullptr) g += h[i] - inner;
-        float v = d[i] * inv * g;
-        if (s.sigmoid) {
-          float a, b;
-          sigmoid_pair(x[i], &a, &b);
-          v *= b;
-        }
-        d[i] = v;
+        const float g = dmean != nullptr ? (h[i] - inner) * inv_T - all : -all;
+        d[i] *= inv * g;
+        if (s.sigmoid) d[i] *= sigmoid_fast(-x[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < P; ++i) d[i] = 0.f;
     }
+    // the chosen: an expert's first slot adds up all of its slots
+    float sum_k = 0.f;
+    bool first_k = e >= 0;
     for (int k = 0; k < s.K; ++k) {
       const int ek = __shfl_sync(kFull, e, lane - sub + k);
       const float ak = __shfl_sync(kFull, add, lane - sub + k);
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (i < sp.n && sp.e0 + i == ek) d[i] += ak;
+      sum_k += ek == e ? ak : 0.f;
+      if (ek == e && k < sub) first_k = false;
     }
+    if (dense && first_k) {
+      float p = !s.sigmoid || most < -60.f ? __expf(xk - most) : sigmoid_fast(xk);
+      p *= inv * ((dmean != nullptr ? (__ldg(dmean + e) - inner) * inv_T : 0.f) - all);
+      if (s.sigmoid) p *= sigmoid_fast(-xk);
+      sum_k += xk == neg_inf() ? 0.f : p;
+    }
+    const int64_t at = t * s.E;
     if (valid) {
-      const int64_t at = t * s.E + sp.e0;
-      if (s.dtype == MOE_BF16) store_as<P, __nv_bfloat16>(dx, at, sp.n, vec_out, d);
-      else if (s.dtype == MOE_FP16) store_as<P, __half>(dx, at, sp.n, vec_out, d);
-      else store_as<P, float>(dx, at, sp.n, vec_out, d);
+      if (s.dtype == MOE_BF16) store_as<P, __nv_bfloat16>(dx, at + sp.e0, sp.n, vec_out, d);
+      else if (s.dtype == MOE_FP16) store_as<P, __half>(dx, at + sp.e0, sp.n, vec_out, d);
+      else store_as<P, float>(dx, at + sp.e0, sp.n, vec_out, d);
+    }
+    __syncwarp();  // the chosen experts' stores come after those of their lanes
+    if (valid && first_k) {
+      if (s.dtype == MOE_BF16) static_cast<__nv_bfloat16*>(dx)[at + e] = from_f32<__nv_bfloat16>(sum_k);
+      else if (s.dtype == MOE_FP16) static_cast<__half*>(dx)[at + e] = from_f32<__half>(sum_k);
+      else static_cast<float*>(dx)[at + e] = sum_k;
     }
   }
 }
@@ -535,13 +790,15 @@ cudaError_t with_split(Split sp, F&& f) {
 }
 
 Shape shape_of(int dtype, const RouteArgs& a, const void* vec_ptr, int64_t ld, Split sp) {
-  Shape s = {a.T, a.E, a.K, dtype, a.G, a.top_groups, a.group_max, a.sigmoid, a.renorm, a.ld, a.scale, false};
+  Shape s = {a.T, a.E, a.K, dtype, a.G, a.top_groups, a.group_max, a.sigmoid, a.renorm, a.ld, a.scale, false, false};
   const int es = dtype == MOE_FP32 ? 4 : 2, bytes = sp.P * es < 16 ? sp.P * es : 16;
   // a lane's run starts at a multiple of its load's width and is a whole number of them
   const int lpg = a.G == 1 ? sp.L : 1 << (31 - __builtin_clz(32 / a.G));
   const int run = a.G == 1 ? sp.P : ceil_div(a.E / a.G, lpg);
   s.vec = run == sp.P && (a.G == 1 || a.E / a.G == run * lpg) && reinterpret_cast<uintptr_t>(vec_ptr) % bytes == 0 &&
           ld * es % bytes == 0;
+  const int bias_bytes = sp.P * 4 < 16 ? sp.P * 4 : 16;
+  s.vec_bias = run == sp.P && (a.G == 1 || a.E / a.G == run * lpg) && reinterpret_cast<uintptr_t>(a.bias) % bias_bytes == 0;
   return s;
 }
 
@@ -559,8 +816,9 @@ cudaError_t launch_route_tokens(int dtype, const RouteArgs& a, int num_sms, cuda
   const int blocks = route_blocks(a, sp, num_sms);
   if (blocks > 0) {
     const cudaError_t e = with_split(sp, [&](auto P, auto L) {
-      return launch_kernel(false, route_kernel<decltype(P)::value, decltype(L)::value>, blocks, kRouteThreads, 0, st, s,
-                           a.logits, a.bias, a.idx, a.w, a.mean != nullptr ? a.partials : nullptr);
+      constexpr int p = decltype(P)::value, l = decltype(L)::value;
+      return launch_kernel(false, a.mean != nullptr ? route_kernel<p, l, true> : route_kernel<p, l, false>, blocks,
+                           kRouteThreads, 0, st, s, a.logits, a.bias, a.idx, a.w, a.partials);
     });
     if (e != cudaSuccess) return e;
   }
@@ -572,7 +830,8 @@ cudaError_t launch_route_tokens(int dtype, const RouteArgs& a, int num_sms, cuda
 cudaError_t launch_route_tokens_backward(int dtype, const RouteArgs& a, const float* dw, const float* dmean, void* dx,
                                          int num_sms, cudaStream_t st) {
   const Split sp = split_of(a.E, a.K, 1);
-  const Shape s = shape_of(dtype, a, a.logits, a.ld, sp);
+  Shape s = shape_of(dtype, a, a.logits, a.ld, sp);
+  s.vec_bias = s.vec_bias && reinterpret_cast<uintptr_t>(dmean) % 16 == 0;  // dmean is read as a bias is
   const bool vec_out = shape_of(dtype, a, dx, a.E, sp).vec;
   return with_split(sp, [&](auto P, auto L) {
     return launch_kernel(false, route_backward_kernel<decltype(P)::value, decltype(L)::value>,
