@@ -433,12 +433,8 @@ moe_status moe_matmul_fp4(int N, int K, int swiglu, float swiglu_limit, const vo
   const moe_status s = check_ptrs({{prepared, 256}, {x, 2}, {workspace, 256}, {y, 2}}, &d);
   if (s != MOE_OK) return s;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const MatmulWorkspace w = matmul_workspace(T, K);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_quantize_act(dtype, x, ld_x, T, K, ws + w.codes, reinterpret_cast<uint32_t*>(ws + w.sf),
-                                            reinterpret_cast<uint32_t*>(ws), d.sms, st);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  return launched(launch_matmul_fp4(shape, swiglu_limit, prepared, dtype, T, y, ws, d.sms, st));
+  return launched(launch_matmul_fp4(shape, swiglu_limit, prepared, dtype, x, ld_x, T, y, ws, d.sms,
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -117,6 +117,11 @@ cudaError_t launch_dequantize_fp4(int dtype, const uint8_t* codes, const uint8_t
 // Tensor map of rows of `row_bytes` bytes (a multiple of 16), boxes of 128 bytes x
 // box_rows rows in the 128-byte swizzle; false if it cannot be made (api.cu).
 bool byte_tmap(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+// That of scale words [blocks][KB][128], boxes of 2 K blocks x box_blocks.
+bool scale_tmap(CUtensorMap* m, const void* base, uint64_t KB, uint64_t blocks, uint32_t box_blocks);
+// That of rows of 16-bit elements to be stored, contiguous and 16-byte aligned, boxes of box_cols x
+// box_rows with rows of 128 bytes in the 128-byte swizzle.
+bool store_tmap(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows);
 
 // FP4 x FP4 products.
 struct MatmulShape {
@@ -135,8 +140,8 @@ cudaError_t launch_matmul_prepare(const MatmulShape& s, const void* codes, const
                                   cudaStream_t st);
 // Activations [T][K] to codes [T][Kp / 2] and scale words; clears the status word.
 cudaError_t launch_quantize_act(int dtype, const void* x, int64_t ld, int T, int K, uint8_t* codes, uint32_t* sf,
-                                uint32_t* status, int num_sms, cudaStream_t st);
-cudaError_t launch_matmul_fp4(const MatmulShape& s, float limit, const void* prepared, int dtype, int T, void* y,
-                              uint8_t* workspace, int num_sms, cudaStream_t st);
+                                uint32_t* status, cudaStream_t st);
+cudaError_t launch_matmul_fp4(const MatmulShape& s, float limit, const void* prepared, int dtype, const void* x,
+                              int64_t ld, int T, void* y, uint8_t* workspace, int num_sms, cudaStream_t st);
 
 }  // namespace bsmoe
