@@ -281,12 +281,12 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, score, bias, num_groups, top_groups, group_score, renormalize, scale, mean_scores):
         ctx.args = dict(score=score, renormalize=renormalize, scale=scale)
-        idx, w, mean = _calls.route_tokens(logits, k, score, bias, num_groups, top_groups, group_score, renormalize,
-                                           scale, mean_scores)
-        ctx.save_for_backward(logits, idx)
-        ctx.mark_non_differentiable(idx)
+        out = _calls.route_tokens(logits, k, score, bias, num_groups, top_groups, group_score, renormalize, scale,
+                                  mean_scores)
+        ctx.save_for_backward(logits, out[0])
+        ctx.mark_non_differentiable(out[0])
         ctx.set_materialize_grads(False)
-        return (idx, w, mean) if mean_scores else (idx, w)
+        return out
 
     @staticmethod
     @once_differentiable
@@ -313,12 +313,11 @@ def route_tokens(logits, k, *, score="softmax", bias=None, num_groups=1, top_gro
     mean_scores=True returns also the mean over the tokens of the scores divided by
     their sum, float32 [E]: with the plan's counts, the terms of a balance loss.
     topk_w and the mean scores are differentiable with respect to the logits."""
-    args = (int(k), score, bias, int(num_groups), int(top_groups), group_score, bool(renormalize), float(scale),
-            bool(mean_scores))
     if _tracked(logits):
-        return _Route.apply(logits, *args)
-    idx, w, mean = _calls.route_tokens(logits, *args)
-    return (idx, w, mean) if mean_scores else (idx, w)
+        return _Route.apply(logits, k, score, bias, num_groups, top_groups, group_score, renormalize, float(scale),
+                            mean_scores)
+    return _calls.route_tokens(logits, k, score, bias, num_groups, top_groups, group_score, renormalize, scale,
+                               mean_scores)
 
 
 # --------------------------------------------------------------- the FP4 format

@@ -104,6 +104,8 @@ struct RouteArgs {
   float* partials;  // [kRouteParts][E] with mean
 };
 constexpr int kRouteParts = 608;  // the mean's column sums are taken over at most this many blocks
+cudaError_t launch_route_softmax(int dtype, const RouteArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_route_sigmoid(int dtype, const RouteArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_route_tokens(int dtype, const RouteArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_route_tokens_backward(int dtype, const RouteArgs& a, const float* dw, const float* dmean, void* dx,
                                          int num_sms, cudaStream_t st);

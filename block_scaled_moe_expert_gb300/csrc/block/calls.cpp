@@ -6,9 +6,11 @@
 // Python: what Python spends on a dozen tensor attributes is more than the
 // kernel. No arithmetic and no device code. The entry points come from the
 // library that `binding` loads, by address.
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -441,6 +443,25 @@ Tensor matvec(const Tensor& x, const MatvecWeights& m, std::optional<double> lim
   return y;
 }
 
+// ------------------------------------------------------------------ outputs
+
+// An uninitialised tensor on the current device, without the dispatcher's way to it: that
+// takes longer than the small calls' kernels.
+Tensor make_empty(at::IntArrayRef sizes, at::ScalarType type) {
+  return Tensor(at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(),
+                                          c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
+}
+// A contiguous part of such a tensor as one of its own (element offset `at` in units of type).
+Tensor part_of(const Tensor& whole, int64_t at, at::IntArrayRef sizes, at::ScalarType type) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                      c10::scalarTypeToTypeMeta(type));
+  c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(at);
+  impl->set_sizes_contiguous(sizes);
+  return t;
+}
+int64_t round_up(int64_t n, int64_t unit) { return (n + unit - 1) / unit * unit; }
+
 // ----------------------------------------------------------------- routing
 
 int score_code(const std::string& score) {
@@ -457,7 +478,7 @@ Tensor f32_vector(const Maybe& t, const First& f, const char* what) {
   return t->contiguous();
 }
 
-// (topk_idx, topk_w, mean_scores or None)
+// (topk_idx, topk_w) or (topk_idx, topk_w, mean_scores), parts of one allocation
 py::tuple route_tokens(const Tensor& logits, int k, const std::string& score, const Maybe& bias, int num_groups,
                        int top_groups, const std::string& group_score, bool renormalize, double scale, bool mean) {
   const First f = first(logits, "logits");
@@ -466,15 +487,15 @@ py::tuple route_tokens(const Tensor& logits, int k, const std::string& score, co
                     group_score, "'");
   const Tensor b = f32_vector(bias, f, "bias");
   // sizes are checked by the call below, before any use of these
-  const int64_t cols = k > 0 && k <= 32 ? k : 1;
-  const Tensor idx = at::empty({f.n, cols}, f.t.options().dtype(at::kInt));
-  const Tensor w = at::empty({f.n, cols}, f.t.options().dtype(at::kFloat));
+  const int64_t cols = k > 0 && k <= 32 ? k : 1, slots = round_up(f.n * cols, 64), experts = mean ? round_up(f.H, 64) : 0;
+  const Tensor all = make_empty({2 * slots + experts}, at::kInt);
+  const Tensor idx = part_of(all, 0, {f.n, cols}, at::kInt), w = part_of(all, slots, {f.n, cols}, at::kFloat);
   Tensor m, ws;
   size_t bytes = 0;
   if (mean) {
-    m = at::empty({f.H}, w.options());
+    m = part_of(all, 2 * slots, {f.H}, at::kFloat);
     bytes = api.moe_route_workspace_bytes(static_cast<int>(f.H));
-    ws = at::empty({static_cast<int64_t>(bytes)}, f.t.options().dtype(at::kByte));
+    ws = make_empty({static_cast<int64_t>(bytes)}, at::kByte);
   }
   check(api.moe_route_tokens(f.code, f.ptr(), f.ld, static_cast<const float*>(ptr(b)), static_cast<int>(f.n),
                              static_cast<int>(f.H), k, by, num_groups, top_groups,
@@ -483,7 +504,7 @@ py::tuple route_tokens(const Tensor& logits, int k, const std::string& score, co
                              static_cast<float*>(w.data_ptr()), static_cast<float*>(out_ptr(m)), out_ptr(ws), bytes,
                              stream(f.dev)),
         "moe_route_tokens");
-  return py::make_tuple(idx, w, or_none(m));
+  return mean ? py::make_tuple(idx, w, m) : py::make_tuple(idx, w);
 }
 
 Tensor route_tokens_backward(const Tensor& d_w, const Tensor& logits, const Tensor& topk_idx, const std::string& score,
@@ -498,7 +519,7 @@ Tensor route_tokens_backward(const Tensor& d_w, const Tensor& logits, const Tens
   operand(topk_idx, f.dev);
   operand(d_w, f.dev);
   const Tensor idx = topk_idx.contiguous(), dw = d_w.contiguous(), dm = f32_vector(d_mean, f, "d_mean_scores");
-  const Tensor dx = at::empty({f.n, f.H}, f.t.options());
+  const Tensor dx = make_empty({f.n, f.H}, f.type);
   check(api.moe_route_tokens_backward(f.code, static_cast<const float*>(ptr(dw)), static_cast<const float*>(ptr(dm)),
                                       f.ptr(), f.ld, static_cast<const int32_t*>(ptr(idx)), static_cast<int>(f.n),
                                       static_cast<int>(f.H), static_cast<int>(idx.size(1)), by, renormalize,
@@ -523,11 +544,13 @@ std::tuple<Tensor, Tensor> quantize_fp4(const Tensor& x) {
   // rows: every dimension but the last
   const First f = first(x.dim() == 2 ? x : x.contiguous().view({C == 0 ? 0 : x.numel() / C, C}), "x");
   TORCH_CHECK_VALUE(C > 0 && C % 32 == 0, "the last dimension must be a multiple of 32, got ", C);
-  std::vector<int64_t> cs(sizes.begin(), sizes.end()), ss = cs;
+  c10::SmallVector<int64_t, 6> cs(sizes.begin(), sizes.end()), ss(cs);
   cs.back() = C / 2;
   ss.back() = C / 32;
-  const auto u8 = f.t.options().dtype(at::kByte);
-  const Tensor codes = at::empty(cs, u8), scale = at::empty(ss, u8);
+  // one allocation: the codes, then the scales
+  const int64_t scale_at = round_up(f.n * (C / 2), 256);
+  const Tensor all = make_empty({scale_at + f.n * (C / 32)}, at::kByte);
+  const Tensor codes = part_of(all, 0, cs, at::kByte), scale = part_of(all, scale_at, ss, at::kByte);
   check(api.moe_quantize_fp4(f.code, f.ptr(), f.ld, static_cast<int>(f.n), static_cast<int>(C), codes.data_ptr(),
                              scale.data_ptr(), stream(f.dev)),
         "moe_quantize_fp4");
@@ -539,7 +562,7 @@ Tensor dequantize_fp4(const Tensor& codes, const Tensor& scale, at::ScalarType d
   TORCH_CHECK_VALUE(code >= 0, "dtype must be bfloat16, float16 or float32, got ", dtype);
   TORCH_CHECK_VALUE(codes.scalar_type() == at::kByte && codes.dim() >= 1 && codes.size(-1) % 16 == 0 && codes.size(-1) > 0,
                     "codes must be uint8 [..., C / 2], C a multiple of 32");
-  std::vector<int64_t> sizes = codes.sizes().vec();
+  c10::SmallVector<int64_t, 6> sizes(codes.sizes().begin(), codes.sizes().end());
   const int64_t C = 2 * sizes.back();
   sizes.back() = C / 32;
   TORCH_CHECK_VALUE(scale.scalar_type() == at::kByte && scale.sizes() == at::IntArrayRef(sizes),
@@ -549,7 +572,7 @@ Tensor dequantize_fp4(const Tensor& codes, const Tensor& scale, at::ScalarType d
   operand(scale, dev);
   const Tensor c = codes.contiguous(), s = scale.contiguous();
   sizes.back() = C;
-  const Tensor out = at::empty(sizes, c.options().dtype(dtype));
+  const Tensor out = make_empty(sizes, dtype);
   const int64_t rows = c.numel() / (C / 2);
   TORCH_CHECK_VALUE(rows <= INT32_MAX && C <= INT32_MAX, "codes is too large: ", codes.sizes());
   check(api.moe_dequantize_fp4(code, ptr(c), ptr(s), static_cast<int>(rows), static_cast<int>(C), out.data_ptr(),
@@ -596,17 +619,23 @@ Tensor matmul_fp4(const Tensor& x, const MatmulWeights& m, std::optional<double>
   no_gradient(x, "matmul_fp4");
   TORCH_CHECK_VALUE(!limit || m.swiglu, "swiglu_limit is for weights prepared with swiglu=True");
   operand(m.prepared, f.dev);
-  const int64_t need = matmul_fp4_workspace_bytes(m, f.n);
-  Tensor ws;
+  const int64_t need = matmul_fp4_workspace_bytes(m, f.n), cols = m.swiglu ? m.N / 2 : m.N;
+  Tensor ws, y;
+  if (out) y = output(out, f, f.n, cols);
   if (workspace) {
     TORCH_CHECK_VALUE(workspace->scalar_type() == at::kByte && workspace->is_contiguous(),
                       "workspace must be a contiguous uint8 tensor");
     operand(*workspace, f.dev);
     ws = *workspace;
-  } else {
-    ws = at::empty({need}, f.t.options().dtype(at::kByte));
   }
-  const Tensor y = output(out, f, f.n, m.swiglu ? m.N / 2 : m.N);
+  if (!out && !workspace && need <= 256) {  // a few tokens: y and the status word are one allocation
+    const int64_t status_at = round_up(2 * f.n * cols, 256);
+    ws = make_empty({status_at + need}, at::kByte);
+    y = part_of(ws, 0, {f.n, cols}, f.type);
+    ws = part_of(ws, status_at, {need}, at::kByte);
+  }
+  if (!ws.defined()) ws = make_empty({need}, at::kByte);
+  if (!y.defined()) y = make_empty({f.n, cols}, f.type);
   check(api.moe_matmul_fp4(m.N, m.K, m.swiglu, limit ? static_cast<float>(*limit) : -1.f, m.prepared.const_data_ptr(),
                            f.code, f.ptr(), f.ld, static_cast<int>(f.n), ws.data_ptr(),
                            static_cast<size_t>(ws.numel()), y.data_ptr(), stream(f.dev)),

@@ -611,7 +611,8 @@ MatmulLayout matmul_layout(const MatmulShape& s) {
 MatmulWorkspace matmul_workspace(int T, int K) {
   MatmulWorkspace w = {};
   const int KB = ceil_div(K, 128);
-  w.sf = 256;
+  w.sf = w.codes = w.total = 256;  // up to kOwnTokens: the status word alone
+  if (T <= kOwnTokens) return w;
   w.codes = w.sf + static_cast<size_t>(ceil_div(T, 2 * kMmM)) * 2 * KB * 512;  // whole tiles of a pair
   w.total = w.codes + align_up(static_cast<size_t>(T) * KB * 64, 256);
   return w;

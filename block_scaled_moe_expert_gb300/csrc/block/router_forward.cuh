@@ -1,0 +1,717 @@
+// The router's choice of experts, its weights and mean scores (moe_route_tokens), for
+// one kind of score.
+//
+// The K best are taken one after the other (largest of the lanes' largest, lowest
+// lane first: lanes hold ascending indices, so ties go to the lowest index); lane k
+// keeps the k-th. Keys are fp32 as whole numbers, the low log2(P) bits replaced by the
+// expert's place in the lane (lower places larger): a lane sorts its keys once, a
+// round is one maximum over the lanes' heads, and the lane that has it moves up.
+//
+// The choice is that of the exact scores. Without a bias the order is that of the
+// logits. With a bias, or where groups are ranked by sums of scores, neighbours of the
+// result that are nearer than the keys' error and do not come from the same inputs
+// are settled by pairs of floats (about 2^-43), in the lanes that hold them; what
+// pairs leave open, or needs experts that no lane holds yet, by 64 bits. Of tokens with
+// scores spread like a router's about one in 300 takes the first way, one in 10^5 the second.
+//
+// Bounds: the logits are read once, 2 or 4 bytes for some 15 instructions a logit and
+// 25 a choice: instruction issue for large batches, launch latency for small ones.
+#pragma once
+#include "router_common.cuh"
+
+namespace bsmoe {
+
+namespace {
+
+// What the lanes of a token know about all its logits.
+struct Row {
+  float most;  // largest logit
+  float sum;   // sum of e^(x - most), where softmax scores are needed
+};
+
+// A monotone map of floats to whole numbers above 0, and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ int64_t ordered(double v) {
+  const int64_t u = __double_as_longlong(v);
+  return u ^ static_cast<int64_t>(static_cast<uint64_t>(u >> 63) >> 1);
+}
+constexpr int64_t kNone64 = INT64_MIN;  // below the image of every number
+
+template <int L>
+__device__ __forceinline__ uint32_t lane_max_u32(uint32_t v) {
+  if constexpr (L == 32) {
+    return __reduce_max_sync(kFull, v);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  }
+}
+// The lowest lane of the token for which `mine` holds.
+template <int L>
+__device__ __forceinline__ int first_lane(bool mine, int first) {
+  unsigned who = __ballot_sync(kFull, mine);
+  if (L < 32) who = (who >> first) & ((1u << (L & 31)) - 1u);
+  return first + __ffs(who) - 1;
+}
+
+// Descending sort of a lane's keys (Batcher's odd-even merge network).
+template <int P>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[P]) {
+#pragma unroll
+  for (int p = 1; p < P; p *= 2) {
+#pragma unroll
+    for (int q = p; q > 0; q /= 2) {
+#pragma unroll
+      for (int j = q % p; j + q < P; j += 2 * q) {
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          const int a = i + j, b = i + j + q;
+          if (b < P && a / (2 * p) == b / (2 * p)) {
+            const uint32_t hi = max(k[a], k[b]), lo = min(k[a], k[b]);
+            k[a] = hi;
+            k[b] = lo;
+          }
+        }
+      }
+    }
+  }
+}
+
+// fp32 scores plus bias of a lane's experts, NaN or -inf where one is not available.
+// Errors of an fp32 score: sigmoid: below 3e-7 (its slope times the exponential's
+// 2^-22 and its argument's |x| 2^-23, the sum's and the quotient's roundings);
+// softmax: those of the exponential and of the sum, in all below 1.2e-6 of the
+// largest score. `score_slack` is above both.
+template <bool SIGMOID>
+__device__ __forceinline__ float score_slack(Row row) {
+  return SIGMOID ? 4e-7f : 1.5e-6f * rcp_fast(row.sum);
+}
+template <int P>
+__device__ __forceinline__ void add_bias(const float* bias, Span sp, bool vec, float (&q)[P]) {
+  float b[P];
+  load_as<P, float>(bias, sp.e0, sp.n, vec, b);
+#pragma unroll
+  for (int i = 0; i < P; ++i) q[i] += b[i];
+}
+
+// 64-bit scores of a few of a lane's experts (bits of `need`) into keys. All lanes call it.
+template <int P, bool SIGMOID>
+__device__ __forceinline__ void exact_keys(const Shape& s, const float (&x)[P], Span sp, const float* bias, float most,
+                                           double total, unsigned need, int64_t (&key)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) key[i] = kNone64;
+  while (__any_sync(kFull, need != 0)) {
+    const int at = need != 0 ? __ffs(need) - 1 : 0;
+    float xv = x[0];
+#pragma unroll
+    for (int i = 1; i < P; ++i) xv = i == at ? x[i] : xv;
+    const double e = exp(SIGMOID ? -static_cast<double>(xv) : static_cast<double>(xv) - static_cast<double>(most));
+    double q = SIGMOID ? 1.0 / (1.0 + e) : e / total;
+    if (bias != nullptr && at < sp.n) q += static_cast<double>(__ldg(bias + sp.e0 + at));
+    const int64_t k = ordered(q);
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = need != 0 && i == at ? k : key[i];
+    need &= need - 1;
+  }
+}
+
+template <int L>
+__device__ __forceinline__ int64_t lane_max_i64(int64_t v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const int64_t w = __shfl_xor_sync(kFull, v, o);
+    v = v > w ? v : w;
+  }
+  return v;
+}
+
+// The choice with keys in 64 bits: the whole warp calls it where a token of it is
+// unsure. Only experts whose fp32 key is within its error of the border get one.
+// Returns the index of the sub-th choice.
+template <int P, int L, bool SIGMOID>
+__device__ __noinline__ int choose_exact(Shape s, const void* logits, int64_t t, const float* bias, Row row, int sub) {
+  const int first = (threadIdx.x & 31) - sub;
+  const Span sp = span_of(s, sub);
+  const bool by_score = bias != nullptr || (s.G > 1 && !s.group_max);
+  const float slack = score_slack<SIGMOID>(row);
+  float x[P], q[P];
+  load_logits<P>(s, logits, t, sp, x);
+  double total = 1;
+  if (by_score && !SIGMOID) {
+    double sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < P; ++i) {
+      float xv = x[0];
+#pragma unroll
+      for (int j = 1; j < P; ++j) xv = j == i ? x[j] : xv;
+      sum += xv > neg_inf() ? exp(static_cast<double>(xv) - static_cast<double>(row.most)) : 0.0;
+    }
+    total = lane_sum<L>(sum);
+  }
+  const float inv = by_score && !SIGMOID ? rcp_fast(row.sum) : 1.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    q[i] = x[i] + 0.f;
+    if (by_score) q[i] = SIGMOID ? sigmoid_fast(x[i]) : exp_fast(x[i] - row.most) * inv;
+  }
+  if (bias != nullptr) add_bias<P>(bias, sp, false, q);
+#pragma unroll
+  for (int i = 0; i < P; ++i) q[i] = i < sp.n && x[i] > neg_inf() && q[i] > neg_inf() ? q[i] : neg_inf();
+  int64_t key[P];
+  // the experts that may reach a border at `edge`
+  auto near = [&](float edge) {
+    const float from = fabsf(edge) < INFINITY ? edge - 4.f * slack - 0x1p-20f * fabsf(edge) : edge;
+    unsigned need = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) need |= static_cast<unsigned>(q[i] > neg_inf() && q[i] >= from) << i;
+    return need;
+  };
+  if (s.G > 1) {
+    const int lpg = 1 << s.lanes_log2;
+    float a = neg_inf(), b = neg_inf();
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      b = fmaxf(b, fminf(a, q[i]));
+      a = fmaxf(a, q[i]);
+    }
+    for (int o = lpg / 2; o > 0; o >>= 1) {
+      const float a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+      b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+      a = fmaxf(a, a2);
+    }
+    if (by_score) {
+      exact_keys<P, SIGMOID>(s, x, sp, bias, row.most, total, near(s.group_max ? a : b), key);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) key[i] = q[i] > neg_inf() ? ordered(static_cast<double>(q[i])) : kNone64;
+    }
+    int64_t c = kNone64, d = kNone64;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int64_t lo = key[i] < c ? key[i] : c;
+      d = d > lo ? d : lo;
+      c = c > key[i] ? c : key[i];
+    }
+    for (int o = lpg / 2; o > 0; o >>= 1) {
+      const int64_t c2 = __shfl_xor_sync(kFull, c, o), d2 = __shfl_xor_sync(kFull, d, o);
+      const int64_t lo = c < c2 ? c : c2, hi = d > d2 ? d : d2;
+      d = lo > hi ? lo : hi;
+      c = c > c2 ? c : c2;
+    }
+    auto value_of = [](int64_t o) { return __longlong_as_double(o ^ static_cast<int64_t>(static_cast<uint64_t>(o >> 63) >> 1)); };
+    const int64_t value = s.group_max || d == kNone64 ? c : ordered(value_of(c) + value_of(d));
+    const int g = sub >> s.lanes_log2;
+    int rank = 0;
+    for (int j = 0; j < s.G; ++j) {
+      const int64_t v = __shfl_sync(kFull, value, j * lpg);
+      rank += v > value || (v == value && j < g);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) q[i] = rank < s.top_groups && g < s.G ? q[i] : neg_inf();
+  }
+  // the K-th fp32 key, then 64-bit keys from there up
+  float edge = neg_inf();
+  {
+    uint32_t k[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) k[i] = q[i] > neg_inf() ? ordered(q[i] + 0.f) : 0u;
+    for (int r = 0; r < s.K; ++r) {
+      uint32_t best = k[0];
+      int at = 0;
+#pragma unroll
+      for (int i = 1; i < P; ++i) {
+        at = k[i] > best ? i : at;
+        best = max(best, k[i]);
+      }
+      const uint32_t top = lane_max_u32<L>(best);
+      const bool mine = first + sub == first_lane<L>(best == top, first);
+#pragma unroll
+      for (int i = 0; i < P; ++i) k[i] = mine && i == at ? 0u : k[i];
+      edge = top != 0 ? unordered(top) : neg_inf();
+    }
+  }
+  if (bias != nullptr) {
+    exact_keys<P, SIGMOID>(s, x, sp, bias, row.most, total, near(edge), key);
+  } else {  // the order is that of the logits
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = q[i] > neg_inf() ? static_cast<int64_t>(ordered(x[i] + 0.f)) : kNone64;
+  }
+  int chosen = -1;
+  for (int r = 0; r < s.K; ++r) {
+    int64_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < P; ++i) {
+      at = key[i] > best ? i : at;
+      best = key[i] > best ? key[i] : best;
+    }
+    const int64_t top = lane_max_i64<L>(best);
+    const int from = first_lane<L>(best == top, first);
+    const int idx = __shfl_sync(kFull, sp.e0 + at, from);
+    if (r == sub) chosen = top != kNone64 ? idx : -1;
+    const bool mine = first + sub == from;
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = mine && i == at ? kNone64 : key[i];
+  }
+  return chosen;
+}
+
+// ------------------------------------------------- sums of two floats
+// hi + lo with |lo| at most half a unit of hi: the error-free sums and products of
+// T. J. Dekker, A floating-point technique for extending the available precision
+// (1971), and D. E. Knuth's sum of two.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two renormalise(float a, float b) {  // |a| >= |b|
+  const float s = a + b;
+  return {s, b - (s - a)};
+}
+__device__ __forceinline__ Two sum_of(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = sum_of(a.hi, b.hi);
+  return renormalise(s.hi, s.lo + (a.lo + b.lo));
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  const float p = a.hi * b.hi;
+  return renormalise(p, fmaf(a.lo, b.hi, fmaf(a.hi, b.lo, fmaf(a.hi, b.hi, -p))));
+}
+__device__ __forceinline__ Two reciprocal(Two a) {  // one Newton step from the fp32 value
+  const float q = 1.f / a.hi;
+  const float r = fmaf(-q, a.lo, fmaf(-q, a.hi, 1.f));
+  return renormalise(q, q * r);
+}
+// e^y for -80 <= y <= 80 to about 2^-44: y = n ln 2 + 8 r, ln 2 as 1419 / 2048 (n times it is
+// exact) and two floats; Taylor's series of e^r, |r| < 0.0434, its terms from the fifth on
+// in fp32; three squarings.
+__device__ __forceinline__ Two exp_two(Two y) {
+  const float n = rintf(y.hi * 1.44269504f);
+  const float p = n * 0x1.217f7ep-12f;
+  Two r = add(add(sum_of(y.hi, -n * 0.69287109375f), {y.lo, 0.f}),
+              {-p, -fmaf(n, 0x1.217f7ep-12f, -p) - n * -0x1.c610cap-37f});
+  r = {r.hi * 0.125f, r.lo * 0.125f};
+  const float t = fmaf(r.hi, fmaf(r.hi, 0x1.a01a02p-13f, 0x1.6c16c2p-10f), 0x1.111112p-7f);  // 1/5! + r/6! + r^2/7!
+  Two e = add(mul(r, {t, 0.f}), {0x1.555556p-5f, -0x1.555556p-30f});                          // 1/4!
+  e = add(mul(r, e), {0x1.555556p-3f, -0x1.555556p-28f});                                     // 1/3!
+  e = add(mul(r, e), {0.5f, 0.f});
+  e = add(mul(r, e), {1.f, 0.f});
+  e = add(mul(r, e), {1.f, 0.f});
+  e = mul(e, e);
+  e = mul(e, e);
+  e = mul(e, e);
+  return {ldexpf(e.hi, static_cast<int>(n)), ldexpf(e.lo, static_cast<int>(n))};
+}
+
+// A key of two floats as a whole number above 0 in the same order.
+__device__ __forceinline__ uint64_t packed(Two v) {
+  return static_cast<uint64_t>(ordered(v.hi + 0.f)) << 32 | ordered(v.lo + 0.f);
+}
+__device__ __forceinline__ Two unpacked(uint64_t k) {
+  return {unordered(static_cast<uint32_t>(k >> 32)), unordered(static_cast<uint32_t>(k))};
+}
+// Whether pairs of floats settle the order of two keys.
+__device__ __forceinline__ bool settled(Two a, Two b) {
+  return fabsf((a.hi - b.hi) + (a.lo - b.lo)) > 0x1p-40f * (fabsf(a.hi) + fabsf(b.hi));
+}
+
+// Score plus bias; `ok` is cleared where exp_two does not reach.
+template <bool SIGMOID>
+__device__ __forceinline__ Two key_two(float x, float bias, float most, Two inv_total, bool* ok) {
+  const Two y = SIGMOID ? Two{-fabsf(x), 0.f} : sum_of(x, -most);
+  if (!(fabsf(y.hi) <= 80.f)) {
+    *ok = false;
+    return {0.f, 0.f};
+  }
+  const Two z = exp_two(y);
+  Two s;
+  if (SIGMOID) {
+    s = reciprocal(add({1.f, 0.f}, z));
+    if (x < 0.f) s = mul(s, z);
+  } else {
+    s = mul(z, inv_total);
+  }
+  return bias == 0.f ? s : add(s, {bias, 0.f});
+}
+// 1 / sum of e^(x - most) over the token (softmax).
+template <int P, int L>
+__device__ __forceinline__ Two inv_total_two(const Shape& s, const void* logits, int64_t t, Span sp, float most) {
+  Two sum = {0.f, 0.f};
+#pragma unroll 1
+  for (int i = 0; i < P; ++i) {
+    const float x = i < sp.n ? logit_at(s, logits, t * s.ld + sp.e0 + i) : neg_inf();
+    const Two y = sum_of(x, -most);
+    if (x - most >= -80.f) sum = add(sum, exp_two(y));  // less than e^-80 of the sum does not show
+  }
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1)
+    sum = add(sum, {__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)});
+  return reciprocal(sum);
+}
+
+// The order of the candidates that lanes 0..K of a token hold, settled by pairs
+// of floats: the sub-th expert, or -2 for the whole warp where they do not.
+template <int P, int L, bool SIGMOID>
+__device__ __noinline__ int order_candidates(Shape s, const void* logits, int64_t t, const float* bias, Row row, int sub,
+                                             int e, float x) {
+  const int first = (threadIdx.x & 31) - sub;
+  const bool have = e >= 0;
+  const float b = have && bias != nullptr ? __ldg(bias + e) : 0.f;
+  bool ok = true;
+  uint64_t key = 0;
+  if (bias == nullptr) {  // within groups: the order of the logits
+    if (have) key = packed({x, 0.f});
+  } else {
+    Two inv = {1.f, 0.f};
+    if (!SIGMOID) inv = inv_total_two<P, L>(s, logits, t, span_of(s, sub), row.most);
+    if (have) key = packed(key_two<SIGMOID>(x, b, row.most, inv, &ok));
+  }
+  int rank = 0;
+  for (int j = 0; j <= s.K; ++j) {
+    const uint64_t kj = __shfl_sync(kFull, key, first + j);
+    const int ej = __shfl_sync(kFull, e, first + j);
+    const float xj = __shfl_sync(kFull, x, first + j), bj = __shfl_sync(kFull, b, first + j);
+    if (j != sub && have && ej >= 0) {
+      rank += kj > key || (kj == key && ej < e);
+      if (bias != nullptr && !(xj == x && bj == b) && !settled(unpacked(kj), unpacked(key))) ok = false;
+    } else if (j != sub && !have && (ej >= 0 || j < sub)) {
+      ++rank;
+    }
+  }
+  if (sub > s.K) rank = sub;
+  int out = -1;
+  for (int j = 0; j <= s.K; ++j) {
+    const int rj = __shfl_sync(kFull, rank, first + j), ej = __shfl_sync(kFull, e, first + j);
+    if (rj == sub) out = ej;
+  }
+  return __all_sync(kFull, ok) ? out : -2;
+}
+
+// Whether this lane's group is among the best, from the two best keys of each lane in
+// pairs of floats (key: the lane's three best fp32 keys; edge: the fp32 value
+// that a group's third may not come near). L is 32. -1 where they do not settle it.
+template <int P, bool SIGMOID>
+__device__ __noinline__ int rank_groups(Shape s, const void* logits, int64_t t, const float* bias, Row row, int sub,
+                                        uint3 key, float edge, float err) {
+  const Span sp = span_of(s, sub);
+  Two inv = {1.f, 0.f};
+  if (!SIGMOID) inv = inv_total_two<P, 32>(s, logits, t, sp, row.most);
+  bool ok = true;
+  uint64_t c[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t k = j == 0 ? key.x : key.y;
+    if (k != 0) {
+      const int e = sp.e0 + P - 1 - static_cast<int>(k & (P - 1));
+      c[j] = packed(key_two<SIGMOID>(logit_at(s, logits, t * s.ld + e), bias != nullptr ? __ldg(bias + e) : 0.f, row.most,
+                                     inv, &ok));
+    }
+  }
+  if (key.z != 0 && unordered(key.z & ~static_cast<uint32_t>(P - 1)) + err >= edge) ok = false;
+  uint64_t a = max(c[0], c[1]), b = min(c[0], c[1]);
+  for (int o = 1 << s.lanes_log2 >> 1; o > 0; o >>= 1) {
+    const uint64_t a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+    b = max(min(a, a2), max(b, b2));
+    a = max(a, a2);
+  }
+  const uint64_t value = s.group_max || b == 0 ? a : packed(add(unpacked(a), unpacked(b)));
+  const int g = sub >> s.lanes_log2;
+  int rank = 0;
+  for (int j = 0; j < s.G; ++j) {
+    const uint64_t v = __shfl_sync(kFull, value, j << s.lanes_log2);
+    rank += v > value || (v == value && j < g);
+    if (g < s.G && j != g && v != 0 && value != 0 && !settled(unpacked(v), unpacked(value))) ok = false;
+  }
+  return __all_sync(kFull, ok) ? (rank < s.top_groups && g < s.G) : -1;
+}
+
+// Over the first `width` lanes of a token (a power of two), valid in these.
+__device__ __forceinline__ float head_max(float v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float head_sum(float v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+template <int P, int L, bool SIGMOID, bool MEAN>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(Shape s, const void* __restrict__ logits,
+                                                              const float* __restrict__ bias, int32_t* __restrict__ idx,
+                                                              float* __restrict__ w, float* __restrict__ partials) {
+  constexpr int kTokens = kRouteThreads / L;  // a block at a time
+  constexpr float kCut = P * 0x1p-22f;        // of a key: the cut bits, and its own rounding
+  const int lane = threadIdx.x & 31, sub = lane % L, first = lane - sub;
+  const Span sp = span_of(s, sub);
+  const bool by_score = bias != nullptr || (s.G > 1 && !s.group_max);
+  const bool softmax_sum = !SIGMOID && (by_score || !s.renorm || MEAN);
+  // 16-bit logits keep all their bits in a key
+  const bool check = by_score || s.dtype == MOE_FP32;
+  const int rounds = s.K + (check && s.K < s.E ? 1 : 0);
+  const int width = s.K > 1 ? 2 << (31 - __clz(s.K - 1)) : 1;
+  const bool vec_bias = bias != nullptr && s.vec_bias;
+  float acc[MEAN ? P : 1];
+  if constexpr (MEAN) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) acc[i] = 0.f;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTokens;
+  float ahead[MEAN ? P : 1];  // blocks that take many tokens: the next one's logits are on their way
+  if constexpr (MEAN) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / L;
+    load_logits<P>(s, logits, t < s.T ? t : s.T - 1, sp, ahead);
+  }
+  // every lane walks the same number of tokens: the shuffles take whole warps
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < s.T; t0 += step) {
+    const int64_t t = t0 + threadIdx.x / L;
+    const bool valid = t < s.T;
+    const int64_t tr = valid ? t : s.T - 1;
+    float x[P], q[P];  // logits; scores (softmax: times their sum)
+    if constexpr (MEAN) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[i] = ahead[i];
+      if (t0 + step < s.T) load_logits<P>(s, logits, t + step < s.T ? t + step : s.T - 1, sp, ahead);
+    } else {
+      load_logits<P>(s, logits, tr, sp, x);
+    }
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < P; ++i) nan |= x[i] != x[i];
+    unsigned any_nan = __ballot_sync(kFull, nan);
+    if (L < 32) any_nan = (any_nan >> first) & ((1u << (L & 31)) - 1u);
+    Row row = {neg_inf(), 1.f};
+    if (softmax_sum) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) row.most = fmaxf(row.most, x[i]);
+      row.most = lane_max<L>(row.most);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        q[i] = x[i] > neg_inf() ? exp_fast(x[i] - row.most) : 0.f;
+        sum += q[i];
+      }
+      row.sum = lane_sum<L>(sum);
+    } else if (SIGMOID && (by_score || MEAN)) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) q[i] = sigmoid_fast(x[i]);
+    }
+    uint32_t key[P];
+    {
+      float v[P];
+      const float inv = by_score && !SIGMOID ? rcp_fast(row.sum) : 1.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = by_score ? q[i] * inv : x[i];
+      if (bias != nullptr) add_bias<P>(bias, sp, vec_bias, v);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const bool ok = x[i] > neg_inf() && v[i] > neg_inf();  // -inf behind the lane's last
+        key[i] = ok ? (ordered(v[i] + 0.f) & ~static_cast<uint32_t>(P - 1)) | (P - 1 - i) : 0u;
+      }
+    }
+    sort_keys<P>(key);
+    const float slack = by_score ? score_slack<SIGMOID>(row) : 0.f;
+    bool unsure = false, exact = false;  // settled by pairs of floats; by 64 bits
+    if (s.G > 1) {
+      const int lpg = 1 << s.lanes_log2;
+      uint32_t a = key[0], b = key[P > 1 ? 1 : 0];
+      for (int o = lpg / 2; o > 0; o >>= 1) {
+        const uint32_t a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+        b = max(min(a, a2), max(b, b2));
+        a = max(a, a2);
+      }
+      const float va = a != 0 ? unordered(a & ~static_cast<uint32_t>(P - 1)) : neg_inf();
+      const float vb = s.group_max || b == 0 ? 0.f : unordered(b & ~static_cast<uint32_t>(P - 1));
+      const float value = va + vb;
+      const int g = sub >> s.lanes_log2;
+      int rank = 0;
+      for (int j = 0; j < s.G; ++j) {
+        const float v = __shfl_sync(kFull, value, j * lpg);
+        rank += v > value || (v == value && j < g);
+      }
+      bool in = rank < s.top_groups && g < s.G;
+      if (check && s.top_groups < s.G) {
+        const float err = 2.f * slack + kCut * (fabsf(va) + fabsf(vb));
+        const float worst = -lane_max<L>(in ? err - value : neg_inf());
+        const float best = lane_max<L>(in || g >= s.G ? neg_inf() : value + err);
+        if (worst <= best) {  // the token's lanes are the warp's: all agree
+          int settled_in = -1;
+          if (by_score)
+            settled_in = rank_groups<P, SIGMOID>(s, logits, tr, bias, row, sub, make_uint3(key[0], key[1], P > 2 ? key[P > 2 ? 2 : 0] : 0u),
+                                                 (s.group_max ? va : b == 0 ? neg_inf() : vb) - err, err);
+          exact = settled_in < 0;
+          if (!exact) in = settled_in != 0;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) key[i] = in ? key[i] : 0u;
+    }
+    // lane k keeps the k-th key and the lane that had it; `next`: the one behind the last lane's
+    uint32_t mine = 0, next = 0;
+    int from_k = lane, from_next = lane;
+    for (int k = 0; k < rounds; ++k) {
+      // between lanes the places do not count: equal keys go to the lowest lane
+      const uint32_t head = key[0] & ~static_cast<uint32_t>(P - 1);
+      const int from = first_lane<L>(head == lane_max_u32<L>(head), first);
+      const uint32_t top = __shfl_sync(kFull, key[0], from);
+      if (k == sub) {
+        mine = top;
+        from_k = from;
+      }
+      if (k == L) {
+        next = top;
+        from_next = from;
+      }
+      if (lane == from) {
+#pragma unroll
+        for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1];
+        key[P - 1] = 0u;
+      }
+    }
+    const int place = P - 1 - static_cast<int>(mine & (P - 1));
+    int e = __shfl_sync(kFull, sp.e0, from_k) + place;
+    if (mine == 0) e = -1;
+    float xe = e >= 0 ? logit_at(s, logits, tr * s.ld + e) : neg_inf();
+    if (check) {
+      const float be = e >= 0 && bias != nullptr ? __ldg(bias + e) : 0.f;
+      // the neighbour behind: the next lane's, or the extra one
+      uint32_t after = __shfl_sync(kFull, mine, (lane + 1) & 31);
+      float xa = __shfl_sync(kFull, xe, (lane + 1) & 31), ba = __shfl_sync(kFull, be, (lane + 1) & 31);
+      const int ea = __shfl_sync(kFull, sp.e0, from_next) + P - 1 - static_cast<int>(next & (P - 1));
+      if (sub == L - 1) {
+        after = next;
+        if (next != 0) {
+          xa = logit_at(s, logits, tr * s.ld + ea);
+          ba = bias != nullptr ? __ldg(bias + ea) : 0.f;
+        }
+      }
+      if (sub < s.K && sub + 1 < rounds && mine != 0 && after != 0) {
+        const float a = unordered(mine & ~static_cast<uint32_t>(P - 1)), b = unordered(after & ~static_cast<uint32_t>(P - 1));
+        const float err = by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f;
+        unsure |= a - b <= err && !(xe == xa && be == ba);
+      }
+      if (__any_sync(kFull, unsure || exact)) {
+        // candidates: the K + 1 that the lanes hold, if the next one is surely none
+        const uint32_t head = lane_max_u32<L>(key[0]);
+        const uint32_t kth = __shfl_sync(kFull, mine, first + s.K - 1);
+        if (head != 0 && s.K < L) {
+          const float a = unordered(kth & ~static_cast<uint32_t>(P - 1)), b = unordered(head & ~static_cast<uint32_t>(P - 1));
+          exact |= a - b <= (by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f);
+        }
+        exact |= s.K == L;
+        int chosen = -2;
+        if (!__any_sync(kFull, exact)) chosen = order_candidates<P, L, SIGMOID>(s, logits, tr, bias, row, sub, e, xe);
+        if (chosen == -2) chosen = choose_exact<P, L, SIGMOID>(s, logits, tr, bias, row, sub);
+        e = sub < s.K ? chosen : -1;
+        xe = e >= 0 ? logit_at(s, logits, tr * s.ld + e) : neg_inf();
+      }
+    }
+    const bool have = sub < s.K && e >= 0;
+    float weight = 0.f;
+    if (SIGMOID) {
+      float score = 0.f, n;
+      if (have) sigmoid_pair(xe, &score, &n);
+      if (s.renorm) {
+        float sum = head_sum(score, width);
+        if (__any_sync(kFull, sub < width && sum < 1e-20f)) {  // below fp32's range the ratios are those of e^x
+          const float most = head_max(have ? xe : neg_inf(), width);
+          const float low = have ? ratio_score<true>(xe, most) : 0.f;
+          const float low_sum = head_sum(low, width);
+          if (sum < 1e-20f) {
+            score = low;
+            sum = low_sum;
+          }
+        }
+        score = have ? score / sum : 0.f;
+      }
+      weight = score * s.scale;
+    } else if (s.renorm) {
+      const float most = head_max(have ? xe : neg_inf(), width);
+      const float score = have ? expf(xe - most) : 0.f;
+      const float sum = head_sum(score, width);
+      weight = have ? score / sum * s.scale : 0.f;
+    } else {
+      weight = have ? expf(xe - row.most) / row.sum * s.scale : 0.f;
+    }
+    if (any_nan) weight = __int_as_float(0x7fffffff);
+    if (valid && sub < s.K) {
+      idx[t * s.K + sub] = e;
+      w[t * s.K + sub] = weight;
+    }
+    if constexpr (MEAN) {
+      float sum = row.sum;
+      if (SIGMOID) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) sum += q[i];
+        sum = lane_sum<L>(sum);
+        if (__any_sync(kFull, sum < 1e-20f)) {
+          float most = neg_inf(), low = 0.f;
+#pragma unroll
+          for (int i = 0; i < P; ++i) most = fmaxf(most, x[i]);
+          most = lane_max<L>(most);
+          const bool small = sum < 1e-20f;
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            if (small) q[i] = x[i] == neg_inf() ? 0.f : exp_fast(x[i] - most);
+            low += q[i];
+          }
+          low = lane_sum<L>(low);
+          if (small) sum = low;
+        }
+      }
+      if (any_nan) sum = __int_as_float(0x7fffffff);
+      const float f = sum != 0.f ? rcp_fast(sum) : 0.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) acc[i] += valid ? q[i] * f : 0.f;
+    }
+  }
+  if constexpr (MEAN) {
+    // lanes that hold the same experts, then the block's warps, in a fixed order
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int o = 16; o >= L; o >>= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
+    }
+    __shared__ float cols[kRouteThreads / 32][kMaxExperts];
+    if (lane < L) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (i < sp.n) cols[threadIdx.x / 32][sp.e0 + i] = acc[i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < s.E; e += kRouteThreads) {
+      float v = 0.f;
+      for (int k = 0; k < kRouteThreads / 32; ++k) v += cols[k][e];
+      partials[static_cast<size_t>(blockIdx.x) * s.E + e] = v;
+    }
+  }
+}
+
+template <bool SIGMOID>
+cudaError_t launch_route_kind(int dtype, const RouteArgs& a, int num_sms, cudaStream_t st) {
+  const Split sp = split_of(a.E, a.K, a.G);
+  const Shape s = shape_of(dtype, a, a.logits, a.ld, sp);
+  const int blocks = route_blocks(a, sp, a.mean != nullptr ? kRouteParts : 16 * num_sms);
+  // A dependent launch hides the start of a large grid (8192 x 256: 14.3 us without, 11.5 with) and
+  // costs the host 0.7 us, which is what a small call takes longest.
+  return with_split(sp, [&](auto P, auto L) {
+    constexpr int p = decltype(P)::value, l = decltype(L)::value;
+    return launch_kernel(blocks >= num_sms, a.mean != nullptr ? route_kernel<p, l, SIGMOID, true> : route_kernel<p, l, SIGMOID, false>,
+                         blocks, kRouteThreads, 0, st, s, a.logits, a.bias, a.idx, a.w, a.partials);
+  });
+}
+
+}  // namespace
+
+}  // namespace bsmoe
