@@ -53,19 +53,39 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D K-major operand: rows x k_elems; box 128 (K) x box_rows.
-bool make_tmap(CUtensorMap* m, bool fp4, const void* base, uint64_t k_elems, uint64_t rows, uint32_t box_rows) {
+// Some kernel of the library: what binds the runtime's context to a thread (below).
+__global__ void wait_timeout_selftest_kernel(uint32_t* status);
+
+// cuTensorMapEncodeTiled. The runtime makes its context current on a host thread at the
+// thread's first call that needs one; encoding goes past the runtime, so a thread whose
+// first call it is has none yet: then a question about a kernel binds it (allowed while
+// a stream captures, nothing enqueued) and the map is encoded again.
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion l2) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
+  const cuuint32_t es[3] = {1, 1, 1};
+  auto encode = [&] {
+    return enc(m, type, rank, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, wait_timeout_selftest_kernel) != cudaSuccess) return false;
+    r = encode();
+  }
+  return r == CUDA_SUCCESS;
+}
+
+// 2-D K-major operand: rows x k_elems; box 128 (K) x box_rows.
+bool make_tmap(CUtensorMap* m, bool fp4, const void* base, uint64_t k_elems, uint64_t rows, uint32_t box_rows) {
   const cuuint64_t dims[2] = {k_elems, rows};
   const cuuint64_t strides[1] = {fp4 ? k_elems / 2 : k_elems};
   const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t es[2] = {1, 1};
-  const CUresult r = enc(m, fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                         const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode_map(m, fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                    const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace
@@ -75,27 +95,19 @@ bool byte_tmap(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t ro
 }
 
 bool scale_tmap(CUtensorMap* m, const void* base, uint64_t KB, uint64_t blocks, uint32_t box_blocks) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {128, KB, blocks};
   const cuuint64_t strides[2] = {512, KB * 512};
   const cuuint32_t box[3] = {128, 2, box_blocks};
-  const cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool store_tmap(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * 2};
   const cuuint32_t box[2] = {box_cols, box_rows};
-  const cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 namespace {
