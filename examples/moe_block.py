@@ -6,12 +6,13 @@ The block is norm -> router -> experts -> gated norm + residual, with a shared
 expert beside the routed ones at decode:
 
 * training (`TrainBlock`): bf16 experts as products over the sorted rows; the
-  sort, the rows' way there and back, both norms and their gradients are the
-  package's (sort_tokens, permute_tokens, unpermute_tokens, norm_before,
-  norm_after), through autograd;
+  router's choice, the sort, the rows' way there and back, both norms and their
+  gradients are the package's (route_tokens, sort_tokens, permute_tokens,
+  unpermute_tokens, norm_before, norm_after), through autograd;
 * decoding (`DecodeBlock`): FP4 experts by experts_forward, the shared expert by
   matvec on FP4 weights with the SwiGLU applied, norm_after with the next
-  block's norm in the same pass.
+  block's norm in the same pass; for a prompt (`prefill`) the shared expert by
+  matmul_fp4 on the same weights.
 """
 import os
 import sys
@@ -28,8 +29,7 @@ from block_scaled_moe_expert_gb300 import workloads as W  # noqa: E402
 
 def route(logits, k):
     """Top-k experts and softmax weights over them."""
-    top, idx = torch.topk(logits.float(), k, dim=1)
-    return idx.to(torch.int32), torch.softmax(top, dim=1)
+    return M.route_tokens(logits, k)
 
 
 class TrainBlock(torch.nn.Module):
@@ -74,9 +74,10 @@ class DecodeBlock:
         self.K = K
         self.experts = M.prepare_weights(W.make_weights(wl, "cuda"))
         shared = W.make_weights(W.scaled(wl, E=1, K=1, seed=seed + 1), "cuda")
-        self.shared_in = M.prepare_matvec(dict(fmt="fp4", N=2 * I, K=H, w=shared["w13"][0],
-                                               w_scale=shared["w13_scale"][0]), swiglu=True)
-        self.shared_out = M.prepare_matvec(dict(fmt="fp4", N=H, K=I, w=shared["w2"][0], w_scale=shared["w2_scale"][0]))
+        w_in = dict(fmt="fp4", N=2 * I, K=H, w=shared["w13"][0], w_scale=shared["w13_scale"][0])
+        w_out = dict(fmt="fp4", N=H, K=I, w=shared["w2"][0], w_scale=shared["w2_scale"][0])
+        self.shared_in, self.shared_out = M.prepare_matvec(w_in, swiglu=True), M.prepare_matvec(w_out)
+        self.prompt_in, self.prompt_out = M.prepare_matmul_fp4(w_in, swiglu=True), M.prepare_matmul_fp4(w_out)
         g = torch.Generator(device="cuda")
         g.manual_seed(seed + 2)
         self.router = (torch.randn(E, H, generator=g, device="cuda") * H ** -0.5).to(torch.bfloat16)
@@ -87,6 +88,14 @@ class DecodeBlock:
         idx, w = route(y @ self.router.t(), self.K)
         h = M.experts_forward(y, idx, w, self.experts)
         h += M.matvec(M.matvec(y, self.shared_in), self.shared_out)
+        return M.norm_after(x, h, self.norm_out, next_weight=self.norm_next)
+
+    def prefill(self, x):
+        """The same for the many tokens of a prompt, the shared expert's activations in FP4 too."""
+        y = M.norm_before(x, self.norm_in)
+        idx, w = route(y @ self.router.t(), self.K)
+        h = M.experts_forward(y, idx, w, self.experts)
+        h += M.matmul_fp4(M.matmul_fp4(y, self.prompt_in), self.prompt_out)
         return M.norm_after(x, h, self.norm_out, next_weight=self.norm_next)
 
 
@@ -108,12 +117,13 @@ def train(steps=5, T=512, H=256, I=128, E=8, K=2):
     return losses
 
 
-def decode(steps=4, T=4, H=512, I=256, E=16, K=2):
-    """The residual stream after a few passes through one block."""
+def decode(steps=4, T=4, H=512, I=256, E=16, K=2, prompt=64):
+    """The residual stream of the last T tokens of a prompt after it and a few passes through one block."""
     block = DecodeBlock(H, I, E, K)
     g = torch.Generator(device="cuda")
     g.manual_seed(8)
-    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    x = torch.randn(prompt, H, generator=g, device="cuda").to(torch.bfloat16)
+    x = block.prefill(x)[0][-T:]
     for _ in range(steps):
         x, y = block(x)
     return x, y
