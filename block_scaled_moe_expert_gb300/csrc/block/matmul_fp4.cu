@@ -565,8 +565,10 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
 }
 
 // Weights [N][K / 2] and scales [N][K / 32] to the kernel's rows: padded with
-// zeros to tiles of 256 and K blocks of 128; with swiglu in runs of 64 gate, 64 up.
-__global__ void __launch_bounds__(256) matmul_prepare_kernel(MatmulShape s, int KB, const uint8_t* __restrict__ codes,
+// zeros to tiles of 256 and K blocks of 128; with swiglu in runs of 64 gate, 64 up. K / 2 is
+// a multiple of 16: rows are whole 16-byte loads where the codes start at one.
+__global__ void __launch_bounds__(128) matmul_prepare_kernel(MatmulShape s, int KB, bool packs,
+                                                             const uint8_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ scale, uint8_t* __restrict__ out,
                                                              uint32_t* __restrict__ sf) {
   const int p = blockIdx.x;  // prepared row
@@ -577,15 +579,23 @@ __global__ void __launch_bounds__(256) matmul_prepare_kernel(MatmulShape s, int 
   }
   const bool have = src < s.N;
   const int bytes = s.K / 2;
-  for (int i = threadIdx.x * 4; i < KB * 64; i += 256 * 4) {
-    uint32_t w = 0;
-    if (have && i < bytes) {  // K / 2 is a multiple of 16
+  const uint8_t* from = codes + static_cast<size_t>(src) * bytes;
+  uint8_t* to = out + static_cast<size_t>(p) * KB * 64;
+  for (int i = threadIdx.x * 16; i < KB * 64; i += 128 * 16) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (have && i < bytes) {
+      if (packs) {
+        v = *reinterpret_cast<const uint4*>(from + i);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(codes[static_cast<size_t>(src) * bytes + i + j]) << (8 * j);
+        for (int j = 0; j < 16; ++j) w[j / 4] |= static_cast<uint32_t>(from[i + j]) << (8 * (j % 4));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(p) * KB * 64 + i) = w;
+    *reinterpret_cast<uint4*>(to + i) = v;
   }
-  for (int b = threadIdx.x; b < KB; b += 256) {
+  for (int b = threadIdx.x; b < KB; b += 128) {
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -622,7 +632,7 @@ cudaError_t launch_matmul_prepare(const MatmulShape& s, const void* codes, const
                                   cudaStream_t st) {
   const MatmulLayout l = matmul_layout(s);
   uint8_t* p = static_cast<uint8_t*>(prepared);
-  return launch_kernel(false, matmul_prepare_kernel, l.NT * kMmN, 256, 0, st, s, l.KB,
+  return launch_kernel(false, matmul_prepare_kernel, l.NT * kMmN, 128, 0, st, s, l.KB, aligned16(codes),
                        static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scale), p,
                        reinterpret_cast<uint32_t*>(p + l.codes_bytes));
 }

@@ -15,8 +15,13 @@
 // with 256 sigmoid scores of normal logits and a bias one in 270 took the first way (for its
 // groups one in 3000), none the second.
 //
-// Bounds: the logits are read once, 2 or 4 bytes for some 15 instructions a logit and
-// 25 a choice: instruction issue for large batches, launch latency for small ones.
+// Bounds: the logits are read once, 2 or 4 bytes for some 10 instructions a logit and 20 a
+// choice, most of them comparisons, selections and whole-number ones: instruction issue for
+// large batches (issue slots 68% busy, memory at a fifth of its rate), the launch for small
+// ones. 65536 x 256 fp32: one expert by sigmoid 33 us, eight with a bias 48, in groups 60
+// (67 MB: 10 us at the memory's rate); 8192 x 256 in groups 10; 16384 x 128 bf16 with mean
+// scores 10.6; 4 tokens 3.2. Registers for 7 blocks per SM: with 6, 7, 8 and 10 blocks the 8192
+// tokens took 11.3, 10.0, 11.4 and 12.4 us.
 #pragma once
 #include "router_common.cuh"
 
@@ -446,9 +451,9 @@ __device__ __forceinline__ float head_sum(float v, int width) {
 }
 
 template <int P, int L, bool SIGMOID, bool MEAN>
-__global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shape s, const void* __restrict__ logits,
-                                                              const float* __restrict__ bias, int32_t* __restrict__ idx,
-                                                              float* __restrict__ w, float* __restrict__ partials) {
+__global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
+    route_kernel(Shape s, const void* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ idx,
+                 float* __restrict__ w, float* __restrict__ partials) {
   constexpr int kTokens = kRouteThreads / L;  // a block at a time
   constexpr float kCut = P * 0x1p-22f;        // of a key: the cut bits, and its own rounding
   const int lane = threadIdx.x & 31, sub = lane % L, first = lane - sub;
@@ -459,7 +464,10 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shap
   const bool check = by_score || s.dtype == MOE_FP32;
   const int rounds = s.K + (check && s.K < s.E ? 1 : 0);
   const int width = s.K > 1 ? 2 << (31 - __clz(s.K - 1)) : 1;
-  const bool vec_bias = bias != nullptr && s.vec_bias;
+  const bool vec_bias = s.vec_bias;
+  __shared__ uint2 slots[kTokens][L + 1];  // keys in the order they are taken, and where their lane starts
+  uint2* taken = slots[threadIdx.x / L];
+  const unsigned below = ((1u << lane) - 1u) & ~((1u << first) - 1u);  // lower lanes of the token
   float acc[MEAN ? P : 1];
   if constexpr (MEAN) {
 #pragma unroll
@@ -486,11 +494,26 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shap
     } else {
       load_logits<P>(s, logits, tr, sp, x);
     }
-    bool nan = false;
+    // Comparisons, selections and whole numbers share a pipe of half the rate, which is
+    // what the kernel is bound by; so whether any logit or bias of the warp's tokens needs
+    // a second look (infinite, NaN, behind the last expert) is a sum, 0 if none does.
+    float v[P], look = 0.f;
+    if (bias != nullptr) load_as<P, float>(bias, sp.e0, sp.n, vec_bias, v);
 #pragma unroll
-    for (int i = 0; i < P; ++i) nan |= x[i] != x[i];
-    unsigned any_nan = __ballot_sync(kFull, nan);
-    if (L < 32) any_nan = (any_nan >> first) & ((1u << (L & 31)) - 1u);
+    for (int i = 0; i < P; ++i) look = fmaf(x[i], 0.f, look);
+    if (bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) look = fmaf(v[i], 0.f, look);
+    }
+    const bool plain = __all_sync(kFull, look == 0.f);
+    unsigned any_nan = 0;
+    if (!plain) {
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < P; ++i) nan |= x[i] != x[i];
+      any_nan = __ballot_sync(kFull, nan);
+      if (L < 32) any_nan = (any_nan >> first) & ((1u << (L & 31)) - 1u);
+    }
     Row row = {neg_inf(), 1.f};
     if (softmax_sum) {
 #pragma unroll
@@ -499,7 +522,8 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shap
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        q[i] = x[i] > neg_inf() ? exp_fast(x[i] - row.most) : 0.f;
+        q[i] = exp_fast(x[i] - row.most);
+        if (!plain) q[i] = x[i] > neg_inf() ? q[i] : 0.f;
         sum += q[i];
       }
       row.sum = lane_sum<L>(sum);
@@ -508,17 +532,22 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shap
       for (int i = 0; i < P; ++i) q[i] = sigmoid_fast(x[i]);
     }
     uint32_t key[P];
-    {
-      float v[P];
-      const float inv = by_score && !SIGMOID ? rcp_fast(row.sum) : 1.f;
+    const float inv = SIGMOID ? 1.f : rcp_fast(row.sum);
+    if (bias != nullptr) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = by_score ? q[i] * inv : x[i];
-      if (bias != nullptr) add_bias<P>(bias, sp, vec_bias, v);
+      for (int i = 0; i < P; ++i) v[i] = fmaf(q[i], inv, v[i]);
+    } else if (by_score) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const bool ok = x[i] > neg_inf() && v[i] > neg_inf();  // -inf behind the lane's last
-        key[i] = ok ? (ordered(v[i] + 0.f) & ~static_cast<uint32_t>(P - 1)) | (P - 1 - i) : 0u;
-      }
+      for (int i = 0; i < P; ++i) v[i] = q[i] * inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = x[i] + 0.f;  // -0 and 0 are one value
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = (ordered(v[i]) & ~static_cast<uint32_t>(P - 1)) | (P - 1 - i);
+    if (!plain) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) key[i] = x[i] > neg_inf() && v[i] > neg_inf() ? key[i] : 0u;
     }
     sort_keys<P>(key);
     const float slack = by_score ? score_slack<SIGMOID>(row) : 0.f;
@@ -543,8 +572,8 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shap
       bool in = rank < s.top_groups && g < s.G;
       if (check && s.top_groups < s.G) {
         const float err = 2.f * slack + kCut * (fabsf(va) + fabsf(vb));
-        const float worst = -lane_max<L>(in ? err - value : neg_inf());
-        const float best = lane_max<L>(in || g >= s.G ? neg_inf() : value + err);
+        const float worst = -unordered(lane_max_u32<L>(ordered(in ? err - value : neg_inf())));
+        const float best = unordered(lane_max_u32<L>(ordered(in || g >= s.G ? neg_inf() : value + err)));
         if (worst <= best) {  // the token's lanes are the warp's: all agree
           int settled_in = -1;
           if (by_score)
@@ -557,54 +586,39 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shap
 #pragma unroll
       for (int i = 0; i < P; ++i) key[i] = in ? key[i] : 0u;
     }
-    // lane k keeps the k-th key and the lane that had it; `next`: the one behind the last lane's
-    uint32_t mine = 0, next = 0;
-    int from_k = lane, from_next = lane;
+    // The lane of the best key left writes it down and moves up; between lanes the places
+    // do not count: equal keys go to the lowest lane.
     for (int k = 0; k < rounds; ++k) {
-      // between lanes the places do not count: equal keys go to the lowest lane
       const uint32_t head = key[0] & ~static_cast<uint32_t>(P - 1);
-      const int from = first_lane<L>(head == lane_max_u32<L>(head), first);
-      const uint32_t top = __shfl_sync(kFull, key[0], from);
-      if (k == sub) {
-        mine = top;
-        from_k = from;
-      }
-      if (k == L) {
-        next = top;
-        from_next = from;
-      }
-      if (lane == from) {
+      const bool best = head == lane_max_u32<L>(head);
+      const unsigned who = __ballot_sync(kFull, best);
+      if (best && (who & below) == 0) {
+        taken[k] = make_uint2(key[0], sp.e0 + P - 1);
 #pragma unroll
         for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1];
         key[P - 1] = 0u;
       }
     }
-    const int place = P - 1 - static_cast<int>(mine & (P - 1));
-    int e = __shfl_sync(kFull, sp.e0, from_k) + place;
-    if (mine == 0) e = -1;
+    __syncwarp();
+    // lane k: the k-th choice and the one behind it
+    auto expert = [&](uint2 t) { return t.x != 0 ? static_cast<int>(t.y) - static_cast<int>(t.x & (P - 1)) : -1; };
+    const uint2 mine = sub < rounds ? taken[sub] : make_uint2(0, 0);
+    const uint2 after = sub + 1 < rounds ? taken[sub + 1] : make_uint2(0, 0);
+    int e = expert(mine);
     float xe = e >= 0 ? logit_at(s, logits, tr * s.ld + e) : neg_inf();
     if (check) {
-      const float be = e >= 0 && bias != nullptr ? __ldg(bias + e) : 0.f;
-      // the neighbour behind: the next lane's, or the extra one
-      uint32_t after = __shfl_sync(kFull, mine, (lane + 1) & 31);
-      float xa = __shfl_sync(kFull, xe, (lane + 1) & 31), ba = __shfl_sync(kFull, be, (lane + 1) & 31);
-      const int ea = __shfl_sync(kFull, sp.e0, from_next) + P - 1 - static_cast<int>(next & (P - 1));
-      if (sub == L - 1) {
-        after = next;
-        if (next != 0) {
-          xa = logit_at(s, logits, tr * s.ld + ea);
-          ba = bias != nullptr ? __ldg(bias + ea) : 0.f;
-        }
+      if (sub < s.K && mine.x != 0 && after.x != 0) {
+        const float a = unordered(mine.x & ~static_cast<uint32_t>(P - 1)), b = unordered(after.x & ~static_cast<uint32_t>(P - 1));
+        unsure |= a - b <= (by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f);
       }
-      if (sub < s.K && sub + 1 < rounds && mine != 0 && after != 0) {
-        const float a = unordered(mine & ~static_cast<uint32_t>(P - 1)), b = unordered(after & ~static_cast<uint32_t>(P - 1));
-        const float err = by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f;
-        unsure |= a - b <= err && !(xe == xa && be == ba);
+      if (__any_sync(kFull, unsure) && unsure) {  // the same inputs are the same key
+        const int ea = expert(after);
+        unsure = !(xe == logit_at(s, logits, tr * s.ld + ea) && (bias == nullptr || __ldg(bias + e) == __ldg(bias + ea)));
       }
       if (__any_sync(kFull, unsure || exact)) {
         // candidates: the K + 1 that the lanes hold, if the next one is surely none
         const uint32_t head = lane_max_u32<L>(key[0]);
-        const uint32_t kth = __shfl_sync(kFull, mine, first + s.K - 1);
+        const uint32_t kth = taken[s.K - 1].x;
         if (head != 0 && s.K < L) {
           const float a = unordered(kth & ~static_cast<uint32_t>(P - 1)), b = unordered(head & ~static_cast<uint32_t>(P - 1));
           exact |= a - b <= (by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f);
@@ -633,17 +647,18 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 8) route_kernel(Shap
             sum = low_sum;
           }
         }
-        score = have ? score / sum : 0.f;
+        score = have ? __fdividef(score, sum) : 0.f;
       }
       weight = score * s.scale;
     } else if (s.renorm) {
       const float most = head_max(have ? xe : neg_inf(), width);
       const float score = have ? expf(xe - most) : 0.f;
       const float sum = head_sum(score, width);
-      weight = have ? score / sum * s.scale : 0.f;
+      weight = have ? __fdividef(score, sum) * s.scale : 0.f;
     } else {
-      weight = have ? expf(xe - row.most) / row.sum * s.scale : 0.f;
+      weight = have ? __fdividef(expf(xe - row.most), row.sum) * s.scale : 0.f;
     }
+    __syncwarp();  // `taken` has been read
     if (any_nan) weight = __int_as_float(0x7fffffff);
     if (valid && sub < s.K) {
       idx[t * s.K + sub] = e;

@@ -192,3 +192,19 @@ def test_offsets_that_pass_32_bits():
     x = C.randn(g, 17000, 64, dtype=torch.bfloat16)
     y = M.matmul_fp4(x, prepared)
     assert torch.equal(y[-200:], M.matmul_fp4(x[-200:], prepared))
+
+
+def test_weights_at_any_address():
+    """Checkpoint bytes that start at no 16-byte boundary prepare to the same bytes."""
+    g = C.gen(11)
+    for swiglu in (False, True):
+        weights = weights_of(g, 130, 352)
+        want = M.prepare_matmul_fp4(weights, swiglu=swiglu)
+        for lead in (1, 8):
+            moved = dict(weights)
+            for name in ("w", "w_scale"):
+                flat = torch.zeros(weights[name].numel() + lead, dtype=torch.uint8, device="cuda")
+                flat[lead:] = weights[name].reshape(-1)
+                moved[name] = flat[lead:].view(weights[name].shape)
+            got = M.prepare_matmul_fp4(moved, swiglu=swiglu)
+            assert torch.equal(got.prepared, want.prepared)
