@@ -13,7 +13,9 @@
 // of each CTA keeps five stages in flight (TMA tiles of codes and scale words, all counted on
 // the leader's barriers), warp 1 of the leader issues the products of both, warps 4..11
 // move the accumulators to registers, hand tensor memory back and store while the next
-// tile is multiplied.
+// tile is multiplied. 8192 x 4096 x 7168: 68 to 70 us, 6.9 PFLOP/s, the tensor pipe 72% busy;
+// 8192 x 7168 x 2048: 45 us. What is left: a tile's drain before the next begins (9 us of the 70),
+// copies (5), the rest products and scale copies.
 #include <cuda.h>
 
 #include "fp4.cuh"
@@ -295,7 +297,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) matmul_fp4_kernel(const __grid_
 // of their share of the tokens in rank order over distributed shared memory:
 // no atomics, the same bits every time. Two CTAs per SM, all stages of weights
 // in flight before the quantizing kernel in front has finished. Bound by the
-// weights' bytes.
+// weights' bytes: 28671 x 4096 (62 MB) in 13.5 us with one token, 13.8 with 16, 15.8 with 64 and
+// 19.3 with 128; small ones by a chain of latencies: 4096 x 7168 with one token 6.2 us, 2880 x 2880
+// 4.4 (a call among others, quantization included).
 constexpr int kStThreads = 192;
 // Up to so many tokens the kernel quantizes the activations itself, every CTA those of its
 // part of K: one launch, and no way through memory.

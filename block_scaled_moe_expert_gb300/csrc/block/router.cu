@@ -2,7 +2,9 @@
 //
 // The gradient reads a token's logits once where every expert has a part (mean scores, or
 // softmax weights that are not renormalised) and only the chosen ones' otherwise; it
-// writes a row of d_logits, the chosen experts' elements last. Bound like the forward.
+// writes a row of d_logits, the chosen experts' elements last. Bound like the forward:
+// 65536 x 256 fp32, K = 8: 36 us, with mean scores 45; 16384 x 128 bf16, K = 4, with mean
+// scores 6.4 (8.9 MB).
 #include "router_common.cuh"
 
 namespace bsmoe {

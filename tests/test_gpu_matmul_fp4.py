@@ -208,3 +208,14 @@ def test_weights_at_any_address():
                 moved[name] = flat[lead:].view(weights[name].shape)
             got = M.prepare_matmul_fp4(moved, swiglu=swiglu)
             assert torch.equal(got.prepared, want.prepared)
+
+
+def test_bits_of_a_row_in_batches_of_other_sizes():
+    """The sums' order goes by the way a batch takes (up to 8, up to 128, more tokens), not by its size."""
+    g = C.gen(12)
+    for N, K in ((4096, 2048), (300, 4128), (20000, 512)):
+        prepared = M.prepare_matmul_fp4(weights_of(g, N, K))
+        x = C.randn(g, 520, K, dtype=torch.bfloat16)
+        for sizes in ((1, 2, 8), (9, 16, 17, 40, 65, 128), (129, 256, 257, 520)):
+            rows = [M.matmul_fp4(x[:T], prepared)[0] for T in sizes]
+            assert all(torch.equal(r, rows[0]) for r in rows)
