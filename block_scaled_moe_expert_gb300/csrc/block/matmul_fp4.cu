@@ -70,11 +70,11 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int64_t
   }
 }
 
-// silu(g) * u after the optional clamp.
+// silu(g) * u after the optional clamp, which leaves a NaN one.
 __device__ __forceinline__ float swiglu_of(float g, float u, bool clamp, float limit) {
   if (clamp) {
-    g = fminf(g, limit);
-    u = fminf(fmaxf(u, -limit), limit);
+    g = g > limit ? limit : g;
+    u = u > limit ? limit : u < -limit ? -limit : u;
   }
   return __fdividef(g, 1.f + __expf(-g)) * u;
 }
@@ -393,7 +393,6 @@ __device__ __forceinline__ void quantize_stages(Smem& sm, const MmArgs& a, int k
     const int k = (k0 + i) * 256;
     next = i < n && t < a.T && k + c * kUnit < a.K ? load_unit(x + k, a.how) : zero_unit<T>();
   };
-  pdl_wait();
   load(0);
   int stage = 0;
   uint32_t phase = 0;
@@ -491,6 +490,7 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
     }
     if (!ok && lane == 0) drain_copies(sm.full, kStages, issued);
   } else if (warp == 1) {
+    pdl_wait();  // the bounded waits begin when the kernel in front has ended
     const uint64_t a0 = smem_desc(smem_u32(sm.a[0]), 16, 1024, kSwizzle128B);
     const uint64_t b0 = smem_desc(smem_u32(sm.b[0]), 16, 1024, kSwizzle128B);
     const uint64_t sfa0 = smem_desc(smem_u32(sm.sfa[0]), 0, 128, kSwizzleNone);
@@ -523,6 +523,7 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
     }
     if (ok && elect_one()) mma_commit(&sm.tfull);
   } else if (warp >= 2) {
+    pdl_wait();
     if constexpr (OWN) quantize_stages<T, kStages>(sm, a, k0, n, abort_flag);
     const int quarter = warp & 3, m = quarter * 32 + lane;
     const int count = min(N, a.T - tt * N);  // tokens of the tile
@@ -662,9 +663,9 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int threads, int 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int N, bool OWN>
+template <typename T, int N, bool OWN, typename F>
 cudaError_t launch_stream(const MatmulLayout& l, const uint8_t* prepared, const uint8_t* codes, MmArgs a, int num_sms,
-                          cudaStream_t st) {
+                          cudaStream_t st, F&& quantize) {
   CUtensorMap tw, tx = {};
   const uint64_t row = static_cast<uint64_t>(l.KB) * 64;
   if (!byte_tmap(&tw, prepared, row, static_cast<uint64_t>(l.NT) * kMmN, kMmM) ||
@@ -679,19 +680,20 @@ cudaError_t launch_stream(const MatmulLayout& l, const uint8_t* prepared, const 
   while (S < 8 && units * S * 2 <= (OWN ? 2 : 1) * num_sms && KS >= 4 * S) S *= 2;
   auto* kernel = matmul_fp4_stream_kernel<T, N, OWN>;
   const size_t smem = sizeof(StSmem<N>) + 1024;
-  const cudaError_t e = allow_smem(kernel, smem);
+  cudaError_t e = allow_smem(kernel, smem);
+  if (e == cudaSuccess && !OWN) e = quantize();
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, units * S, kStThreads, S, smem, st, tw, tx, a, S);
 }
 
-template <typename T>
+template <typename T, typename F>
 cudaError_t launch_stream(const MatmulLayout& l, const uint8_t* prepared, const uint8_t* codes, const MmArgs& a,
-                          int num_sms, cudaStream_t st) {
-  return a.T <= kOwnTokens ? launch_stream<T, 16, true>(l, prepared, codes, a, num_sms, st)
-         : a.T <= 16 ? launch_stream<T, 16, false>(l, prepared, codes, a, num_sms, st)
-         : a.T <= 32 ? launch_stream<T, 32, false>(l, prepared, codes, a, num_sms, st)
-         : a.T <= 64 ? launch_stream<T, 64, false>(l, prepared, codes, a, num_sms, st)
-                     : launch_stream<T, 128, false>(l, prepared, codes, a, num_sms, st);
+                          int num_sms, cudaStream_t st, F&& quantize) {
+  return a.T <= kOwnTokens ? launch_stream<T, 16, true>(l, prepared, codes, a, num_sms, st, quantize)
+         : a.T <= 16 ? launch_stream<T, 16, false>(l, prepared, codes, a, num_sms, st, quantize)
+         : a.T <= 32 ? launch_stream<T, 32, false>(l, prepared, codes, a, num_sms, st, quantize)
+         : a.T <= 64 ? launch_stream<T, 64, false>(l, prepared, codes, a, num_sms, st, quantize)
+                     : launch_stream<T, 128, false>(l, prepared, codes, a, num_sms, st, quantize);
 }
 
 }  // namespace
@@ -704,14 +706,13 @@ cudaError_t launch_matmul_fp4(const MatmulShape& s, float limit, const void* pre
   MmArgs a = {ws + w.sf, p + l.codes_bytes, reinterpret_cast<uint32_t*>(ws), y, T, s.swiglu ? s.N / 2 : s.N,
               l.KB, ceil_div(T, kMmM), l.NT, s.swiglu, limit, false, x, ld, s.K, how_aligned(x, ld, 2)};
   a.packs = aligned16(y) && a.N % 8 == 0;
-  if (T > kOwnTokens) {
-    const cudaError_t e = launch_quantize_act(dtype, x, ld, T, s.K, ws + w.codes, reinterpret_cast<uint32_t*>(ws + w.sf),
-                                              a.status, st);
-    if (e != cudaSuccess) return e;
-  }
+  // enqueued when nothing is left that could refuse the product
+  auto quantize = [&] {
+    return launch_quantize_act(dtype, x, ld, T, s.K, ws + w.codes, reinterpret_cast<uint32_t*>(ws + w.sf), a.status, st);
+  };
   if (T <= kStreamTokens)
-    return dtype == MOE_BF16 ? launch_stream<__nv_bfloat16>(l, p, ws + w.codes, a, num_sms, st)
-                             : launch_stream<__half>(l, p, ws + w.codes, a, num_sms, st);
+    return dtype == MOE_BF16 ? launch_stream<__nv_bfloat16>(l, p, ws + w.codes, a, num_sms, st, quantize)
+                             : launch_stream<__half>(l, p, ws + w.codes, a, num_sms, st, quantize);
   a.MT = ceil_div(T, 2 * kMmM);
   CUtensorMap ta, tb, tsa, tsb, ty = {};
   if (!byte_tmap(&ta, ws + w.codes, static_cast<uint64_t>(l.KB) * 64, T, kMmM) ||
@@ -722,7 +723,8 @@ cudaError_t launch_matmul_fp4(const MatmulShape& s, float limit, const void* pre
   const size_t smem = sizeof(MmSmem) + 1024;
   const int pairs = num_sms / 2, tiles = a.MT * a.NT;
   auto run = [&](auto* kernel) {
-    const cudaError_t e = allow_smem(kernel, smem);
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e == cudaSuccess) e = quantize();
     if (e != cudaSuccess) return e;
     return launch_cluster(kernel, 2 * (tiles < pairs ? tiles : pairs), kMmThreads, 2, smem, st, ta, tb, tsa, tsb, ty, a);
   };

@@ -219,3 +219,17 @@ def test_bits_of_a_row_in_batches_of_other_sizes():
         for sizes in ((1, 2, 8), (9, 16, 17, 40, 65, 128), (129, 256, 257, 520)):
             rows = [M.matmul_fp4(x[:T], prepared)[0] for T in sizes]
             assert all(torch.equal(r, rows[0]) for r in rows)
+
+
+def test_a_clamp_leaves_nan():
+    g = C.gen(13)
+    weights = weights_of(g, 64, 128)
+    weights["w_scale"][5, 1] = weights["w_scale"][32 + 9, 0] = 255  # a gate's row, an up's row
+    prepared = M.prepare_matmul_fp4(weights, swiglu=True)
+    for T in (3, 30, 150):
+        x = C.randn(g, T, 128, dtype=torch.bfloat16)
+        x[1] = float("nan")
+        y = M.matmul_fp4(x, prepared, swiglu_limit=2.0)
+        bad = torch.zeros(T, 32, dtype=torch.bool, device="cuda")
+        bad[1] = bad[:, 5] = bad[:, 9] = True
+        assert torch.equal(y.isnan(), bad)
