@@ -325,7 +325,8 @@ __device__ __forceinline__ uint64_t packed(Two v) {
 __device__ __forceinline__ Two unpacked(uint64_t k) {
   return {unordered(static_cast<uint32_t>(k >> 32)), unordered(static_cast<uint32_t>(k))};
 }
-// Whether pairs of floats settle the order of two keys.
+// Whether pairs of floats settle the order of two keys that differ (the same pair is a tie:
+// the same inputs give it, and others only where 64 bits would hardly tell them apart).
 __device__ __forceinline__ bool settled(Two a, Two b) {
   return fabsf((a.hi - b.hi) + (a.lo - b.lo)) > 0x1p-40f * (fabsf(a.hi) + fabsf(b.hi));
 }
@@ -385,10 +386,9 @@ __device__ __noinline__ int order_candidates(Shape s, const void* logits, int64_
   for (int j = 0; j <= s.K; ++j) {
     const uint64_t kj = __shfl_sync(kFull, key, first + j);
     const int ej = __shfl_sync(kFull, e, first + j);
-    const float xj = __shfl_sync(kFull, x, first + j), bj = __shfl_sync(kFull, b, first + j);
     if (j != sub && have && ej >= 0) {
       rank += kj > key || (kj == key && ej < e);
-      if (bias != nullptr && !(xj == x && bj == b) && !settled(unpacked(kj), unpacked(key))) ok = false;
+      if (bias != nullptr && kj != key && !settled(unpacked(kj), unpacked(key))) ok = false;
     } else if (j != sub && !have && (ej >= 0 || j < sub)) {
       ++rank;
     }
@@ -435,7 +435,7 @@ __device__ __noinline__ int rank_groups(Shape s, const void* logits, int64_t t, 
   for (int j = 0; j < s.G; ++j) {
     const uint64_t v = __shfl_sync(kFull, value, j << s.lanes_log2);
     rank += v > value || (v == value && j < g);
-    if (g < s.G && j != g && v != 0 && value != 0 && !settled(unpacked(v), unpacked(value))) ok = false;
+    if (g < s.G && j != g && v != 0 && value != 0 && v != value && !settled(unpacked(v), unpacked(value))) ok = false;
   }
   return __all_sync(kFull, ok) ? (rank < s.top_groups && g < s.G) : -1;
 }

@@ -278,3 +278,17 @@ def test_captured_and_repeated_calls_give_the_same_bits():
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(got, call()))
     x.copy_(keep)
+
+
+def test_tied_groups():
+    """Routers of zeros and of a few values: groups and experts that tie exactly, in every kind of call."""
+    g = C.gen(24)
+    for x in (torch.zeros(700, 64, device="cuda"), torch.randint(-1, 2, (700, 64), generator=g, device="cuda").float(),
+              torch.randint(0, 2, (700, 64), generator=g, device="cuda").float() * 0.25):
+        bias = torch.randint(0, 3, (64,), generator=g, device="cuda").float() * 0.125
+        for dtype in (torch.float32, torch.bfloat16):
+            for b in (None, torch.zeros_like(bias), bias):
+                for score in ("softmax", "sigmoid"):
+                    for group_score in ("top2", "max"):
+                        check(x.to(dtype), 6, score, b, 8, 3, group_score, mean=False)
+                    check(x.to(dtype), 6, score, b, mean=False)
