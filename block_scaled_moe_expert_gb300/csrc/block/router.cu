@@ -186,6 +186,7 @@ cudaError_t launch_route_tokens(int dtype, const RouteArgs& a, int num_sms, cuda
   }
   if (a.mean == nullptr) return cudaSuccess;
   const int blocks = route_blocks(a, split_of(a.E, a.K, a.G), kRouteParts);
+  if (blocks == 1) return cudaSuccess;  // written by the block itself
   return launch_kernel(true, route_mean_kernel, ceil_div(a.E, 8), 256, 0, st, static_cast<const float*>(a.partials),
                        blocks, a.E, static_cast<float>(a.T), a.mean);
 }

@@ -709,7 +709,8 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
     for (int e = threadIdx.x; e < s.E; e += kRouteThreads) {
       float v = 0.f;
       for (int k = 0; k < kRouteThreads / 32; ++k) v += cols[k][e];
-      partials[static_cast<size_t>(blockIdx.x) * s.E + e] = v;
+      // one block's columns are the means already
+      partials[static_cast<size_t>(blockIdx.x) * s.E + e] = gridDim.x == 1 ? v / static_cast<float>(s.T) : v;
     }
   }
 }
@@ -724,7 +725,8 @@ cudaError_t launch_route_kind(int dtype, const RouteArgs& a, int num_sms, cudaSt
   return with_split(sp, [&](auto P, auto L) {
     constexpr int p = decltype(P)::value, l = decltype(L)::value;
     return launch_kernel(blocks >= num_sms, a.mean != nullptr ? route_kernel<p, l, SIGMOID, true> : route_kernel<p, l, SIGMOID, false>,
-                         blocks, kRouteThreads, 0, st, s, a.logits, a.bias, a.idx, a.w, a.partials);
+                         blocks, kRouteThreads, 0, st, s, a.logits, a.bias, a.idx, a.w,
+                         blocks == 1 ? a.mean : a.partials);
   });
 }
 
