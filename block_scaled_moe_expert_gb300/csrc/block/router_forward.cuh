@@ -23,6 +23,8 @@
 // scores 10.6; 4 tokens 3.2. Registers for 7 blocks per SM: with 6, 7, 8 and 10 blocks the 8192
 // tokens took 11.3, 10.0, 11.4 and 12.4 us.
 #pragma once
+#include <cfloat>
+
 #include "router_common.cuh"
 
 namespace bsmoe {
@@ -562,7 +564,8 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
       }
       const float va = a != 0 ? unordered(a & ~static_cast<uint32_t>(P - 1)) : neg_inf();
       const float vb = s.group_max || b == 0 ? 0.f : unordered(b & ~static_cast<uint32_t>(P - 1));
-      const float value = va + vb;
+      // below every other value without an expert, not below the type's range with some
+      const float value = a != 0 ? fmaxf(va + vb, -FLT_MAX) : neg_inf();
       const int g = sub >> s.lanes_log2;
       int rank = 0;
       for (int j = 0; j < s.G; ++j) {
@@ -571,9 +574,11 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
       }
       bool in = rank < s.top_groups && g < s.G;
       if (check && s.top_groups < s.G) {
-        const float err = 2.f * slack + kCut * (fabsf(va) + fabsf(vb));
-        const float worst = -unordered(lane_max_u32<L>(ordered(in ? err - value : neg_inf())));
-        const float best = unordered(lane_max_u32<L>(ordered(in || g >= s.G ? neg_inf() : value + err)));
+        // of a value; an infinite one is itself, and a group without an expert is near no other
+        const float err = fabsf(value) < INFINITY ? 2.f * slack + kCut * (fabsf(va) + fabsf(vb)) : 0.f;
+        const bool some = a != 0;
+        const float worst = -unordered(lane_max_u32<L>(ordered(in && some ? err - value : neg_inf())));
+        const float best = unordered(lane_max_u32<L>(ordered(!in && some && g < s.G ? value + err : neg_inf())));
         if (worst <= best) {  // the token's lanes are the warp's: all agree
           int settled_in = -1;
           if (by_score)

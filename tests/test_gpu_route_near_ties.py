@@ -1,0 +1,93 @@
+"""GPU: routing where groups have no available expert or an infinite value, and
+near ties between the others, against the 64-bit oracle."""
+import math
+
+import pytest
+import torch
+
+import block_scaled_moe_expert_gb300 as M
+from oracle import block as O
+from tests import block_cases as C
+from tests.test_gpu_route_tokens import check, logits_of
+
+pytestmark = pytest.mark.gpu
+
+STEP = 1.0 + 2.0 ** -23
+
+
+def near_ties(seed, T, E, groups, score, shut=()):
+    """Logits and a bias that cancels the scores: the groups' two best within a few fp32 steps of all the others',
+    the rest of a group in clear steps below. shut: experts with logits of -inf."""
+    x, _ = logits_of(seed, 1, E)
+    x[:, list(shut)] = -math.inf
+    below = torch.arange(E, device="cuda") % (E // groups) // 2
+    bias = (0.75 - O.scores(x, score)[0][0] - 0.01 * below).float()
+    return x + 1e-6 * C.randn(C.gen(seed + 1), T, E), bias
+
+
+SHAPES = [(256, 8, 4), (64, 4, 2), (96, 3, 1), (32, 16, 5), (512, 16, 12)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["top2", "max"])
+@pytest.mark.parametrize("E,groups,top_groups", SHAPES)
+def test_near_ties_beside_masked_groups(E, groups, top_groups, score, group_score):
+    size, K = E // groups, 2 * top_groups
+    for shut in ([groups - 1], [0], list(range(0, groups, 4))[: groups - top_groups - 1]):
+        experts = [g * size + i for g in shut for i in range(size)]
+        x, bias = near_ties(E + groups, 3000, E, groups, score, experts)
+        check(x, K, score, bias, groups, top_groups, group_score, mean=False)
+        x, bias = near_ties(E + groups, 3000, E, groups, score)
+        for low in (-math.inf, torch.finfo(torch.float32).min):
+            closed = bias.clone()
+            closed[experts] = low
+            check(x, K, score, closed, groups, top_groups, group_score, mean=False)
+
+
+def test_groups_of_the_lowest_bias_come_before_masked_ones():
+    """Sums of two biases of the type's lowest value pass its range; such groups are available all the same."""
+    low = torch.finfo(torch.float32).min
+    x, _ = logits_of(3, 50, 64)
+    for score in ("softmax", "sigmoid"):
+        for masked in ((0, 1), (5, 2), (0, 7)):
+            bias = torch.full((64,), low, device="cuda")
+            bias[24:32] = 0.0
+            for g in masked:
+                bias[8 * g:8 * g + 8] = -math.inf
+            for top_groups in (2, 3, 6, 7):
+                check(x, 8, score, bias, 8, top_groups, "top2", mean=False)
+
+
+def test_neighbouring_logits_beside_a_masked_group():
+    """Maxima of two groups one fp32 step apart, the lower group's index the lower one."""
+    x = torch.full((4, 32), -1.0, device="cuda")
+    x[:, 3], x[:, 9] = 1.0, STEP
+    x[1, 24:] = -math.inf
+    x[2, 16:] = -math.inf
+    x[3, 31] = -math.inf
+    for score in ("softmax", "sigmoid"):
+        assert check(x, 1, score, None, 4, 1, "max", mean=False)[0].tolist() == [[9]] * 4
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["top2", "max"])
+def test_near_ties_beside_an_infinite_group(score, group_score):
+    """A bias of +inf takes its expert's group first; the rest is as near as before."""
+    for E, groups, top_groups in SHAPES:
+        x, bias = near_ties(E, 3000, E, groups, score)
+        for first in ([5], [5, E - 1], [5, 6, E - 1]):
+            b = bias.clone()
+            b[first] = math.inf
+            check(x, 2 * top_groups, score, b, groups, top_groups, group_score, mean=False)
+
+
+def test_neighbouring_logits_beside_an_infinite_one():
+    """By the logits: the second group of two, whose maxima are one fp32 step apart."""
+    x = torch.full((3, 32), -1.0, device="cuda")
+    x[:, 3], x[:, 9], x[:, 30] = 1.0, STEP, math.inf
+    x[1, 31] = math.inf
+    idx, w = M.route_tokens(x, 2, score="sigmoid", num_groups=4, top_groups=2, group_score="max")
+    assert idx.tolist() == [[30, 9], [30, 31], [30, 9]]
+    assert torch.allclose(w.sum(1), torch.ones(3, device="cuda"))
+    idx, w = M.route_tokens(x[:, :31].contiguous(), 2, score="sigmoid")
+    assert idx.tolist() == [[30, 9]] * 3
