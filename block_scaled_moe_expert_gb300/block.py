@@ -310,6 +310,8 @@ def route_tokens(logits, k, *, score="softmax", bias=None, num_groups=1, top_gro
     ("max") biased scores are largest. topk_w: the scores of the chosen, divided by
     their sum with renormalize, times scale. Ties go to the lowest index; an expert
     with a logit of -inf is never chosen, and slots left over get -1 and weight 0.
+    A NaN logit, and +inf under softmax, make the token's weights NaN (and the mean
+    scores); scores do not choose its expert.
     mean_scores=True returns also the mean over the tokens of the scores divided by
     their sum, float32 [E]: with the plan's counts, the terms of a balance loss.
     topk_w and the mean scores are differentiable with respect to the logits."""

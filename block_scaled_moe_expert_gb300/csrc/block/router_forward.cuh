@@ -151,6 +151,10 @@ __device__ __noinline__ int choose_exact(Shape s, const void* logits, int64_t t,
   const float slack = score_slack<SIGMOID>(row);
   float x[P], q[P];
   load_logits<P>(s, logits, t, sp, x);
+  if (by_score && !SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = x[i] < INFINITY ? x[i] : neg_inf();  // +inf and NaN: as in the kernel
+  }
   double total = 1;
   if (by_score && !SIGMOID) {
     double sum = 0;
@@ -359,7 +363,8 @@ __device__ __forceinline__ Two inv_total_two(const Shape& s, const void* logits,
   for (int i = 0; i < P; ++i) {
     const float x = i < sp.n ? logit_at(s, logits, t * s.ld + sp.e0 + i) : neg_inf();
     const Two y = sum_of(x, -most);
-    if (x - most >= -80.f) sum = add(sum, exp_two(y));  // less than e^-80 of the sum does not show
+    // less than e^-80 of the sum does not show; no logit of +inf or NaN counts
+    if (x - most >= -80.f && x < INFINITY) sum = add(sum, exp_two(y));
   }
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1)
@@ -510,9 +515,14 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
     const bool plain = __all_sync(kFull, look == 0.f);
     unsigned any_nan = 0;
     if (!plain) {
+      // a logit of +inf has no softmax: where scores choose it is out like a NaN one
       bool nan = false;
 #pragma unroll
-      for (int i = 0; i < P; ++i) nan |= x[i] != x[i];
+      for (int i = 0; i < P; ++i) {
+        const bool lost = x[i] != x[i] || (!SIGMOID && x[i] == INFINITY);
+        if (lost && by_score) x[i] = __int_as_float(0x7fffffff);
+        nan |= lost;
+      }
       any_nan = __ballot_sync(kFull, nan);
       if (L < 32) any_nan = (any_nan >> first) & ((1u << (L & 31)) - 1u);
     }

@@ -20,17 +20,20 @@ extern "C" {
 /* ---------------------------------------------------------- routing ------
  * Scores s[t, e]: softmax of a token's logits over the experts, or the sigmoid of
  * each. An expert is available to a token if its logit and, where one is given,
- * its bias are more than -inf and no NaN. The K best available experts, best first, ties to the lowest index, go to topk_idx [T, K]; where fewer are
- * available the last slots get -1 and weight 0. Best: by s + bias where bias
- * (f32 [E]) is given, as the scores compare before any rounding (evaluated in
- * 64 bits where fp32 does not settle it), else by the logits. With num_groups
- * > 1 the experts form groups of E / num_groups neighbours, and the choice is
- * among those of the top_groups groups of the largest value: the sum of the
- * group's two largest s + bias (MOE_GROUP_TOP2; the largest alone where one
- * expert is available) or the largest (MOE_GROUP_MAX); ties to the lowest group.
- * topk_w [T, K] = scale * s (without bias) of the chosen, divided by their sum
- * first with renormalize. A NaN among a token's logits makes its weights NaN (the
- * choice is that without the experts of such logits).
+ * its bias are more than -inf and no NaN. The K best available experts, best first,
+ * ties to the lowest index, go to topk_idx [T, K]; where fewer are available the
+ * last slots get -1 and weight 0. Best: by s + bias where bias (f32 [E]) is given, as
+ * the scores compare before any rounding (evaluated in 64 bits where fp32 does not
+ * settle it), else by the logits. With num_groups > 1 the experts form groups of
+ * E / num_groups neighbours, and the choice is among those of the top_groups groups
+ * of the largest value: the sum of the group's two largest s + bias (MOE_GROUP_TOP2;
+ * the largest alone where one expert is available) or the largest (MOE_GROUP_MAX);
+ * ties to the lowest group. topk_w [T, K] = scale * s (without bias) of the chosen,
+ * divided by their sum first with renormalize.
+ * A NaN among a token's logits makes its weights NaN (the choice is that without the
+ * experts of such logits). So does +inf under softmax, which then has no scores: where
+ * scores decide (a bias, or groups by their two best) the choice is that without its
+ * expert, where logits alone do it is the largest.
  * mean_scores f32 [E] (may be null): mean over the tokens of
  * s[t, e] / (sum over e of s[t, e]); a token without logits above -inf counts 0.
  *

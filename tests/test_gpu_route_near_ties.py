@@ -91,3 +91,31 @@ def test_neighbouring_logits_beside_an_infinite_one():
     assert torch.allclose(w.sum(1), torch.ones(3, device="cuda"))
     idx, w = M.route_tokens(x[:, :31].contiguous(), 2, score="sigmoid")
     assert idx.tolist() == [[30, 9]] * 3
+
+
+def test_infinite_logits_under_softmax():
+    """A logit of +inf has no softmax: the token's weights and the mean scores are NaN, as its scores are; where
+    scores choose, the choice is that without its expert (like a NaN's), where logits do, it is the largest."""
+    for dtype in C.DTYPES:
+        x, bias = logits_of(11, 40, 64, dtype)
+        x[3, 5] = x[6, 60] = x[9, 0] = math.inf
+        x[9, 1] = math.inf
+        x[12] = math.inf
+        bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+        bad[[3, 6, 9, 12]] = True
+        rest = torch.where(x == math.inf, -math.inf, x.float())
+        for renorm in (True, False):
+            for b, groups, top in ((bias, 1, 1), (bias, 8, 3), (bias, 4, 4), (None, 8, 3)):
+                for group_score in ("top2", "max"):
+                    if b is None and group_score == "max":
+                        continue
+                    idx, w, mean = M.route_tokens(x, 6, bias=b, num_groups=groups, top_groups=top, group_score=group_score,
+                                                  renormalize=renorm, mean_scores=True)
+                    assert torch.equal(idx.long(), O.choose(rest, 6, "softmax", b, groups, top, group_score))
+                    assert torch.equal(w.isnan().all(1), bad) and torch.equal(w.isnan().any(1), bad)
+                    assert bool(mean.isnan().all())
+                    want = O.route_weights(rest, idx.long(), "softmax", renorm, 1.0)[~bad]
+                    assert torch.allclose(w[~bad].double(), want, rtol=1e-5, atol=1e-30)
+            idx, w, mean = M.route_tokens(x, 6, renormalize=renorm, mean_scores=True)
+            assert idx[3, 0] == 5 and idx[6, 0] == 60 and idx[9, :2].tolist() == [0, 1]
+            assert torch.equal(w.isnan().all(1), bad) and torch.equal(w.isnan().any(1), bad) and bool(mean.isnan().all())
