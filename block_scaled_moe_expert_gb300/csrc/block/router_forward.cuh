@@ -331,16 +331,20 @@ __device__ __forceinline__ uint64_t packed(Two v) {
 __device__ __forceinline__ Two unpacked(uint64_t k) {
   return {unordered(static_cast<uint32_t>(k >> 32)), unordered(static_cast<uint32_t>(k))};
 }
-// Whether pairs of floats settle the order of two keys that differ (the same pair is a tie:
-// the same inputs give it, and others only where 64 bits would hardly tell them apart).
-__device__ __forceinline__ bool settled(Two a, Two b) {
-  return fabsf((a.hi - b.hi) + (a.lo - b.lo)) > 0x1p-40f * (fabsf(a.hi) + fabsf(b.hi));
+// Whether pairs of floats settle the order of two keys that differ, `err` the sum of their errors (the same
+// pair is a tie: the same inputs give it, and others only where 64 bits would hardly tell them apart).
+__device__ __forceinline__ bool settled(Two a, Two b, float err) {
+  return fabsf((a.hi - b.hi) + (a.lo - b.lo)) > err;
 }
 
-// Score plus bias; `ok` is cleared where exp_two does not reach.
+// Score plus bias and a bound on its error; `ok` is cleared where exp_two does not reach. The
+// score is off by at most 2^-42 of itself (2^-43 the exponential, the rest its quotient or product), which
+// a bias that cancels it leaves as it is; the sum adds 2^-46 of what it adds up. Four times
+// that, and 2^-120 for products whose low parts leave fp32's range.
 template <bool SIGMOID>
-__device__ __forceinline__ Two key_two(float x, float bias, float most, Two inv_total, bool* ok) {
+__device__ __forceinline__ Two key_two(float x, float bias, float most, Two inv_total, bool* ok, float* err) {
   const Two y = SIGMOID ? Two{-fabsf(x), 0.f} : sum_of(x, -most);
+  *err = 0.f;
   if (!(fabsf(y.hi) <= 80.f)) {
     *ok = false;
     return {0.f, 0.f};
@@ -353,7 +357,9 @@ __device__ __forceinline__ Two key_two(float x, float bias, float most, Two inv_
   } else {
     s = mul(z, inv_total);
   }
-  return bias == 0.f ? s : add(s, {bias, 0.f});
+  const Two k = bias == 0.f ? s : add(s, {bias, 0.f});
+  *err = fmaf(fabsf(s.hi) + fabsf(k.hi), 0x1p-40f, 0x1p-120f);
+  return k;
 }
 // 1 / sum of e^(x - most) over the token (softmax).
 template <int P, int L>
@@ -381,21 +387,23 @@ __device__ __noinline__ int order_candidates(Shape s, const void* logits, int64_
   const bool have = e >= 0;
   const float b = have && bias != nullptr ? __ldg(bias + e) : 0.f;
   bool ok = true;
+  float err = 0.f;
   uint64_t key = 0;
   if (bias == nullptr) {  // within groups: the order of the logits
     if (have) key = packed({x, 0.f});
   } else {
     Two inv = {1.f, 0.f};
     if (!SIGMOID) inv = inv_total_two<P, L>(s, logits, t, span_of(s, sub), row.most);
-    if (have) key = packed(key_two<SIGMOID>(x, b, row.most, inv, &ok));
+    if (have) key = packed(key_two<SIGMOID>(x, b, row.most, inv, &ok, &err));
   }
   int rank = 0;
   for (int j = 0; j <= s.K; ++j) {
     const uint64_t kj = __shfl_sync(kFull, key, first + j);
     const int ej = __shfl_sync(kFull, e, first + j);
+    const float both = __shfl_sync(kFull, err, first + j) + err;
     if (j != sub && have && ej >= 0) {
       rank += kj > key || (kj == key && ej < e);
-      if (bias != nullptr && kj != key && !settled(unpacked(kj), unpacked(key))) ok = false;
+      if (bias != nullptr && kj != key && !settled(unpacked(kj), unpacked(key), both)) ok = false;
     } else if (j != sub && !have && (ej >= 0 || j < sub)) {
       ++rank;
     }
@@ -414,35 +422,41 @@ __device__ __noinline__ int order_candidates(Shape s, const void* logits, int64_
 // that a group's third may not come near). L is 32. -1 where they do not settle it.
 template <int P, bool SIGMOID>
 __device__ __noinline__ int rank_groups(Shape s, const void* logits, int64_t t, const float* bias, Row row, int sub,
-                                        uint3 key, float edge, float err) {
+                                        uint3 key, float edge, float slack) {
   const Span sp = span_of(s, sub);
   Two inv = {1.f, 0.f};
   if (!SIGMOID) inv = inv_total_two<P, 32>(s, logits, t, sp, row.most);
   bool ok = true;
+  float err = 0.f;  // the largest of the group's keys
   uint64_t c[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const uint32_t k = j == 0 ? key.x : key.y;
     if (k != 0) {
       const int e = sp.e0 + P - 1 - static_cast<int>(k & (P - 1));
+      float of_key;
       c[j] = packed(key_two<SIGMOID>(logit_at(s, logits, t * s.ld + e), bias != nullptr ? __ldg(bias + e) : 0.f, row.most,
-                                     inv, &ok));
+                                     inv, &ok, &of_key));
+      err = fmaxf(err, of_key);
     }
   }
-  if (key.z != 0 && unordered(key.z & ~static_cast<uint32_t>(P - 1)) + err >= edge) ok = false;
+  if (key.z != 0 && unordered(key.z & ~static_cast<uint32_t>(P - 1)) + slack >= edge) ok = false;
   uint64_t a = max(c[0], c[1]), b = min(c[0], c[1]);
   for (int o = 1 << s.lanes_log2 >> 1; o > 0; o >>= 1) {
     const uint64_t a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
     b = max(min(a, a2), max(b, b2));
     a = max(a, a2);
+    err = fmaxf(err, __shfl_xor_sync(kFull, err, o));
   }
   const uint64_t value = s.group_max || b == 0 ? a : packed(add(unpacked(a), unpacked(b)));
+  err *= 2.f;  // of the sum of two
   const int g = sub >> s.lanes_log2;
   int rank = 0;
   for (int j = 0; j < s.G; ++j) {
     const uint64_t v = __shfl_sync(kFull, value, j << s.lanes_log2);
+    const float both = __shfl_sync(kFull, err, j << s.lanes_log2) + err;
     rank += v > value || (v == value && j < g);
-    if (g < s.G && j != g && v != 0 && value != 0 && v != value && !settled(unpacked(v), unpacked(value))) ok = false;
+    if (g < s.G && j != g && v != 0 && value != 0 && v != value && !settled(unpacked(v), unpacked(value), both)) ok = false;
   }
   return __all_sync(kFull, ok) ? (rank < s.top_groups && g < s.G) : -1;
 }

@@ -119,3 +119,43 @@ def test_infinite_logits_under_softmax():
             idx, w, mean = M.route_tokens(x, 6, renormalize=renorm, mean_scores=True)
             assert idx[3, 0] == 5 and idx[6, 0] == 60 and idx[9, :2].tolist() == [0, 1]
             assert torch.equal(w.isnan().all(1), bad) and torch.equal(w.isnan().any(1), bad) and bool(mean.isnan().all())
+
+
+def neighbours(value, low, high, count):
+    """Index pairs (i, j) of `value` [N] that are next to each other in order and between low and high apart."""
+    order = value.argsort()
+    gap = value[order][1:] - value[order][:-1]
+    at = ((gap >= low) & (gap <= high)).nonzero().flatten()
+    at = at[:: max(1, at.numel() // count)][:count]
+    assert at.numel() >= count // 2
+    return order[at], order[at + 1]
+
+
+def test_bias_that_cancels_the_score():
+    """bias = -score in fp32 leaves keys of 1e-8, whose error is that of the scores: neighbours 1e-15 to 8e-15
+    apart, 5 to 40 times the error of their 64-bit values (a sigmoid 2^-53, a sum that is exact)."""
+    x = C.randn(C.gen(30), 400000, scale=1.5)
+    s = O.scores(x[:, None], "sigmoid")[0][:, 0]
+    i, j = neighbours(s - s.float().double(), 1e-15, 8e-15, 320)
+    for a, b in ((i, j), (j, i)):
+        # 16 pairs a call, each pair's expert with the smaller or the larger key first
+        for k in range(0, i.numel() - 15, 16):
+            row = x[torch.stack([a[k:k + 16], b[k:k + 16]], 1).flatten()][None]
+            bias = -O.scores(row, "sigmoid")[0][0].float()
+            for K in (31, 32):
+                check(row, K, "sigmoid", bias, mean=False)
+            row, bias = torch.cat([row, row], 1), torch.cat([bias, bias - 0.25])
+            check(row, 31, "sigmoid", bias, mean=False)
+            check(row, 20, "sigmoid", bias, 2, 1, "max", mean=False)
+
+
+def test_softmax_bias_that_cancels_the_score():
+    """The same for scores of some 1/64 that share a sum: 1e-17 to 1e-15 apart, 64-bit values good to 1e-17 / 5."""
+    x = C.randn(C.gen(31), 60000, 64)
+    s = O.scores(x, "softmax")[0]
+    top = (s - s.float().double()).sort(1, descending=True)[0][:, :33]
+    gap = (top[:, :-1] - top[:, 1:]).amin(1)
+    rows = ((gap >= 1e-17) & (gap <= 1e-15)).nonzero().flatten()[:80]
+    assert rows.numel() == 80
+    for r in rows.tolist():
+        check(x[r:r + 1], 32, "softmax", -s[r].float(), mean=False)
