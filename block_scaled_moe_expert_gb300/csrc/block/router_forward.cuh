@@ -640,9 +640,30 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
         const float a = unordered(mine.x & ~static_cast<uint32_t>(P - 1)), b = unordered(after.x & ~static_cast<uint32_t>(P - 1));
         unsure |= a - b <= (by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f);
       }
-      if (__any_sync(kFull, unsure) && unsure) {  // the same inputs are the same key
-        const int ea = expert(after);
-        unsure = !(xe == logit_at(s, logits, tr * s.ld + ea) && (bias == nullptr || __ldg(bias + e) == __ldg(bias + ea)));
+      if (__any_sync(kFull, unsure)) {  // the same inputs are the same key
+        bool border = false;            // the K-th and the one behind it are
+        if (unsure) {
+          const int ea = expert(after);
+          unsure = !(xe == logit_at(s, logits, tr * s.ld + ea) && (bias == nullptr || __ldg(bias + e) == __ldg(bias + ea)));
+          border = !unsure && sub == s.K - 1;
+        }
+        // then others that are as near may be left in the lanes
+        unsigned who = __ballot_sync(kFull, border);
+        if (L < 32) who = (who >> first) & ((1u << (L & 31)) - 1u);
+        if (who != 0) {
+          const uint2 last = taken[s.K - 1];
+          const int el = expert(last);
+          const float xl = logit_at(s, logits, tr * s.ld + el), bl = bias != nullptr ? __ldg(bias + el) : 0.f;
+          const float a = unordered(last.x & ~static_cast<uint32_t>(P - 1));
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            if (key[i] == 0) continue;
+            const float b = unordered(key[i] & ~static_cast<uint32_t>(P - 1));
+            if (a - b > (by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f)) continue;
+            const int ei = sp.e0 + P - 1 - static_cast<int>(key[i] & (P - 1));
+            unsure |= !(xl == logit_at(s, logits, tr * s.ld + ei) && (bias == nullptr || bl == __ldg(bias + ei)));
+          }
+        }
       }
       if (__any_sync(kFull, unsure || exact)) {
         // candidates: the K + 1 that the lanes hold, if the next one is surely none

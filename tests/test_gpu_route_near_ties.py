@@ -159,3 +159,21 @@ def test_softmax_bias_that_cancels_the_score():
     assert rows.numel() == 80
     for r in rows.tolist():
         check(x[r:r + 1], 32, "softmax", -s[r].float(), mean=False)
+
+
+def test_equal_experts_do_not_hide_a_larger_one():
+    """Experts with the same logit at the border of the choice, and one a step of fp32 above them further on."""
+    for E in (32, 60, 256, 512):
+        for K in (1, 2, 5):
+            for dtype, step in ((torch.float32, STEP), (torch.float32, 1.0 + 2.0 ** -22), (torch.bfloat16, 1.0 + 2.0 ** -7)):
+                x = torch.full((6, E), -1.0, device="cuda")
+                x[:5, : E // 2 : 2] = 1.0
+                for t, at in enumerate((E - 1, E // 2, E // 2 - 1, 1)):
+                    x[t, at] = step
+                x[4, E - 7:] = step
+                x = x.to(dtype)
+                for score in ("softmax", "sigmoid"):
+                    check(x, K, score, None, mean=False)
+                    check(x, K, score, torch.zeros(E, device="cuda"), mean=False)
+                    check(x, min(K, E // 2), score, None, 2, 1, "max", mean=False)
+                    check(x, min(K, E // 2), score, torch.full((E,), 0.25, device="cuda"), 4, 2, "top2", mean=False)
