@@ -331,10 +331,21 @@ __device__ __forceinline__ uint64_t packed(Two v) {
 __device__ __forceinline__ Two unpacked(uint64_t k) {
   return {unordered(static_cast<uint32_t>(k >> 32)), unordered(static_cast<uint32_t>(k))};
 }
-// Whether pairs of floats settle the order of two keys that differ, `err` the sum of their errors (the same
-// pair is a tie: the same inputs give it, and others only where 64 bits would hardly tell them apart).
+// Whether pairs of floats settle the order of two keys, `err` the sum of their errors. The same
+// pair is a tie where the same inputs give it (`Inputs`): other inputs may leave a pair that 64
+// bits tell apart, as sigmoids next to 1 with a bias whose sum fills the low part.
 __device__ __forceinline__ bool settled(Two a, Two b, float err) {
   return fabsf((a.hi - b.hi) + (a.lo - b.lo)) > err;
+}
+struct Inputs {
+  float x, b;  // logit and bias, zeros without a sign
+  __device__ __forceinline__ bool operator==(Inputs o) const { return x == o.x && b == o.b; }
+};
+__device__ __forceinline__ Inputs shfl_xor(Inputs v, int o) {
+  return {__shfl_xor_sync(kFull, v.x, o), __shfl_xor_sync(kFull, v.b, o)};
+}
+__device__ __forceinline__ Inputs shfl_from(Inputs v, int lane) {
+  return {__shfl_sync(kFull, v.x, lane), __shfl_sync(kFull, v.b, lane)};
 }
 
 // Score plus bias and a bound on its error; `ok` is cleared where exp_two does not reach. The
@@ -401,9 +412,10 @@ __device__ __noinline__ int order_candidates(Shape s, const void* logits, int64_
     const uint64_t kj = __shfl_sync(kFull, key, first + j);
     const int ej = __shfl_sync(kFull, e, first + j);
     const float both = __shfl_sync(kFull, err, first + j) + err;
+    const Inputs from = shfl_from({x, b}, first + j);
     if (j != sub && have && ej >= 0) {
       rank += kj > key || (kj == key && ej < e);
-      if (bias != nullptr && kj != key && !settled(unpacked(kj), unpacked(key), both)) ok = false;
+      if (bias != nullptr && !(from == Inputs{x, b}) && !settled(unpacked(kj), unpacked(key), both)) ok = false;
     } else if (j != sub && !have && (ej >= 0 || j < sub)) {
       ++rank;
     }
@@ -429,34 +441,60 @@ __device__ __noinline__ int rank_groups(Shape s, const void* logits, int64_t t, 
   bool ok = true;
   float err = 0.f;  // the largest of the group's keys
   uint64_t c[2] = {0, 0};
+  Inputs in[2] = {};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const uint32_t k = j == 0 ? key.x : key.y;
     if (k != 0) {
       const int e = sp.e0 + P - 1 - static_cast<int>(k & (P - 1));
       float of_key;
-      c[j] = packed(key_two<SIGMOID>(logit_at(s, logits, t * s.ld + e), bias != nullptr ? __ldg(bias + e) : 0.f, row.most,
-                                     inv, &ok, &of_key));
+      in[j] = {logit_at(s, logits, t * s.ld + e), bias != nullptr ? __ldg(bias + e) : 0.f};
+      c[j] = packed(key_two<SIGMOID>(in[j].x, in[j].b, row.most, inv, &ok, &of_key));
       err = fmaxf(err, of_key);
     }
   }
   if (key.z != 0 && unordered(key.z & ~static_cast<uint32_t>(P - 1)) + slack >= edge) ok = false;
-  uint64_t a = max(c[0], c[1]), b = min(c[0], c[1]);
+  const bool first = c[0] >= c[1];
+  uint64_t a = first ? c[0] : c[1], b = first ? c[1] : c[0];  // the group's two best, and where they are from
+  Inputs from_a = in[first ? 0 : 1], from_b = in[first ? 1 : 0];
   for (int o = 1 << s.lanes_log2 >> 1; o > 0; o >>= 1) {
     const uint64_t a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
-    b = max(min(a, a2), max(b, b2));
-    a = max(a, a2);
+    const Inputs from_a2 = shfl_xor(from_a, o), from_b2 = shfl_xor(from_b, o);
+    if (b2 > b) {
+      b = b2;
+      from_b = from_b2;
+    }
+    if (min(a, a2) > b) {
+      b = min(a, a2);
+      from_b = a2 > a ? from_a : from_a2;
+    }
+    if (a2 > a) {
+      a = a2;
+      from_a = from_a2;
+    }
     err = fmaxf(err, __shfl_xor_sync(kFull, err, o));
   }
-  const uint64_t value = s.group_max || b == 0 ? a : packed(add(unpacked(a), unpacked(b)));
+  // a value that others may tie with is that of these two surely
+  const uint64_t last = s.group_max ? a : b;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const bool is = in[j] == from_a || (!s.group_max && in[j] == from_b);
+    if (c[j] != 0 && !is && !settled(unpacked(last), unpacked(c[j]), 2.f * err)) ok = false;
+  }
+  const bool sum = !s.group_max && b != 0;
+  if (!sum) from_b = {0.f, neg_inf()};
+  const uint64_t value = sum ? packed(add(unpacked(a), unpacked(b))) : a;
   err *= 2.f;  // of the sum of two
   const int g = sub >> s.lanes_log2;
   int rank = 0;
   for (int j = 0; j < s.G; ++j) {
-    const uint64_t v = __shfl_sync(kFull, value, j << s.lanes_log2);
-    const float both = __shfl_sync(kFull, err, j << s.lanes_log2) + err;
+    const int lane = j << s.lanes_log2;
+    const uint64_t v = __shfl_sync(kFull, value, lane);
+    const float both = __shfl_sync(kFull, err, lane) + err;
+    const Inputs its_a = shfl_from(from_a, lane), its_b = shfl_from(from_b, lane);
+    const bool same = its_a == from_a && its_b == from_b;
     rank += v > value || (v == value && j < g);
-    if (g < s.G && j != g && v != 0 && value != 0 && v != value && !settled(unpacked(v), unpacked(value), both)) ok = false;
+    if (g < s.G && j != g && v != 0 && value != 0 && !same && !settled(unpacked(v), unpacked(value), both)) ok = false;
   }
   return __all_sync(kFull, ok) ? (rank < s.top_groups && g < s.G) : -1;
 }

@@ -177,3 +177,45 @@ def test_equal_experts_do_not_hide_a_larger_one():
                     check(x, K, score, torch.zeros(E, device="cuda"), mean=False)
                     check(x, min(K, E // 2), score, None, 2, 1, "max", mean=False)
                     check(x, min(K, E // 2), score, torch.full((E,), 0.25, device="cuda"), 4, 2, "top2", mean=False)
+
+
+def test_group_sums_that_cancel():
+    """Groups whose two best biased scores cancel to 1e-8: sums 3e-15 to 2e-14 apart, 64-bit ones good to 5e-16."""
+    x = C.randn(C.gen(32), 200000, 2, scale=1.5)
+    s = O.scores(x, "sigmoid")[0]
+    low = -(0.5 + s.sum(1)).float()
+    i, j = neighbours(s.sum(1) + 0.5 + low.double(), 3e-15, 2e-14, 200)
+    bias = torch.stack([torch.full_like(low, 0.5), low], 1)
+    for a, b in ((i, j), (j, i)):
+        rows, biases = torch.cat([x[a], x[b]], 1), torch.cat([bias[a], bias[b]], 1)
+        for r in range(rows.shape[0]):
+            check(rows[r:r + 1], 1, "sigmoid", biases[r], 2, 1, "top2", mean=False)
+
+
+def test_softmax_group_sums_that_cancel():
+    """The same for 32 groups of two whose scores share a sum, with the border between two near ones."""
+    x = C.randn(C.gen(33), 400000, 64)
+    s = O.scores(x, "softmax")[0].view(-1, 32, 2)
+    low = -(0.5 + s.sum(2)).float()
+    value, order = (s.sum(2) + 0.5 + low.double()).sort(1, descending=True)
+    gap = (value[:, :-1] - value[:, 1:])[:, :16]
+    rows, at = ((gap >= 2e-15) & (gap <= 2e-14)).nonzero(as_tuple=True)
+    assert rows.numel() >= 20
+    for r, p in list(zip(rows.tolist(), at.tolist()))[:80]:
+        bias = torch.stack([torch.full_like(low[r], 0.5), low[r]], 1).flatten()
+        check(x[r:r + 1], 2 * (p + 1), "softmax", bias, 32, p + 1, "top2", mean=False)
+
+
+def test_saturated_scores_with_a_bias():
+    """Sigmoids next to 1 whose biased keys share a pair of floats while 64 bits tell them apart: steps of
+    5 and more units of 2^-52. The larger logits have the larger indices."""
+    steps = torch.tensor([32.0, 33.0, 34.0], device="cuda")
+    for b in (0.1, 0.7, -0.3, 0.9):
+        bias = torch.full((24,), b, device="cuda")
+        x = steps.repeat_interleave(8)[None] + 0.0
+        for K in (4, 12, 23):
+            check(x, K, "sigmoid", bias, mean=False)
+            check(x.flip(1), K, "sigmoid", bias, mean=False)
+        check(x, 4, "sigmoid", bias, 3, 1, "max", mean=False)
+        check(x, 4, "sigmoid", bias, 3, 1, "top2", mean=False)
+        check(x, 4, "sigmoid", bias, 6, 3, "top2", mean=False)
