@@ -93,13 +93,18 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[P]) {
 }
 
 // fp32 scores plus bias of a lane's experts, NaN or -inf where one is not available.
-// Errors of an fp32 score: sigmoid: below 3e-7 (its slope times the exponential's
-// 2^-22 and its argument's |x| 2^-23, the sum's and the quotient's roundings);
-// softmax: those of the exponential and of the sum, in all below 1.2e-6 of the
-// largest score. `score_slack` is above both.
-template <bool SIGMOID>
+// Errors of an fp32 score, in units u = 2^-24. ex2.approx is good to 4 u of its value, its argument x log2(e)
+// adds 1.5 |x| u, the subtraction of the largest logit |x| u; rcp.approx is good to 2 u.
+// Sigmoid: 4 u and 1.5 |x| u times s (1 - s), u of 1 + e^-x, 2 u of the quotient: below 4.4 u.
+// Softmax, of the largest score 1 / sum: 4 u and 2.5 |x| u times e^-|x| (at most 0.92 u), the expert's
+// own; and what all of a token's scores have in common: 2 u of the quotient, the same of the terms
+// of the sum (4 u and 2.5 u times at most 3.9, the mean |x| of 511 terms beside one of 1 weighted by
+// them), P - 1 + log2(L) <= P + 4 roundings of the sum. That part moves the difference of two keys by
+// no more than itself, so half of it goes to each: 4.92 + (P + 19.75) / 2 u, and 1 u for what is
+// of second order.
+template <int P, bool SIGMOID>
 __device__ __forceinline__ float score_slack(Row row) {
-  return SIGMOID ? 4e-7f : 1.5e-6f * rcp_fast(row.sum);
+  return SIGMOID ? 5.f * 0x1p-24f : (16.f + 0.5f * P) * 0x1p-24f * rcp_fast(row.sum);
 }
 template <int P>
 __device__ __forceinline__ void add_bias(const float* bias, Span sp, bool vec, float (&q)[P]) {
@@ -148,7 +153,7 @@ __device__ __noinline__ int choose_exact(Shape s, const void* logits, int64_t t,
   const int first = (threadIdx.x & 31) - sub;
   const Span sp = span_of(s, sub);
   const bool by_score = bias != nullptr || (s.G > 1 && !s.group_max);
-  const float slack = score_slack<SIGMOID>(row);
+  const float slack = score_slack<P, SIGMOID>(row);
   float x[P], q[P];
   load_logits<P>(s, logits, t, sp, x);
   if (by_score && !SIGMOID) {
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
       for (int i = 0; i < P; ++i) key[i] = x[i] > neg_inf() && v[i] > neg_inf() ? key[i] : 0u;
     }
     sort_keys<P>(key);
-    const float slack = by_score ? score_slack<SIGMOID>(row) : 0.f;
+    const float slack = by_score ? score_slack<P, SIGMOID>(row) : 0.f;
     bool unsure = false, exact = false;  // settled by pairs of floats; by 64 bits
     if (s.G > 1) {
       const int lpg = 1 << s.lanes_log2;

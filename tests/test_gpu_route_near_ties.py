@@ -219,3 +219,21 @@ def test_saturated_scores_with_a_bias():
         check(x, 4, "sigmoid", bias, 3, 1, "max", mean=False)
         check(x, 4, "sigmoid", bias, 3, 1, "top2", mean=False)
         check(x, 4, "sigmoid", bias, 6, 3, "top2", mean=False)
+
+
+@pytest.mark.parametrize("E,groups,top_groups", [(510, 17, 4), (512, 16, 5), (512, 1, 1), (256, 8, 3), (60, 1, 1)])
+def test_sums_whose_terms_all_round_down(E, groups, top_groups):
+    """Softmax sums of one term of 1 a lane and terms just below the half of its last place, which fp32 drops: scores
+    come out too large by a step for every term. Biases put small scores next to large ones, from half of that to
+    twice it away."""
+    size = E // groups
+    x = torch.full((400, E), math.log(0.99 * 2.0 ** -24), device="cuda")
+    x[:, :: size if groups > 1 else 8] = 0.0
+    s = O.scores(x[:1], "softmax")[0][0]
+    small = s < 0.5 * s.max()
+    shift = torch.linspace(-4, 4, E, device="cuda", dtype=torch.float64)[torch.randperm(E, generator=C.gen(34), device="cuda")]
+    bias = torch.where(small, s.max() - s, 0.0) + s.max() * E * 2.0 ** -24 * shift
+    bias = torch.where(torch.arange(E, device="cuda") % size < 5, bias, bias - 0.1).float()
+    noise = torch.where(x == 0, 0.0, C.randn(C.gen(35), 400, E, scale=1e-3))
+    for group_score in ("top2", "max"):
+        check(x - noise.abs(), 8, "softmax", bias, groups, top_groups, group_score, mean=False)
