@@ -434,6 +434,32 @@ __device__ __noinline__ int order_candidates(Shape s, const void* logits, int64_
   return __all_sync(kFull, ok) ? out : -2;
 }
 
+// Whether the lane has an expert that is not taken, next to the K-th (taken[K - 1]) by its
+// fp32 key and of other inputs. All lanes' groups that are not `in` are out.
+template <int P, bool SIGMOID>
+__device__ __noinline__ bool near_the_last(Shape s, const void* logits, int64_t t, const float* bias, Row row, Span sp,
+                                           const uint2* taken, bool in) {
+  auto expert = [&](uint2 v) { return v.x != 0 ? static_cast<int>(v.y) - static_cast<int>(v.x & (P - 1)) : -1; };
+  const bool by_score = bias != nullptr || (s.G > 1 && !s.group_max);
+  const float slack = by_score ? score_slack<P, SIGMOID>(row) : 0.f, inv = rcp_fast(row.sum);
+  const uint2 last = taken[s.K - 1];
+  const int el = expert(last);
+  const Inputs from = {logit_at(s, logits, t * s.ld + el), bias != nullptr ? __ldg(bias + el) : 0.f};
+  const float a = unordered(last.x & ~static_cast<uint32_t>(P - 1));
+  bool near = false;
+  for (int i = 0; i < (in ? sp.n : 0); ++i) {
+    const Inputs its = {logit_at(s, logits, t * s.ld + sp.e0 + i), bias != nullptr ? __ldg(bias + sp.e0 + i) : 0.f};
+    if (its == from || !(its.x > neg_inf()) || !(its.b > neg_inf())) continue;
+    float v = its.x;
+    if (by_score) v = (SIGMOID ? sigmoid_fast(its.x) : exp_fast(its.x - row.most) * inv) + its.b;
+    if (a - v > (by_score ? 2.f * slack + P * 0x1p-22f * (fabsf(a) + fabsf(v)) : 0.f)) continue;
+    bool has = false;
+    for (int k = 0; k <= s.K; ++k) has |= expert(taken[k]) == sp.e0 + i;
+    near |= !has;
+  }
+  return near;
+}
+
 // Whether this lane's group is among the best, from the two best keys of each lane in
 // pairs of floats (key: the lane's three best fp32 keys; edge: the fp32 value
 // that a group's third may not come near). L is 32. -1 where they do not settle it.
@@ -539,17 +565,17 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
   }
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kTokens;
+  const int step = gridDim.x * kTokens;  // T is at most 2^26
   float ahead[MEAN ? P : 1];  // blocks that take many tokens: the next one's logits are on their way
   if constexpr (MEAN) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / L;
+    const int t = blockIdx.x * kTokens + threadIdx.x / L;
     load_logits<P>(s, logits, t < s.T ? t : s.T - 1, sp, ahead);
   }
   // every lane walks the same number of tokens: the shuffles take whole warps
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < s.T; t0 += step) {
-    const int64_t t = t0 + threadIdx.x / L;
+  for (int t0 = blockIdx.x * kTokens; t0 < s.T; t0 += step) {
+    const int t = t0 + threadIdx.x / L;
     const bool valid = t < s.T;
-    const int64_t tr = valid ? t : s.T - 1;
+    const int tr = valid ? t : s.T - 1;
     float x[P], q[P];  // logits; scores (softmax: times their sum)
     if constexpr (MEAN) {
 #pragma unroll
@@ -621,6 +647,7 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
     sort_keys<P>(key);
     const float slack = by_score ? score_slack<P, SIGMOID>(row) : 0.f;
     bool unsure = false, exact = false;  // settled by pairs of floats; by 64 bits
+    bool in = true;                      // the lane's group is among the best
     if (s.G > 1) {
       const int lpg = 1 << s.lanes_log2;
       uint32_t a = key[0], b = key[P > 1 ? 1 : 0];
@@ -639,7 +666,7 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
         const float v = __shfl_sync(kFull, value, j * lpg);
         rank += v > value || (v == value && j < g);
       }
-      bool in = rank < s.top_groups && g < s.G;
+      in = rank < s.top_groups && g < s.G;
       if (check && s.top_groups < s.G) {
         // of a value; an infinite one is itself, and a group without an expert is near no other
         const float err = fabsf(value) < INFINITY ? 2.f * slack + kCut * (fabsf(va) + fabsf(vb)) : 0.f;
@@ -693,20 +720,7 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
         // then others that are as near may be left in the lanes
         unsigned who = __ballot_sync(kFull, border);
         if (L < 32) who = (who >> first) & ((1u << (L & 31)) - 1u);
-        if (who != 0) {
-          const uint2 last = taken[s.K - 1];
-          const int el = expert(last);
-          const float xl = logit_at(s, logits, tr * s.ld + el), bl = bias != nullptr ? __ldg(bias + el) : 0.f;
-          const float a = unordered(last.x & ~static_cast<uint32_t>(P - 1));
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            if (key[i] == 0) continue;
-            const float b = unordered(key[i] & ~static_cast<uint32_t>(P - 1));
-            if (a - b > (by_score ? 2.f * slack + kCut * (fabsf(a) + fabsf(b)) : 0.f)) continue;
-            const int ei = sp.e0 + P - 1 - static_cast<int>(key[i] & (P - 1));
-            unsure |= !(xl == logit_at(s, logits, tr * s.ld + ei) && (bias == nullptr || bl == __ldg(bias + ei)));
-          }
-        }
+        if (who != 0) unsure |= near_the_last<P, SIGMOID>(s, logits, tr, bias, row, span_of(s, sub), taken, in);
       }
       if (__any_sync(kFull, unsure || exact)) {
         // candidates: the K + 1 that the lanes hold, if the next one is surely none
