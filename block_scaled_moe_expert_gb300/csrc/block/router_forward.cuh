@@ -558,7 +558,14 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
   __shared__ uint2 slots[kTokens][L + 1];  // keys in the order they are taken, and where their lane starts
   uint2* taken = slots[threadIdx.x / L];
   const unsigned below = ((1u << lane) - 1u) & ~((1u << first) - 1u);  // lower lanes of the token
+  // Mean scores: a lane adds up kMeanRun tokens, then its sums so far and what their additions lost
+  // (float2, in shared memory: few blocks walk as many), so that the roundings do not grow with T.
+  constexpr int kMeanRun = 16;
+  constexpr int kColsBytes = kRouteThreads / 32 * kMaxExperts * 4, kSumsBytes = P * kRouteThreads * 8;
+  __shared__ __align__(16) uint8_t mean_smem[MEAN ? (kColsBytes > kSumsBytes ? kColsBytes : kSumsBytes) : 16];
+  float2(*sums)[kRouteThreads] = reinterpret_cast<float2(*)[kRouteThreads]>(mean_smem);  // [P][threads]
   float acc[MEAN ? P : 1];
+  int walked = 0;
   if constexpr (MEAN) {
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[i] = 0.f;
@@ -797,16 +804,33 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
       const float f = sum != 0.f ? rcp_fast(sum) : 0.f;
 #pragma unroll
       for (int i = 0; i < P; ++i) acc[i] += valid ? q[i] * f : 0.f;
+      if (++walked % kMeanRun == 0) {  // every thread of the block at once
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float2 so_far = walked > kMeanRun ? sums[i][threadIdx.x] : make_float2(0.f, 0.f);
+          const Two v = sum_of(so_far.x, acc[i]);
+          sums[i][threadIdx.x] = make_float2(v.hi, so_far.y + v.lo);
+          acc[i] = 0.f;
+        }
+      }
     }
   }
   if constexpr (MEAN) {
+    if (walked >= kMeanRun) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 so_far = sums[i][threadIdx.x];
+        acc[i] = (acc[i] + so_far.y) + so_far.x;
+      }
+      __syncthreads();  // the columns take their place
+    }
     // lanes that hold the same experts, then the block's warps, in a fixed order
 #pragma unroll
     for (int i = 0; i < P; ++i) {
 #pragma unroll
       for (int o = 16; o >= L; o >>= 1) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
     }
-    __shared__ float cols[kRouteThreads / 32][kMaxExperts];
+    float(*cols)[kMaxExperts] = reinterpret_cast<float(*)[kMaxExperts]>(mean_smem);  // [warps][experts]
     if (lane < L) {
 #pragma unroll
       for (int i = 0; i < P; ++i)

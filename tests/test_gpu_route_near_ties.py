@@ -237,3 +237,18 @@ def test_sums_whose_terms_all_round_down(E, groups, top_groups):
     noise = torch.where(x == 0, 0.0, C.randn(C.gen(35), 400, E, scale=1e-3))
     for group_score in ("top2", "max"):
         check(x - noise.abs(), 8, "softmax", bias, groups, top_groups, group_score, mean=False)
+
+
+def test_mean_scores_of_many_tokens():
+    """The error of a mean does not grow with the number of tokens: 64 roundings of 2^-24 for thousands of tokens a
+    lane, beside those of a score, the same in every row: 4 + 3 D of an exponential (2^-22 and its argument's), as much
+    again and 21 of the sum over the experts, 3 of the quotient (a sigmoid's own 8 are fewer). Rows share their memory,
+    so that there may be many."""
+    for E, T, values in ((256, 1 << 22, (0.0, 0.3, -0.2)), (512, 1 << 21, (0.1, -0.05, 0.2)), (8, 1 << 25, (0.0, 0.7, -0.4))):
+        row = torch.tensor(values, device="cuda").repeat(E // 3 + 1)[:E]
+        for score in ("softmax", "sigmoid"):
+            mean = M.route_tokens(row.expand(T, E), 1, score=score, mean_scores=True)[2].double()
+            p = O.scores(row[None], score)[1][0]
+            D = float(row.max() - row.min())
+            tol = (2 * (4 + 3 * D) + 24 + 64) * 2.0 ** -24
+            assert bool(((mean - p).abs() <= tol * p).all()), float(((mean - p).abs() / p).max() / tol)
