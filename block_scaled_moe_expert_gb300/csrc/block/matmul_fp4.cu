@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) matmul_fp4_kernel(const __grid_
 // of S CTAs (a rule on the number of tiles, launch below); each leaves its partial
 // sums in its shared memory, and after a cluster barrier the CTAs add up the partials
 // of their share of the tokens in rank order over distributed shared memory:
-// no atomics, the same bits every time. Two CTAs per SM, all stages of weights
-// in flight before the quantizing kernel in front has finished. Bound by the
+// no atomics, the same bits every time. Two CTAs per SM, all stages of weights in flight
+// at once, before the quantizing kernel in front has finished where there is one. Bound by the
 // weights' bytes: 28671 x 4096 (62 MB) in 13.5 us with one token, 13.8 with 16, 15.8 with 64 and
 // 19.3 with 128; small ones by a chain of latencies: 4096 x 7168 with one token 6.2 us, 2880 x 2880
 // 4.4 (a call among others, quantization included).
@@ -463,10 +463,20 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
       bulk_load(sm.sfb[st], a.a_sf + (static_cast<size_t>(tt) * a.KB + 2 * ks) * 512, nch * 512, &sm.full[st]);
     };
     const int pre = min(kStages, n);
-    for (int i = 0; i < pre; ++i)
-      if (elect_one()) weights(i, i);
+    // The first weights are on their way while the quantization ends: that kernel waited for whatever
+    // wrote them. With its own quantization the call's kernel in front may be the one that writes them,
+    // whose stores are only promised to be seen behind the wait. (Loads in front of it: 4 tokens
+    // 4096 x 7168 5.96 us a call, behind it 6.04; in a graph 5.9 and 6.3, 8 tokens 7168 x 2048 4.4 and 4.2.)
+    if (!OWN) {
+      for (int i = 0; i < pre; ++i)
+        if (elect_one()) weights(i, i);
+    }
     pdl_wait();
     pdl_launch_dependents();
+    if (OWN) {
+      for (int i = 0; i < pre; ++i)
+        if (elect_one()) weights(i, i);
+    }
     // a wait takes a second to give up, so no CTA can have set a flag by now
     if (OWN && tid == 0 && blockIdx.x == 0) *a.status = 0;
     for (int i = 0; i < pre; ++i)

@@ -97,12 +97,10 @@ size_t moe_matmul_fp4_workspace_bytes(int T_max, int K);
  * x bf16 or fp16 [T, K] (row stride ld_x) -> y of the same type [T, N], or
  * [T, N / 2] with swiglu. The workspace (256-byte aligned) starts with the status
  * word that moe_get_device_status reads (MOE_DEV_TIMEOUT: y is invalid) and must
- * not be used by another call until this one has finished on `stream`. Above 8 tokens
- * it is two launches, the quantization and the product; up to 128 tokens the product starts
- * reading `prepared` while the kernel in front of the call on the stream ends: a kernel
- * of the caller's that writes prepared weights itself must not launch its dependents
- * early (cudaTriggerProgrammaticLaunchCompletion). A token's row has the same bits in
- * any batch of up to 128 tokens that is on the same side of 8, and in any larger batch.
+ * not be used by another call until this one has finished on `stream`; a call without
+ * tokens touches nothing. Above 8 tokens it is two launches, the quantization and the
+ * product. A token's row has the same bits in any batch of up to 128 tokens that is on
+ * the same side of 8, and in any larger batch.
  */
 moe_status moe_matmul_fp4(int N, int K, int swiglu, float swiglu_limit, const void* prepared, int dtype, const void* x,
                           int64_t ld_x, int T, void* workspace, size_t workspace_bytes, void* y, void* stream);
