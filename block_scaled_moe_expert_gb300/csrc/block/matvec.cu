@@ -347,8 +347,7 @@ __device__ __forceinline__ void matvec_cta(const MvArgs a, uint8_t* s_dyn, float
 #pragma unroll
   for (int d = 0; d < DEPTH - 1; ++d) fetch();
   // The weights are on their way before the kernel in front has finished: they
-  // were laid out before it (the layout kernel lets nothing start before its
-  // end). x and y are touched after it.
+  // were laid out before it (layout_ended_kernel). x and y are touched after it.
   if (!WIDE) {
     pdl_wait();
     pdl_launch_dependents();
@@ -530,7 +529,6 @@ __global__ void __launch_bounds__(256)
 matvec_prepare_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scale,
                       const uint8_t* __restrict__ zero, uint8_t* __restrict__ out, int N, int K, int group,
                       bool swiglu, int steps) {
-  // no early launch of dependents: moe_matvec fetches the weights without waiting
   const int tile = blockIdx.x, step = blockIdx.y;
   const int bytes = block_bytes(FMT, group), per_row = (K + group - 1) / group;
   uint8_t* dst = out + (static_cast<size_t>(tile) * steps + step) * bytes;
@@ -579,6 +577,11 @@ matvec_prepare_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
     }
   }
 }
+
+// Behind the layout: moe_matvec fetches weights before it waits for the kernel in front, and what
+// that kernel stored is only promised to be seen behind the wait. An ordinary launch begins when all
+// in front of it has ended and is seen, and moe_matvec not before this kernel.
+__global__ void layout_ended_kernel() {}
 
 int row_tiles(const MatvecShape& s) { return s.swiglu ? ceil_div(s.N / 2, 8) : ceil_div(s.N, kMvRows); }
 
@@ -660,9 +663,11 @@ cudaError_t launch_matvec_prepare(const MatvecShape& s, const void* codes, const
                                   const void* zero, void* prepared, cudaStream_t st) {
   const int steps = ceil_div(s.K, kMvStep), tiles = row_tiles(s);
   auto* k = s.fmt == MOE_Q_FP4 ? matvec_prepare_kernel<MOE_Q_FP4> : matvec_prepare_kernel<MOE_Q_INT4>;
-  return launch_kernel(false, k, dim3(tiles, steps), 256, 0, st, static_cast<const uint8_t*>(codes),
-                       static_cast<const uint8_t*>(scale), static_cast<const uint8_t*>(zero),
-                       static_cast<uint8_t*>(prepared), s.N, s.K, s.group, s.swiglu != 0, steps);
+  const cudaError_t e =
+      launch_kernel(false, k, dim3(tiles, steps), 256, 0, st, static_cast<const uint8_t*>(codes),
+                    static_cast<const uint8_t*>(scale), static_cast<const uint8_t*>(zero),
+                    static_cast<uint8_t*>(prepared), s.N, s.K, s.group, s.swiglu != 0, steps);
+  return e != cudaSuccess ? e : launch_kernel(false, layout_ended_kernel, 1, 32, 0, st);
 }
 
 cudaError_t launch_matvec(const MatvecShape& s, float limit, int scale_dtype, const void* prepared, int dtype,

@@ -192,9 +192,11 @@ moe_status moe_matvec_prepare(int qfmt, int N, int K, int group, int swiglu, con
 /* x bf16 or fp16 [T, K] (row stride ld_x) -> y of the same type [T, N], or
  * [T, N / 2] with swiglu. Meant for few tokens: the weights are read once per
  * 16 tokens (fewer where x would not fit into shared memory). The kernel starts
- * reading `prepared` while the kernel in front of it on the stream ends: a
- * kernel of the caller's that writes prepared weights itself must not launch
- * its dependents early (cudaTriggerProgrammaticLaunchCompletion). */
+ * reading `prepared` while the kernel in front of it on the stream ends. That is
+ * safe behind moe_matvec_prepare and any copy; a kernel of the caller's that writes
+ * prepared weights itself must not be the last operation in front of the call (an
+ * event, a memset or a kernel launched without programmatic serialization in
+ * between is enough). */
 moe_status moe_matvec(int qfmt, int N, int K, int group, int swiglu, float swiglu_limit, int scale_dtype,
                       const void* prepared, int dtype, const void* x, int64_t ld_x, int T, void* y, void* stream);
 
