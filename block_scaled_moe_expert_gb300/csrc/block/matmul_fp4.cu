@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
+  int issued = 0;  // stages that warp 0 has copies for
 
   if (warp == 0) {
     auto weights = [&](int i, int st) {
@@ -483,10 +484,9 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
       if (elect_one()) tokens(i, i);
     int stage = pre == kStages ? 0 : pre;
     uint32_t phase = pre == kStages ? 1 : 0;
-    int64_t issued = pre;
-    bool ok = true;
+    issued = pre;
     for (int i = pre; i < n; ++i) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[stage], phase ^ 1, abort_flag)))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.empty[stage], phase ^ 1, abort_flag))) break;
       if (elect_one()) {
         weights(i, stage);
         tokens(i, stage);
@@ -498,7 +498,6 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
         phase ^= 1;
       }
     }
-    if (!ok && lane == 0) drain_copies(sm.full, kStages, issued);
   } else if (warp == 1) {
     pdl_wait();  // the bounded waits begin when the kernel in front has ended
     const uint64_t a0 = smem_desc(smem_u32(sm.a[0]), 16, 1024, kSwizzle128B);
@@ -562,6 +561,8 @@ __global__ void __launch_bounds__(kStThreads) matmul_fp4_stream_kernel(const __g
   __syncwarp();
   if (S > 1) cluster_barrier();
   else __syncthreads();
+  // (warp 0 may have issued its last copies before another warp gave up on them)
+  if (tid == 0 && *abort_flag) drain_copies(sm.full, kStages, issued);
   if (warp >= 2 && !(S == 1 && !a.swiglu)) {
     const int count = min(N, a.T - tt * N), thread = (warp - 2) * 32 + lane, tile = rt * (a.swiglu ? 64 : kMmM);
     T* y = static_cast<T*>(a.y) + static_cast<int64_t>(tt) * N * a.N;
