@@ -547,10 +547,7 @@ std::tuple<Tensor, Tensor> quantize_fp4(const Tensor& x) {
   c10::SmallVector<int64_t, 6> cs(sizes.begin(), sizes.end()), ss(cs);
   cs.back() = C / 2;
   ss.back() = C / 32;
-  // one allocation: the codes, then the scales
-  const int64_t scale_at = round_up(f.n * (C / 2), 256);
-  const Tensor all = make_empty({scale_at + f.n * (C / 32)}, at::kByte);
-  const Tensor codes = part_of(all, 0, cs, at::kByte), scale = part_of(all, scale_at, ss, at::kByte);
+  const Tensor codes = make_empty(cs, at::kByte), scale = make_empty(ss, at::kByte);
   check(api.moe_quantize_fp4(f.code, f.ptr(), f.ld, static_cast<int>(f.n), static_cast<int>(C), codes.data_ptr(),
                              scale.data_ptr(), stream(f.dev)),
         "moe_quantize_fp4");
