@@ -314,7 +314,8 @@ def route_tokens(logits, k, *, score="softmax", bias=None, num_groups=1, top_gro
     scores); scores do not choose its expert.
     mean_scores=True returns also the mean over the tokens of the scores divided by
     their sum, float32 [E]: with the plan's counts, the terms of a balance loss.
-    topk_w and the mean scores are differentiable with respect to the logits."""
+    topk_w and the mean scores are differentiable with respect to the logits.
+    The results are parts of one storage: keeping or saving one keeps the others' bytes."""
     if _tracked(logits):
         return _Route.apply(logits, k, score, bias, num_groups, top_groups, group_score, renormalize, float(scale),
                             mean_scores)
@@ -372,8 +373,10 @@ def matmul_fp4(x, prepared, swiglu_limit=None, workspace=None, out=None):
     weights: [T, N] ([T, N/2] with SwiGLU) of x's type, on the FP4 tensor cores.
     matvec takes the same weights with the activations as they are, for few tokens.
     workspace: uint8, at least prepared.workspace_bytes(T), 256-byte aligned
-    (allocated if None); device_status(workspace) reads its flags. It has no
-    gradient: an x that requires one is refused while gradients are recorded."""
+    (allocated if None). device_status(workspace) reads its flags, which say whether
+    a wait in the kernel gave up and y is invalid; a call that allocates its own
+    leaves no way to read them, and its y may share its storage. It has no gradient:
+    an x that requires one is refused while gradients are recorded."""
     return _calls.matmul_fp4(x, prepared._weights, swiglu_limit, workspace, out)
 
 

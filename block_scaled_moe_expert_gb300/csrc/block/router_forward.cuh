@@ -10,18 +10,20 @@
 // The choice is that of the exact scores. Without a bias the order is that of the
 // logits. With a bias, or where groups are ranked by sums of scores, neighbours of the
 // result that are nearer than the keys' error and do not come from the same inputs
-// are settled by pairs of floats (about 2^-43), in the lanes that hold them; what
-// pairs leave open, or needs experts that no lane holds yet, by 64 bits. Of 200,000 tokens
-// with 256 sigmoid scores of normal logits and a bias one in 270 took the first way (for its
-// groups one in 3000), none the second.
+// are settled by pairs of floats (about 2^-43 of the scores), in the lanes that hold them; what
+// pairs leave open, or needs experts that no lane holds yet, by 64 bits. Of a million tokens
+// with 256 sigmoid scores of normal logits and a bias one in 410 took the first way (with 8
+// groups one in 510, and one in 4500 for the groups), none the second.
 //
-// Bounds: the logits are read once, 2 or 4 bytes for some 10 instructions a logit and 20 a
-// choice, most of them comparisons, selections and whole-number ones: instruction issue for
-// large batches (issue slots 68% busy, memory at a fifth of its rate), the launch for small
-// ones. 65536 x 256 fp32: one expert by sigmoid 33 us, eight with a bias 48, in groups 60
-// (67 MB: 10 us at the memory's rate); 8192 x 256 in groups 10; 16384 x 128 bf16 with mean
-// scores 10.6; 4 tokens 3.2. Registers for 7 blocks per SM: with 6, 7, 8 and 10 blocks the 8192
-// tokens took 11.3, 10.0, 11.4 and 12.4 us.
+// Bounds: the logits are read once, 2 or 4 bytes for what a lane does to sort its 8 and to pass
+// through the rounds (369 instructions a token of 256 logits and one choice), most of it comparisons,
+// selections and whole numbers: instruction issue for large batches (issue slots 58% busy, memory at
+// a fifth of its rate), the launch for small ones. A call among others, 65536 x 256 fp32: one expert by
+// sigmoid 36.3 us, eight with a bias 50.7, in groups 61.6 (67 MB: 10 us at the memory's rate);
+// 8192 x 256 in groups 10.5; 16384 x 128 bf16 with mean scores 11.1 (their second launch included);
+// 4 tokens 5.4, the kernel 3.2. Registers for 7 blocks per SM, chosen with 8 logits a lane: with 6, 7, 8 and 10
+// blocks 8192 x 256 in groups took 11.3, 10.0, 11.4 and 12.4 us. 16 logits a lane spill 400 to 500 bytes
+// (8192 x 384 24.6 us, 8192 x 512 in 16 groups 32.2), 32 a lane some 1600 (8192 x 510 in 17 groups 109).
 #pragma once
 #include <cfloat>
 
