@@ -464,10 +464,11 @@ __device__ __noinline__ bool near_the_last(Shape s, const void* logits, int64_t 
 
 // Whether this lane's group is among the best, from the two best keys of each lane in
 // pairs of floats (key: the lane's three best fp32 keys; edge: the fp32 value
-// that a group's third may not come near). L is 32. -1 where they do not settle it.
+// that a group's third may not come near). Only the groups `near` the border by their fp32 values
+// take part; the others are `in` or not. L is 32. -1 where the pairs do not settle it.
 template <int P, bool SIGMOID>
 __device__ __noinline__ int rank_groups(Shape s, const void* logits, int64_t t, const float* bias, Row row, int sub,
-                                        uint3 key, float edge, float slack) {
+                                        uint3 key, float edge, float slack, bool near, bool in_now) {
   const Span sp = span_of(s, sub);
   Two inv = {1.f, 0.f};
   if (!SIGMOID) inv = inv_total_two<P, 32>(s, logits, t, sp, row.most);
@@ -507,29 +508,37 @@ __device__ __noinline__ int rank_groups(Shape s, const void* logits, int64_t t, 
     }
     err = fmaxf(err, __shfl_xor_sync(kFull, err, o));
   }
-  // a value that others may tie with is that of these two surely
+  // whether the value is that of these two surely, which a tie needs
   const uint64_t last = s.group_max ? a : b;
+  bool sure = true;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const bool is = in[j] == from_a || (!s.group_max && in[j] == from_b);
-    if (c[j] != 0 && !is && !settled(unpacked(last), unpacked(c[j]), 2.f * err)) ok = false;
+    if (c[j] != 0 && !is && !settled(unpacked(last), unpacked(c[j]), 2.f * err)) sure = false;
   }
   const bool sum = !s.group_max && b != 0;
   if (!sum) from_b = {0.f, neg_inf()};
-  const uint64_t value = sum ? packed(add(unpacked(a), unpacked(b))) : a;
+  const uint64_t value = !near ? 0 : sum ? packed(add(unpacked(a), unpacked(b))) : a;
   err *= 2.f;  // of the sum of two
   const int g = sub >> s.lanes_log2;
+  const bool first_of_group = (sub & ((1 << s.lanes_log2) - 1)) == 0;
+  const int open = s.top_groups - __popc(__ballot_sync(kFull, first_of_group && in_now && !near));
   int rank = 0;
+  for (int j = 0; j < s.G; ++j) {
+    const uint64_t v = __shfl_sync(kFull, value, j << s.lanes_log2);
+    rank += v > value || (v == value && j < g);
+  }
+  const bool mine = near ? rank < open : in_now;
+  // a group of the near ones that is in against each that is not
   for (int j = 0; j < s.G; ++j) {
     const int lane = j << s.lanes_log2;
     const uint64_t v = __shfl_sync(kFull, value, lane);
     const float both = __shfl_sync(kFull, err, lane) + err;
     const Inputs its_a = shfl_from(from_a, lane), its_b = shfl_from(from_b, lane);
-    const bool same = its_a == from_a && its_b == from_b;
-    rank += v > value || (v == value && j < g);
-    if (g < s.G && j != g && v != 0 && value != 0 && !same && !settled(unpacked(v), unpacked(value), both)) ok = false;
+    const bool its = __shfl_sync(kFull, mine, lane), same = its_a == from_a && its_b == from_b;
+    if (v != 0 && its != mine && (same ? !sure : !settled(unpacked(v), unpacked(value), both))) ok = false;
   }
-  return __all_sync(kFull, ok) ? (rank < s.top_groups && g < s.G) : -1;
+  return __all_sync(kFull, ok || !near) ? mine : -1;
 }
 
 // Over the first `width` lanes of a token (a power of two), valid in these.
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
       in = rank < s.top_groups && g < s.G;
       if (check && s.top_groups < s.G) {
         // of a value; an infinite one is itself, and a group without an expert is near no other
-        const float err = fabsf(value) < INFINITY ? 2.f * slack + kCut * (fabsf(va) + fabsf(vb)) : 0.f;
+        const float err = fabsf(value) < INFINITY ? 2.f * slack + (kCut * fabsf(va) + kCut * fabsf(vb)) : 0.f;
         const bool some = a != 0;
         const float worst = -unordered(lane_max_u32<L>(ordered(in && some ? err - value : neg_inf())));
         const float best = unordered(lane_max_u32<L>(ordered(!in && some && g < s.G ? value + err : neg_inf())));
@@ -686,7 +695,8 @@ __global__ void __launch_bounds__(kRouteThreads, MEAN ? 4 : 7)
           int settled_in = -1;
           if (by_score)
             settled_in = rank_groups<P, SIGMOID>(s, logits, tr, bias, row, sub, make_uint3(key[0], key[1], P > 2 ? key[P > 2 ? 2 : 0] : 0u),
-                                                 (s.group_max ? va : b == 0 ? neg_inf() : vb) - err, err);
+                                                 (s.group_max ? va : b == 0 ? neg_inf() : vb) - err, err,
+                                                 some && g < s.G && (in ? value - err <= best : value + err >= worst), in);
           exact = settled_in < 0;
           if (!exact) in = settled_in != 0;
         }
