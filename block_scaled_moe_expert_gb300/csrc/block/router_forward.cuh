@@ -448,15 +448,24 @@ __device__ __noinline__ bool near_the_last(Shape s, const void* logits, int64_t 
   const int el = expert(last);
   const Inputs from = {logit_at(s, logits, t * s.ld + el), bias != nullptr ? __ldg(bias + el) : 0.f};
   const float a = unordered(last.x & ~static_cast<uint32_t>(P - 1));
+  float x[P], b[P];
+  load_logits<P>(s, logits, t, sp, x);
+  if (bias != nullptr) load_as<P, float>(bias, sp.e0, sp.n, s.vec_bias, b);
+  unsigned other = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    if (bias == nullptr) b[i] = 0.f;
+    other |= static_cast<unsigned>(in && x[i] > neg_inf() && b[i] > neg_inf() && !(Inputs{x[i], b[i]} == from)) << i;
+  }
   bool near = false;
-  for (int i = 0; i < (in ? sp.n : 0); ++i) {
-    const Inputs its = {logit_at(s, logits, t * s.ld + sp.e0 + i), bias != nullptr ? __ldg(bias + sp.e0 + i) : 0.f};
-    if (its == from || !(its.x > neg_inf()) || !(its.b > neg_inf())) continue;
-    float v = its.x;
-    if (by_score) v = (SIGMOID ? sigmoid_fast(its.x) : exp_fast(its.x - row.most) * inv) + its.b;
+  for (; other != 0; other &= other - 1) {
+    const int e = sp.e0 + __ffs(other) - 1;
+    const float be = bias != nullptr ? __ldg(bias + e) : 0.f;
+    float v = logit_at(s, logits, t * s.ld + e);
+    if (by_score) v = (SIGMOID ? sigmoid_fast(v) : exp_fast(v - row.most) * inv) + be;
     if (a - v > (by_score ? 2.f * slack + P * 0x1p-22f * (fabsf(a) + fabsf(v)) : 0.f)) continue;
     bool has = false;
-    for (int k = 0; k <= s.K; ++k) has |= expert(taken[k]) == sp.e0 + i;
+    for (int k = 0; k <= s.K; ++k) has |= expert(taken[k]) == e;
     near |= !has;
   }
   return near;
