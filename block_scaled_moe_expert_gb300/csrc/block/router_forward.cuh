@@ -23,7 +23,7 @@
 // 8192 x 256 in groups 10.5; 16384 x 128 bf16 with mean scores 11.1 (their second launch included);
 // 4 tokens 5.4, the kernel 3.2. Registers for 7 blocks per SM, chosen with 8 logits a lane: with 6, 7, 8 and 10
 // blocks 8192 x 256 in groups took 11.3, 10.0, 11.4 and 12.4 us. 16 logits a lane spill 400 to 500 bytes
-// (8192 x 384 24.6 us, 8192 x 512 in 16 groups 32.2), 32 a lane some 1600 (8192 x 510 in 17 groups 109).
+// (8192 x 384 24.6 us, 8192 x 512 in 16 groups 32.2), 32 a lane some 1600 (8192 x 510 in 17 groups 110).
 #pragma once
 #include <cfloat>
 
